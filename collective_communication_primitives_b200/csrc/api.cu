@@ -1702,6 +1702,443 @@ static coll_status_t coll_moe_combine_impl(sim_comm_t c, const void* const* y, s
 
 }  // extern "C"
 
+// ---- router, products with sharded weights, log probabilities ---------------------------------------
+
+namespace {
+
+// Buffers of one call, for the overlap check: outputs against each other and against every input, by
+// sorting the outputs (n log n: at 64 ranks a call has hundreds of buffers). No allocation.
+struct Spans {
+    struct Span { uintptr_t lo, hi; };
+    static constexpr int kCap = 9 * kMaxRanks;
+    Span in[kCap], out[kCap];
+    int n_in = 0, n_out = 0;
+    static void put(Span* list, int* n, const void* p, size_t bytes) {
+        if (p && bytes && *n < kCap) list[(*n)++] = {uintptr_t(p), uintptr_t(p) + bytes};
+    }
+    void add_in(const void* p, size_t bytes) { put(in, &n_in, p, bytes); }
+    void add_out(const void* p, size_t bytes) { put(out, &n_out, p, bytes); }
+    // The last output that starts before s ends, if it overlaps s (after check() has sorted them).
+    const Span* hit(const Span& s) const {
+        const Span* o = std::lower_bound(out, out + n_out, s.hi, [](const Span& x, uintptr_t v) { return x.lo < v; });
+        return o != out && (o - 1)->hi > s.lo ? o - 1 : nullptr;
+    }
+    coll_status_t check() {
+        std::sort(out, out + n_out, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+        for (int i = 1; i < n_out; ++i)
+            if (out[i].lo < out[i - 1].hi) return fail(COLL_ERR_INVALID_ARG, "two output buffers overlap");
+        for (int i = 0; i < n_in; ++i)
+            if (hit(in[i])) return fail(COLL_ERR_INVALID_ARG, "an output overlaps an input");
+        return COLL_OK;
+    }
+};
+
+coll_status_t check_device(sim_comm* c) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev != c->device)
+        return fail(COLL_ERR_INVALID_ARG, "the current device is not the one the communicator was created on");
+    return COLL_OK;
+}
+
+// A float dtype, or the refusal.
+coll_status_t check_float(coll_dtype_t dt, const char* what) {
+    if (!valid_dtype(dt)) return fail(COLL_ERR_INVALID_ARG, "unknown dtype");
+    if (dt == COLL_INT32) return fail(COLL_ERR_UNSUPPORTED, std::string(what) + " must be fp32 or bf16");
+    return COLL_OK;
+}
+
+// Checks one rank's buffer and enters it in the list of the call's buffers.
+coll_status_t take_in(Spans& sp, const void* p, size_t bytes, size_t align, const char* what) {
+    coll_status_t st = check_ptr(p, bytes, align, what);
+    if (st == COLL_OK) sp.add_in(p, bytes);
+    return st;
+}
+coll_status_t take_out(Spans& sp, const void* p, size_t bytes, size_t align, const char* what) {
+    coll_status_t st = check_ptr(p, bytes, align, what);
+    if (st == COLL_OK) sp.add_out(p, bytes);
+    return st;
+}
+
+// The call's ranks: all of them, or the one of a rank view.
+int first_rank(const sim_comm* c) { return c->rank >= 0 ? c->rank : 0; }
+int ranks_of(const sim_comm* c) { return c->rank >= 0 ? 1 : c->p; }
+
+coll_status_t route_common(sim_comm* c, const void* const* logits, size_t tokens, int k, int experts, coll_dtype_t dt) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "router scores")) != COLL_OK) return st;
+    if ((st = check_moe_shape(c, tokens, k, size_t(1), experts)) != COLL_OK) return st;
+    if (k > experts) return fail(COLL_ERR_INVALID_ARG, "k exceeds the number of experts");
+    if (!logits) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    return COLL_OK;
+}
+
+void route_shape(sim_comm* c, RouteArgs& a, size_t tokens, int k, int experts, int normalise) {
+    a.rank0 = first_rank(c);
+    a.k = k;
+    a.E = experts;
+    a.normalise = normalise != 0;
+    a.T = tokens;
+    a.tokens = tokens * size_t(ranks_of(c));
+    a.ctl = make_ctl(c);
+}
+
+// log2 of a scale group that the 4-bit kernels take and that divides `len`, or the refusal.
+coll_status_t check_group(int group, size_t len, const char* what, int* shift) {
+    if (group < 32 || (group & (group - 1)) != 0) return fail(COLL_ERR_INVALID_ARG, "group must be a power of two, 32 or more");
+    if (len == 0 || len % size_t(group) != 0)
+        return fail(COLL_ERR_INVALID_ARG, std::string("group must divide ") + what);
+    *shift = 0;
+    while ((1 << *shift) < group) ++*shift;
+    return COLL_OK;
+}
+
+// Longest row of a product: chunk numbers and element offsets inside a row stay within 32 bits for the
+// concatenated rows of 64 ranks.
+constexpr size_t kMaxRow = size_t(1) << 24;
+
+coll_status_t check_row(size_t len, const char* what) {
+    if (len == 0) return fail(COLL_ERR_INVALID_ARG, std::string(what) + " must be positive");
+    if (len > kMaxRow) return fail(COLL_ERR_INVALID_ARG, std::string(what) + " exceeds 2^24");
+    return COLL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+static coll_status_t coll_moe_route_impl(sim_comm_t c, const void* const* logits, size_t tokens, int k, int experts,
+                                         coll_dtype_t dt, int normalise, int32_t* const* topk_idx,
+                                         float* const* topk_weight, coll_stream_t stream) {
+    coll_status_t st = route_common(c, logits, tokens, k, experts, dt);
+    if (st != COLL_OK) return st;
+    if (!topk_idx || !topk_weight) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (tokens == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), row = size_t(experts) * d, A = tokens * size_t(k);
+    RouteArgs a{};
+    Spans sp;
+    bool vec = experts % 8 == 0;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_in(sp, logits[r], tokens * row, d, "score")) != COLL_OK) return st;
+        if ((st = take_out(sp, topk_idx[r], A * 4, 4, "expert id")) != COLL_OK) return st;
+        if ((st = take_out(sp, topk_weight[r], A * 4, 4, "gate weight")) != COLL_OK) return st;
+        vec = vec && aligned16(logits[r]);
+        a.logits[r] = logits[r];
+        a.idx_out[r] = topk_idx[r];
+        a.weight[r] = topk_weight[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    route_shape(c, a, tokens, k, experts, normalise);
+    a.vec = vec ? 1 : 0;
+    cudaError_t e = launch_route(a, int(dt), false, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "router launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_moe_route_backward_impl(sim_comm_t c, const void* const* logits, const int32_t* const* topk_idx,
+                                                  const float* const* grad_weight, size_t tokens, int k, int experts,
+                                                  coll_dtype_t dt, int normalise, void* const* grad_logits,
+                                                  coll_stream_t stream) {
+    coll_status_t st = route_common(c, logits, tokens, k, experts, dt);
+    if (st != COLL_OK) return st;
+    if (!topk_idx || !grad_weight || !grad_logits) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (tokens == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), row = size_t(experts) * d, A = tokens * size_t(k);
+    RouteArgs a{};
+    Spans sp;
+    bool vec = experts % 8 == 0;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_in(sp, logits[r], tokens * row, d, "score")) != COLL_OK) return st;
+        if ((st = take_in(sp, topk_idx[r], A * 4, 4, "expert id")) != COLL_OK) return st;
+        if ((st = take_in(sp, grad_weight[r], A * 4, 4, "gate weight gradient")) != COLL_OK) return st;
+        if ((st = take_out(sp, grad_logits[r], tokens * row, d, "score gradient")) != COLL_OK) return st;
+        vec = vec && aligned16(logits[r]) && aligned16(grad_logits[r]);
+        a.logits[r] = logits[r];
+        a.idx_in[r] = topk_idx[r];
+        a.grad_weight[r] = grad_weight[r];
+        a.grad_logits[r] = grad_logits[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    route_shape(c, a, tokens, k, experts, normalise);
+    a.vec = vec ? 1 : 0;
+    cudaError_t e = launch_route(a, int(dt), true, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "router gradient launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_linear_w4_impl(sim_comm_t c, const void* const* x, const void* const* w, const void* const* scale,
+                                         size_t tokens, size_t n, size_t k, int group, coll_parallel_t parallel,
+                                         coll_dtype_t dt, void* const* out, coll_stream_t stream) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "the product's output")) != COLL_OK) return st;
+    if (parallel != COLL_PARALLEL_COLUMN && parallel != COLL_PARALLEL_ROW)
+        return fail(COLL_ERR_INVALID_ARG, "unknown parallel form");
+    if ((st = check_row(k, "k")) != COLL_OK) return st;
+    const bool row = parallel == COLL_PARALLEL_ROW;
+    const size_t p = size_t(c->p);
+    if ((row ? k : n) % p != 0) return fail(COLL_ERR_INVALID_ARG, row ? "k must be divisible by p" : "n must be divisible by p");
+    const size_t N = row ? n : n / p, K = row ? k / p : k;
+    int shift = 0;
+    if ((st = check_group(group, K, row ? "k / p" : "k", &shift)) != COLL_OK) return st;
+    if ((st = check_rows(N, K, "n")) != COLL_OK) return st;
+    if ((st = check_rows(tokens, std::max(N, K), "tokens")) != COLL_OK) return st;
+    if (!x || !w || !scale || !out) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (tokens == 0 || N == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt);
+    LinearArgs a{};
+    Spans sp;
+    bool vec = true;
+    for (int r = 0; r < c->p; ++r) {
+        const bool own = c->rank < 0 || r == c->rank;
+        if (own) {
+            if ((st = take_out(sp, out[r], tokens * N * d, d, "out")) != COLL_OK) return st;
+            a.out[r] = out[r];
+        } else if (!row) continue;  // a column-parallel view takes its own shard only
+        if ((st = take_in(sp, x[r], tokens * K * 2, 2, "token")) != COLL_OK) return st;
+        if ((st = take_in(sp, w[r], N * K / 2, 16, "weight")) != COLL_OK) return st;
+        if ((st = take_in(sp, scale[r], N * (K >> shift) * 2, 2, "scale")) != COLL_OK) return st;
+        vec = vec && aligned16(x[r]);
+        a.x[r] = static_cast<const uint16_t*>(x[r]);
+        a.w[r] = static_cast<const char*>(w[r]);
+        a.scale[r] = static_cast<const uint16_t*>(scale[r]);
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.p = c->p;
+    a.row = row ? 1 : 0;
+    a.view_rank = c->rank;
+    a.T = tokens;
+    a.N = N;
+    a.K = K;
+    a.group_shift = shift;
+    a.out_bf16 = dt == COLL_BF16;
+    a.x_vec = vec ? 1 : 0;
+    a.ctl = make_ctl(c);
+    cudaError_t e = launch_linear(a, c->num_sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_moe_layer_impl(sim_comm_t c, const void* const* x, const int32_t* const* topk_idx,
+                                         const float* const* topk_weight, const void* const* residual, size_t tokens,
+                                         int k, size_t hidden, size_t ffn, int experts, coll_weight_t weight, int group,
+                                         const void* const* w_up, const void* const* up_scale, const void* const* w_down,
+                                         const void* const* down_scale, coll_dtype_t dt, void* const* out,
+                                         coll_stream_t stream) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if (!valid_dtype(dt)) return fail(COLL_ERR_INVALID_ARG, "unknown dtype");
+    if (dt != COLL_BF16) return fail(COLL_ERR_UNSUPPORTED, "the expert layer takes bf16 rows");
+    if (weight != COLL_WEIGHT_BF16 && weight != COLL_WEIGHT_INT4) return fail(COLL_ERR_INVALID_ARG, "unknown weight type");
+    if ((st = check_moe_shape(c, tokens, k, hidden, experts)) != COLL_OK) return st;
+    if ((st = check_row(hidden, "hidden")) != COLL_OK || (st = check_row(ffn, "ffn")) != COLL_OK) return st;
+    const bool q4 = weight == COLL_WEIGHT_INT4;
+    int shift = 0;
+    if (q4 && ((st = check_group(group, hidden, "hidden", &shift)) != COLL_OK ||
+               (st = check_group(group, ffn, "ffn", &shift)) != COLL_OK))
+        return st;
+    const size_t ranks = size_t(ranks_of(c)), e_loc = size_t(experts / c->p), A = ranks * tokens * size_t(k);
+    if (A > size_t(kLayerMaxAssignments))
+        return fail(COLL_ERR_UNSUPPORTED, "the expert layer takes at most 4096 assignments (ranks * tokens * k): use "
+                                          "coll_moe_dispatch and coll_moe_combine for larger batches");
+    if (!x || !topk_idx || !topk_weight || !w_up || !w_down || !out || (q4 && (!up_scale || !down_scale)))
+        return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (tokens == 0) return COLL_OK;
+    const size_t bytes = tokens * hidden * 2, per_rank = tokens * size_t(k);
+    const size_t elems = e_loc * 2 * ffn * hidden;  // of w_up; w_down holds half as many
+    MoeLayerArgs a{};
+    Spans sp;
+    bool vec = q4 || (hidden % 8 == 0 && ffn % 8 == 0);
+    for (int r = 0; r < c->p; ++r) {
+        const size_t wb = q4 ? elems / 2 : elems * 2, wa = q4 ? 16 : 2;
+        if ((st = take_in(sp, w_up[r], wb, wa, "up weight")) != COLL_OK) return st;
+        if ((st = take_in(sp, w_down[r], wb / 2, wa, "down weight")) != COLL_OK) return st;
+        if (!q4) vec = vec && aligned16(w_up[r]) && aligned16(w_down[r]);
+        a.up[r] = static_cast<const char*>(w_up[r]);
+        a.down[r] = static_cast<const char*>(w_down[r]);
+        if (q4) {
+            if ((st = take_in(sp, up_scale[r], (elems >> shift) * 2, 2, "up scale")) != COLL_OK) return st;
+            if ((st = take_in(sp, down_scale[r], elems >> shift, 2, "down scale")) != COLL_OK) return st;
+            a.up_scale[r] = static_cast<const uint16_t*>(up_scale[r]);
+            a.down_scale[r] = static_cast<const uint16_t*>(down_scale[r]);
+        }
+        if (c->rank >= 0 && r != c->rank) continue;
+        if ((st = take_in(sp, x[r], bytes, 2, "token")) != COLL_OK) return st;
+        if ((st = take_in(sp, topk_idx[r], per_rank * 4, 4, "expert id")) != COLL_OK) return st;
+        if ((st = take_in(sp, topk_weight[r], per_rank * 4, 4, "gate weight")) != COLL_OK) return st;
+        if ((st = take_out(sp, out[r], bytes, 2, "out")) != COLL_OK) return st;
+        vec = vec && aligned16(x[r]);
+        a.x[r] = static_cast<const uint16_t*>(x[r]);
+        a.idx[r] = topk_idx[r];
+        a.weight[r] = topk_weight[r];
+        a.out[r] = static_cast<uint16_t*>(out[r]);
+        if (residual) {
+            if ((st = check_ptr(residual[r], bytes, 2, "residual")) != COLL_OK) return st;
+            a.res[r] = static_cast<const uint16_t*>(residual[r]);
+        }
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    // a residual may be its own rank's output (each element is read before it is written, by the same
+    // thread), and must not overlap any other
+    for (int r = first_rank(c), n = ranks_of(c); residual && n > 0; ++r, --n) {
+        const Spans::Span* o = sp.hit({uintptr_t(residual[r]), uintptr_t(residual[r]) + bytes});
+        if (o && residual[r] != out[r])
+            return fail(COLL_ERR_INVALID_ARG, "a residual overlaps an output other than its own rank's");
+    }
+    a.rank0 = first_rank(c);
+    a.k = k;
+    a.E = experts;
+    a.E_loc = int(e_loc);
+    a.H = int(hidden);
+    a.F = int(ffn);
+    a.A = int(A);
+    a.has_res = residual ? 1 : 0;
+    a.weight_kind = int(weight);
+    a.group_shift = shift;
+    a.vec = vec ? 1 : 0;
+    a.T = tokens;
+    a.h_stride = round_up(ffn, 8);
+    const size_t b_h = align_up(A * a.h_stride * 2, 256);
+    if ((st = ensure_moe(c, b_h + A * hidden * 4)) != COLL_OK) return st;
+    a.h = reinterpret_cast<uint16_t*>(c->moe);
+    a.y = reinterpret_cast<float*>(c->moe + b_h);
+    a.timeout_ns = uint64_t(c->timeout_ns);
+    a.st = c->dstate;
+    a.ctl = make_ctl(c);
+    cudaError_t e = launch_moe_layer(a, c->num_sms, static_cast<cudaStream_t>(stream));
+    if (e == cudaErrorNotSupported) return fail(COLL_ERR_UNSUPPORTED, "the expert layer needs cooperative launches");
+    if (e != cudaSuccess) return cuda_fail(e, "expert layer launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+// Checks the forward and backward calls share; fills the shape. Shards' scores go into the span list.
+static coll_status_t logprobs_common(sim_comm* c, const void* const* logits, size_t ld, const int32_t* tokens, size_t rows,
+                                     size_t vocab, coll_dtype_t dt, LogprobArgs& a, Spans& sp) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "scores")) != COLL_OK) return st;
+    if (vocab < 1 || vocab > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "vocab must be in [1, 2^31)");
+    const size_t m = (vocab + size_t(c->p) - 1) / size_t(c->p);
+    if (ld < m) return fail(COLL_ERR_INVALID_ARG, "ld is less than the shard's columns, ceil(vocab / p)");
+    if ((st = check_count(rows, "rows")) != COLL_OK || (st = check_count(ld, "ld")) != COLL_OK) return st;
+    if ((st = check_rows(rows, ld, "rows")) != COLL_OK) return st;
+    if (!logits) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if ((st = take_in(sp, tokens, rows * 4, 4, "token")) != COLL_OK) return st;
+    const size_t d = dtype_bytes(dt), bytes = rows ? ((rows - 1) * ld + m) * d : 0;
+    for (int r = 0; r < c->p; ++r) {
+        if ((st = take_in(sp, logits[r], bytes, d, "score")) != COLL_OK) return st;
+        a.logits[r] = logits[r];
+    }
+    a.tokens = tokens;
+    a.p = c->p;
+    a.view_rank = c->rank;
+    a.rows = rows;
+    a.V = vocab;
+    a.m = m;
+    a.ld = ld;
+    a.st = c->dstate;
+    a.ctl = make_ctl(c);
+    return COLL_OK;
+}
+
+static coll_status_t coll_logprobs_impl(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* tokens,
+                                        size_t rows, size_t vocab, coll_dtype_t dt, float* const* logprob,
+                                        float* const* entropy, float* const* lse, int top_n, int32_t* const* top_idx,
+                                        float* const* top_logprob, coll_stream_t stream) {
+    LogprobArgs a{};
+    Spans sp;
+    coll_status_t st = logprobs_common(c, logits, ld, tokens, rows, vocab, dt, a, sp);
+    if (st != COLL_OK) return st;
+    if (top_n < 0 || top_n > kLogprobMaxTop || size_t(top_n) > vocab)
+        return fail(COLL_ERR_INVALID_ARG, "top_n must be in [0, 32] and at most vocab");
+    if (!logprob || (top_n > 0 && (!top_idx || !top_logprob))) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (rows == 0) return COLL_OK;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_out(sp, logprob[r], rows * 4, 4, "logprob")) != COLL_OK) return st;
+        a.logprob[r] = logprob[r];
+        if (entropy) {
+            if ((st = take_out(sp, entropy[r], rows * 4, 4, "entropy")) != COLL_OK) return st;
+            a.entropy[r] = entropy[r];
+        }
+        if (lse) {
+            if ((st = take_out(sp, lse[r], rows * 4, 4, "lse")) != COLL_OK) return st;
+            a.lse[r] = lse[r];
+        }
+        if (top_n > 0) {
+            if ((st = take_out(sp, top_idx[r], rows * top_n * 4, 4, "alternative")) != COLL_OK) return st;
+            if ((st = take_out(sp, top_logprob[r], rows * top_n * 4, 4, "alternative")) != COLL_OK) return st;
+            a.top_idx[r] = top_idx[r];
+            a.top_logprob[r] = top_logprob[r];
+        }
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.n_top = top_n;
+    // Few rows: several CTAs per row, about four per SM in all, none with less than 4096 columns.
+    a.parts = 1;
+    if (rows < size_t(c->num_sms) * 2 && rows <= size_t(kLogprobMaxSplitRows)) {
+        const size_t want = (size_t(c->num_sms) * 4 + rows - 1) / rows, most = std::max<size_t>(1, vocab / 4096);
+        a.parts = int(std::min({want, most, size_t(kLogprobMaxParts)}));
+    }
+    if (a.parts > 1) {
+        const size_t b_stat = align_up(rows * a.parts * sizeof(float4), 256);
+        if ((st = ensure_moe(c, b_stat + rows * a.parts * size_t(top_n) * 8)) != COLL_OK) return st;
+        a.part_stat = reinterpret_cast<float4*>(c->moe);
+        a.part_keys = reinterpret_cast<unsigned long long*>(c->moe + b_stat);
+    }
+    cudaError_t e = launch_logprobs(a, int(dt), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "log probabilities launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_logprobs_backward_impl(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* tokens,
+                                                 size_t rows, size_t vocab, coll_dtype_t dt, const float* const* lse,
+                                                 const float* const* entropy, const float* grad_logprob,
+                                                 const float* grad_entropy, void* const* grad_logits, size_t ld_grad,
+                                                 coll_stream_t stream) {
+    LogprobArgs a{};
+    Spans sp;
+    coll_status_t st = logprobs_common(c, logits, ld, tokens, rows, vocab, dt, a, sp);
+    if (st != COLL_OK) return st;
+    if (!lse || !grad_logits || (grad_entropy && !entropy)) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (ld_grad < a.m) return fail(COLL_ERR_INVALID_ARG, "ld_grad is less than the shard's columns, ceil(vocab / p)");
+    if ((st = check_count(ld_grad, "ld_grad")) != COLL_OK || (st = check_rows(rows, ld_grad, "rows")) != COLL_OK) return st;
+    if (rows == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt);
+    if ((st = take_in(sp, grad_logprob, rows * 4, 4, "logprob gradient")) != COLL_OK) return st;
+    if (grad_entropy && (st = take_in(sp, grad_entropy, rows * 4, 4, "entropy gradient")) != COLL_OK) return st;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_in(sp, lse[r], rows * 4, 4, "lse")) != COLL_OK) return st;
+        a.lse_in[r] = lse[r];
+        if (grad_entropy) {
+            if ((st = take_in(sp, entropy[r], rows * 4, 4, "entropy")) != COLL_OK) return st;
+            a.entropy_in[r] = entropy[r];
+        }
+        if ((st = take_out(sp, grad_logits[r], ((rows - 1) * ld_grad + a.m) * d, d, "score gradient")) != COLL_OK) return st;
+        a.grad_logits[r] = grad_logits[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.grad_logprob = grad_logprob;
+    a.grad_entropy = grad_entropy;
+    a.ld_grad = ld_grad;
+    cudaError_t e = launch_logprobs_grad(a, int(dt), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "log probabilities gradient launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+}  // extern "C"
+
 // =================================================================================================
 // Ring AllReduce without any allocation.
 //
@@ -1944,6 +2381,56 @@ coll_status_t coll_moe_combine(sim_comm_t c, const void* const* y, size_t y_rows
     TraceScope ts(c, "moe_combine", tokens, int(dt), -1, -1, -1, stream);
     return ts.done(coll_moe_combine_impl(c, y, y_rows, topk_idx, route_pos, topk_weight, residual, tokens, k, hidden,
                                          experts, dt, out, stream));
+}
+
+coll_status_t coll_moe_route(sim_comm_t c, const void* const* logits, size_t tokens, int k, int experts,
+                             coll_dtype_t dt, int normalise, int32_t* const* topk_idx, float* const* topk_weight,
+                             coll_stream_t stream) {
+    TraceScope ts(c, "moe_route", tokens, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_moe_route_impl(c, logits, tokens, k, experts, dt, normalise, topk_idx, topk_weight, stream));
+}
+
+coll_status_t coll_moe_route_backward(sim_comm_t c, const void* const* logits, const int32_t* const* topk_idx,
+                                      const float* const* grad_weight, size_t tokens, int k, int experts,
+                                      coll_dtype_t dt, int normalise, void* const* grad_logits, coll_stream_t stream) {
+    TraceScope ts(c, "moe_route_backward", tokens, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_moe_route_backward_impl(c, logits, topk_idx, grad_weight, tokens, k, experts, dt, normalise,
+                                                grad_logits, stream));
+}
+
+coll_status_t coll_linear_w4(sim_comm_t c, const void* const* x, const void* const* w, const void* const* scale,
+                             size_t tokens, size_t n, size_t k, int group, coll_parallel_t parallel, coll_dtype_t dt,
+                             void* const* out, coll_stream_t stream) {
+    TraceScope ts(c, "linear_w4", tokens, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_linear_w4_impl(c, x, w, scale, tokens, n, k, group, parallel, dt, out, stream));
+}
+
+coll_status_t coll_moe_layer(sim_comm_t c, const void* const* x, const int32_t* const* topk_idx,
+                             const float* const* topk_weight, const void* const* residual, size_t tokens, int k,
+                             size_t hidden, size_t ffn, int experts, coll_weight_t weight, int group,
+                             const void* const* w_up, const void* const* up_scale, const void* const* w_down,
+                             const void* const* down_scale, coll_dtype_t dt, void* const* out, coll_stream_t stream) {
+    TraceScope ts(c, "moe_layer", tokens, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_moe_layer_impl(c, x, topk_idx, topk_weight, residual, tokens, k, hidden, ffn, experts, weight,
+                                       group, w_up, up_scale, w_down, down_scale, dt, out, stream));
+}
+
+coll_status_t coll_logprobs(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* tokens, size_t rows,
+                            size_t vocab, coll_dtype_t dt, float* const* logprob, float* const* entropy,
+                            float* const* lse, int top_n, int32_t* const* top_idx, float* const* top_logprob,
+                            coll_stream_t stream) {
+    TraceScope ts(c, "logprobs", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_logprobs_impl(c, logits, ld, tokens, rows, vocab, dt, logprob, entropy, lse, top_n, top_idx,
+                                      top_logprob, stream));
+}
+
+coll_status_t coll_logprobs_backward(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* tokens,
+                                     size_t rows, size_t vocab, coll_dtype_t dt, const float* const* lse,
+                                     const float* const* entropy, const float* grad_logprob, const float* grad_entropy,
+                                     void* const* grad_logits, size_t ld_grad, coll_stream_t stream) {
+    TraceScope ts(c, "logprobs_backward", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_logprobs_backward_impl(c, logits, ld, tokens, rows, vocab, dt, lse, entropy, grad_logprob,
+                                               grad_entropy, grad_logits, ld_grad, stream));
 }
 
 }  // extern "C"

@@ -23,6 +23,9 @@ struct DevState {
     unsigned long long moe_task;     // fused MoE dispatch: next token row to claim (zero between calls)
     unsigned long long comb_task;    // MoE combine: next token to claim (zero between calls)
     uint32_t comb_done;              // MoE combine: CTAs that left the token loop (the last one resets both)
+    uint32_t layer_ctr;              // expert layer: grid-barrier arrivals (zero between calls)
+    uint32_t layer_done;             // expert layer: CTAs that left (the last one resets both)
+    uint32_t row_ctr[1024];          // log probabilities: parts of a row that are done (zero between calls)
 };
 
 // What a kernel needs to report errors and notice an abort.
@@ -231,6 +234,100 @@ struct MoeArgs {
     Ctl ctl;
 };
 
+// ---- router ----------------------------------------------------------------------------------------
+
+struct RouteArgs {
+    const void* logits[kMaxRanks];       // [T][E]
+    int32_t* idx_out[kMaxRanks];         // forward: [T][k]
+    float* weight[kMaxRanks];            // forward: [T][k]
+    const int32_t* idx_in[kMaxRanks];    // gradient: [T][k]
+    const float* grad_weight[kMaxRanks]; // gradient: [T][k]
+    void* grad_logits[kMaxRanks];        // gradient: [T][E]
+    int rank0;                           // first rank (a rank view: the one rank)
+    int k, E;
+    int normalise;
+    int vec;                             // rows of whole 16-byte units at aligned bases, E a multiple of 8
+    size_t T, tokens;                    // tokens per rank, in all
+    Ctl ctl;
+};
+
+// ---- 4-bit linear ----------------------------------------------------------------------------------
+
+struct LinearArgs {
+    const uint16_t* x[kMaxRanks];        // bf16 [T][K]
+    const char* w[kMaxRanks];            // [N][K / 2] bytes, 16-byte aligned
+    const uint16_t* scale[kMaxRanks];    // bf16 [N][K / group]
+    void* out[kMaxRanks];                // [T][N]
+    int p, row;                          // row: the sum runs over the ranks too, every rank gets the result
+    int view_rank;                       // a rank view: the one rank whose output the call writes (-1: every rank)
+    size_t T, N, K;                      // of one rank's shard
+    int group_shift;                     // log2 of the weights per scale
+    int out_bf16;
+    int x_vec;                           // x rows are 16-byte aligned
+    int splits, chunk_shift;             // set by the launcher: warps per row tile; log2 of chunks per group
+    uint32_t tile_blocks, token_tiles;   // set by the launcher
+    Ctl ctl;
+};
+
+// ---- expert layer for few tokens -------------------------------------------------------------------
+
+constexpr int kLayerMaxAssignments = 4096;  // tokens x slots over all ranks: the sorted list is in shared memory
+
+struct MoeLayerArgs {
+    const uint16_t* x[kMaxRanks];        // bf16 [T][H]
+    const int32_t* idx[kMaxRanks];       // [T][k]
+    const float* weight[kMaxRanks];      // [T][k]
+    const uint16_t* res[kMaxRanks];      // bf16 [T][H] (has_res)
+    uint16_t* out[kMaxRanks];            // bf16 [T][H]
+    const char* up[kMaxRanks];           // [E/p][2F][H]: rows of G, then of U
+    const char* down[kMaxRanks];         // [E/p][H][F]
+    const uint16_t* up_scale[kMaxRanks];
+    const uint16_t* down_scale[kMaxRanks];
+    int rank0;                           // first rank whose tokens the call takes (a rank view: the one rank)
+    int k, E, E_loc, H, F, A;            // A: assignments in all
+    int has_res;
+    int weight_kind;                     // coll_weight_t
+    int group_shift;
+    int vec;                             // every row is whole 16-byte units at an aligned address
+    int splits_up, splits_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
+    size_t T;
+    uint16_t* h;                         // scratch: bf16 [A][h_stride]
+    size_t h_stride;
+    float* y;                            // scratch: [A][H]
+    uint64_t timeout_ns;
+    DevState* st;
+    Ctl ctl;
+};
+
+// ---- log probabilities over a sharded vocabulary ---------------------------------------------------
+
+constexpr int kLogprobMaxTop = 32;           // one lane per alternative
+constexpr int kLogprobMaxSplitRows = 1024;   // entries of DevState::row_ctr
+constexpr int kLogprobMaxParts = 64;
+
+struct LogprobArgs {
+    const void* logits[kMaxRanks];       // [rows][ld], m columns used
+    const int32_t* tokens;               // [rows], -1: none
+    float* logprob[kMaxRanks];           // [rows]
+    float* entropy[kMaxRanks];           // [rows] or null
+    float* lse[kMaxRanks];               // [rows] or null
+    int32_t* top_idx[kMaxRanks];         // [rows][n_top]
+    float* top_logprob[kMaxRanks];       // [rows][n_top]
+    const float* lse_in[kMaxRanks];      // gradient
+    const float* entropy_in[kMaxRanks];  // gradient, with grad_entropy
+    const float* grad_logprob;           // gradient: [rows]
+    const float* grad_entropy;           // gradient: [rows] or null
+    void* grad_logits[kMaxRanks];        // gradient: [rows][ld_grad]
+    int p, view_rank;
+    int n_top;
+    int parts;                           // CTAs per row (forward; the gradient's launcher sets its own)
+    size_t rows, V, m, ld, ld_grad;      // m = ceil(V / p): columns per rank
+    float4* part_stat;                   // scratch: [rows][parts]
+    unsigned long long* part_keys;       // scratch: [rows][parts][n_top]
+    DevState* st;
+    Ctl ctl;
+};
+
 // ---- HBM access-pattern probes (not collectives) --------------------------------------------------
 enum ProbeKind { PROBE_LOAD = 0, PROBE_STORE = 1, PROBE_COPY = 2, PROBE_BULK_STORE = 3, PROBE_BULK_FANOUT = 4 };
 constexpr int kProbeFanCopies = 8;  // PROBE_BULK_FANOUT writes this many copies of src
@@ -249,6 +346,11 @@ int ring_ll_max_ctas(int num_sms);
 cudaError_t launch_tree(const TreeArgs& a, int dtype, int op, int ctas, cudaStream_t s);
 cudaError_t launch_moe_dispatch(const MoeArgs& a, int num_sms, cudaStream_t s, int* kernels_launched);
 cudaError_t launch_moe_combine(const MoeArgs& a, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_route(const RouteArgs& a, int dtype, bool backward, cudaStream_t s);
+cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_moe_layer(const MoeLayerArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_logprobs_grad(const LogprobArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_probe(int kind, void* dst, const void* src, size_t bytes, int ctas_per_sm, int num_sms,
                          cudaStream_t s);
 

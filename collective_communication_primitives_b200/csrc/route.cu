@@ -1,0 +1,377 @@
+// Router of a mixture-of-experts layer: softmax over the experts' scores, the k best, their weights; and
+// the gradient of the scores.
+//
+//   P = softmax(x[t]),  idx[t][s] = the s-th largest score (the lower id among equals),
+//   w[t][s] = P[idx[t][s]], or with `normalise` P[idx[t][s]] / sum over the picked ones
+//   gradient, from g = dL/dw:
+//     normalise:  dx[e] = sum over s with idx[s] = e of w[s] (g[s] - sum_q g[q] w[q])
+//     otherwise:  dx[e] = P[e] (G[e] - sum_q g[q] w[q]),  G[e] = the sum of g[s] over s with idx[s] = e
+//
+// One pass: a token's row is held in the registers of a group of lanes (8 scores per lane up to 256
+// experts, so that a warp takes 32 / lanes tokens and a lane's row piece is one or two 16-byte loads),
+// and the k rounds of "largest that is left" work on order-preserving integers: the group's maximum by
+// shuffles, then the first lane that holds it, then the first of its scores. Rows of more than 1024
+// experts are read again for every round, a warp per token (from cache; a row is at most 16 KiB).
+// Scores that are NaN are picked last and make the row's weights NaN; a row of nothing but -inf has
+// weight 0 for every pick.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace simcomm {
+
+constexpr int kRouteThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Unsigned integers in the order of the floats, NaN below everything, 0 below that (no score).
+__device__ __forceinline__ uint32_t order_key(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);  // -0 and +0 are equal scores
+    const uint32_t o = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
+    return x != x ? 1u : o;
+}
+
+template <int DT> __device__ __forceinline__ float ld_score(const void* row, int e) { return load_elem<DT>(row, size_t(e)); }
+
+// The VPL scores from e0 of a row of E (missing ones: `fill`). vec: 16-byte loads, E a multiple of 8.
+template <int DT, int VPL>
+__device__ __forceinline__ void ld_scores(float (&v)[VPL], const void* row, int e0, int E, bool vec, float fill) {
+    if (vec) {
+        using P = Pack16<DT>;
+#pragma unroll
+        for (int j = 0; j < VPL; j += P::L) {
+            float part[P::L];
+            if (e0 + j < E) {
+                P::unpack(ld_stream_v4(static_cast<const char*>(row) + size_t(e0 + j) * Elem<DT>::kBytes), part);
+            } else {
+#pragma unroll
+                for (int q = 0; q < P::L; ++q) part[q] = fill;
+            }
+#pragma unroll
+            for (int q = 0; q < P::L; ++q) v[j + q] = part[q];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) v[j] = e0 + j < E ? ld_score<DT>(row, e0 + j) : fill;
+    }
+}
+
+template <int LPT> __device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+template <int LPT> __device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return v;
+}
+template <int LPT> __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
+    if constexpr (LPT == 32) {
+        return __reduce_max_sync(0xffffffffu, v);
+    } else {
+#pragma unroll
+        for (int d = LPT / 2; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+        return v;
+    }
+}
+
+// Softmax terms of the row in place: v[j] = e^(v[j] - max), the sum over the group returned. Missing
+// scores are -inf. A row of nothing but -inf has terms and sum 0; NaN or +inf makes the sum NaN.
+template <int LPT, int VPL> __device__ __forceinline__ float softmax_terms(float (&v)[VPL], float* top) {
+    float m = v[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) m = fmaxf(m, v[j]);
+    m = group_max<LPT>(m);
+    *top = m;
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        v[j] = exp2_fast((v[j] - base) * kLog2e);
+        sum += v[j];
+    }
+    return group_sum<LPT>(sum);
+}
+
+template <int DT, int LPT, int VPL>
+__global__ void __launch_bounds__(kRouteThreads) k_route(const __grid_constant__ RouteArgs a) {
+    if (status_failed(a.ctl)) return;
+    constexpr int kPerWarp = 32 / LPT;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, grp = lane / LPT;
+    const unsigned gmask = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (grp * LPT);
+    const size_t warp = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
+    const size_t token = warp * kPerWarp + grp;
+    const bool live = token < a.tokens;
+    const int rank = a.rank0 + int(live ? token / a.T : 0);
+    const size_t t = live ? token % a.T : 0;
+    const char* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
+    const int e0 = sub * VPL;
+    float v[VPL];
+    ld_scores<DT, VPL>(v, row, e0, live ? a.E : 0, a.vec, -INFINITY);
+    uint32_t key[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = e0 + j < a.E ? order_key(v[j]) : 0u;
+    float top;
+    const float sum = softmax_terms<LPT, VPL>(v, &top);
+    // k rounds: lane s of the group keeps pick s (k may exceed the group: pick s is kept by lane s % LPT)
+    float picked = 0.0f;  // sum of the picked terms
+    for (int s = 0; s < a.k; ++s) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+        const uint32_t all = group_umax<LPT>(best);
+        const unsigned who = __ballot_sync(0xffffffffu, best == all) & gmask;
+        const int winner = __ffs(who) - 1;
+        int at = 0;
+        float term = 0.0f;
+#pragma unroll
+        for (int j = VPL - 1; j >= 0; --j)
+            if (key[j] == all) {
+                at = j;
+                term = v[j];
+            }
+        if (lane == winner) {
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (j == at) key[j] = 0u;
+        }
+        const int e = __shfl_sync(0xffffffffu, e0 + at, winner);
+        term = __shfl_sync(0xffffffffu, term, winner);
+        picked += term;
+        if (live && sub == 0) {
+            a.idx_out[rank][t * a.k + s] = e;
+            a.weight[rank][t * a.k + s] = term;  // scaled below, by the same lane
+        }
+    }
+    if (live && sub == 0) {
+        const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
+        for (int s = 0; s < a.k; ++s) {
+            float* w = a.weight[rank] + t * a.k + s;
+            *w = total == 0.0f ? 0.0f : *w / total;
+        }
+    }
+}
+
+template <int DT, int LPT, int VPL>
+__global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_constant__ RouteArgs a) {
+    if (status_failed(a.ctl)) return;
+    constexpr int kPerWarp = 32 / LPT;
+    const int lane = threadIdx.x & 31, sub = lane % LPT, grp = lane / LPT;
+    const size_t warp = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
+    const size_t token = warp * kPerWarp + grp;
+    const bool live = token < a.tokens;
+    const int rank = a.rank0 + int(live ? token / a.T : 0);
+    const size_t t = live ? token % a.T : 0;
+    const char* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
+    const int32_t* idx = a.idx_in[rank] + t * a.k;
+    const float* gw = a.grad_weight[rank] + t * a.k;
+    const int e0 = sub * VPL;
+    const int k = live ? a.k : 0;
+    float v[VPL], G[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) G[j] = 0.0f;
+    float total, dot = 0.0f;  // the weights' divisor, and sum_q g[q] * term[q]
+    bool bad = false;
+    if (a.normalise) {
+        // only the picked scores matter: every lane of the group reads all k of them
+        float top = -INFINITY;
+        for (int s = 0; s < k; ++s) {
+            const int e = idx[s];
+            if (e < 0 || e >= a.E) bad = true;
+            else {
+                const float x = ld_score<DT>(row, e);
+                top = x > top || x != x ? x : top;
+            }
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+        total = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) v[j] = 0.0f;
+        for (int s = 0; s < k; ++s) {
+            const int e = idx[s];
+            if (e < 0 || e >= a.E) continue;
+            const float term = exp2_fast((ld_score<DT>(row, e) - base) * kLog2e), g = gw[s];
+            total += term;
+            dot = __fmaf_rn(g, term, dot);
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e == e0 + j) {
+                    v[j] += term;
+                    G[j] = __fmaf_rn(g, term, G[j]);
+                }
+        }
+        // dx = sum of term/total (g - dot/total)
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const float mean = dot * inv;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) G[j] = (G[j] - v[j] * mean) * inv;
+    } else {
+        ld_scores<DT, VPL>(v, row, e0, live ? a.E : 0, a.vec, -INFINITY);
+        float top;
+        total = softmax_terms<LPT, VPL>(v, &top);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        for (int s = 0; s < k; ++s) {
+            const int e = idx[s];
+            if (e < 0 || e >= a.E) {
+                bad = true;
+                continue;
+            }
+            const float g = gw[s];
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (e == e0 + j) {
+                    G[j] += g;
+                    dot = __fmaf_rn(g, v[j], dot);
+                }
+        }
+        const float mean = group_sum<LPT>(dot) * inv;  // each lane summed the picks it holds
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) G[j] = v[j] * inv * (G[j] - mean);
+    }
+    if (bad) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+    if (!live) return;
+    char* out = static_cast<char*>(a.grad_logits[rank]) + t * a.E * Elem<DT>::kBytes;
+    if (a.vec) {
+        using P = Pack16<DT>;
+#pragma unroll
+        for (int j = 0; j < VPL; j += P::L) {
+            if (e0 + j >= a.E) continue;
+            float part[P::L];
+#pragma unroll
+            for (int q = 0; q < P::L; ++q) part[q] = G[j + q];
+            st_v4(out + size_t(e0 + j) * Elem<DT>::kBytes, P::pack(part));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j < a.E) store_elem<DT>(out, size_t(e0 + j), G[j]);
+    }
+}
+
+// More than 1024 experts: a warp per token, the row read again for every round.
+template <int DT> __global__ void __launch_bounds__(kRouteThreads) k_route_wide(const __grid_constant__ RouteArgs a, int backward) {
+    if (status_failed(a.ctl)) return;
+    const int lane = threadIdx.x & 31;
+    const size_t token = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
+    if (token >= a.tokens) return;
+    const int rank = a.rank0 + int(token / a.T);
+    const size_t t = token % a.T;
+    const void* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
+    float m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, ld_score<DT>(row, e));
+    m = group_max<32>(m);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+    for (int e = lane; e < a.E; e += 32) sum += exp2_fast((ld_score<DT>(row, e) - base) * kLog2e);
+    sum = group_sum<32>(sum);
+    if (!backward) {
+        uint32_t last = 0xffffffffu;  // the last pick: (order key, id), picks go down the keys and up the ids
+        int last_e = -1;
+        float picked = 0.0f;
+        for (int s = 0; s < a.k; ++s) {
+            uint32_t best = 0u;
+            int at = INT32_MAX;
+            for (int e = lane; e < a.E; e += 32) {
+                const uint32_t key = order_key(ld_score<DT>(row, e));
+                const bool left = key < last || (key == last && e > last_e);
+                if (left && key > best) {
+                    best = key;
+                    at = e;
+                }
+            }
+            const uint32_t all = __reduce_max_sync(0xffffffffu, best);
+            const int e = int(__reduce_min_sync(0xffffffffu, best == all ? unsigned(at) : unsigned(INT32_MAX)));
+            last = all;
+            last_e = e;
+            const float term = exp2_fast((ld_score<DT>(row, e) - base) * kLog2e);
+            picked += term;
+            if (lane == 0) {
+                a.idx_out[rank][t * a.k + s] = e;
+                a.weight[rank][t * a.k + s] = term;
+            }
+        }
+        if (lane == 0) {
+            const float total = a.normalise ? picked + 0.0f * sum : sum;
+            for (int s = 0; s < a.k; ++s) {
+                float* w = a.weight[rank] + t * a.k + s;
+                *w = total == 0.0f ? 0.0f : *w / total;
+            }
+        }
+        return;
+    }
+    const int32_t* idx = a.idx_in[rank] + t * a.k;
+    const float* gw = a.grad_weight[rank] + t * a.k;
+    bool bad = false;
+    float top = -INFINITY;
+    for (int s = 0; s < a.k; ++s) {
+        if (idx[s] < 0 || idx[s] >= a.E) {
+            bad = true;
+            continue;
+        }
+        const float x = ld_score<DT>(row, idx[s]);
+        top = x > top || x != x ? x : top;
+    }
+    if (bad) {  // nothing written: the call has failed
+        if (lane == 0) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+        return;
+    }
+    const float from = a.normalise ? (top == -INFINITY ? 0.0f : top) : base;
+    float total = 0.0f, dot = 0.0f;
+    for (int s = 0; s < a.k; ++s) {
+        const float term = exp2_fast((ld_score<DT>(row, idx[s]) - from) * kLog2e);
+        total += term;
+        dot = __fmaf_rn(gw[s], term, dot);
+    }
+    if (!a.normalise) total = sum;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * inv;
+    for (int e = lane; e < a.E; e += 32) {
+        float g = 0.0f;
+        int hits = 0;
+        for (int s = 0; s < a.k; ++s)
+            if (idx[s] == e) {
+                g += gw[s];
+                ++hits;
+            }
+        float d = 0.0f;
+        if (!a.normalise) d = exp2_fast((ld_score<DT>(row, e) - from) * kLog2e) * inv * (g - mean);
+        else if (hits) d = exp2_fast((ld_score<DT>(row, e) - from) * kLog2e) * inv * (g - float(hits) * mean);
+        store_elem<DT>(static_cast<char*>(a.grad_logits[rank]) + t * a.E * Elem<DT>::kBytes, size_t(e), d);
+    }
+}
+
+template <int DT> static cudaError_t launch_route_dt(const RouteArgs& a, bool backward, cudaStream_t s) {
+    auto grid = [&](int lanes) {
+        const size_t per_cta = size_t(kRouteThreads / lanes);
+        return unsigned((a.tokens + per_cta - 1) / per_cta);
+    };
+#define SIMCOMM_ROUTE(LPT, VPL)                                                          \
+    do {                                                                                 \
+        if (backward) k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 0, s>>>(a); \
+        else k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 0, s>>>(a);               \
+        return cudaGetLastError();                                                       \
+    } while (0)
+    if (a.E <= 8) SIMCOMM_ROUTE(1, 8);
+    if (a.E <= 16) SIMCOMM_ROUTE(2, 8);
+    if (a.E <= 32) SIMCOMM_ROUTE(4, 8);
+    if (a.E <= 64) SIMCOMM_ROUTE(8, 8);
+    if (a.E <= 128) SIMCOMM_ROUTE(16, 8);
+    if (a.E <= 256) SIMCOMM_ROUTE(32, 8);
+    if (a.E <= 512) SIMCOMM_ROUTE(32, 16);
+    if (a.E <= 1024) SIMCOMM_ROUTE(32, 32);
+#undef SIMCOMM_ROUTE
+    k_route_wide<DT><<<grid(32), kRouteThreads, 0, s>>>(a, backward ? 1 : 0);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_route(const RouteArgs& a, int dtype, bool backward, cudaStream_t s) {
+    if ((a.tokens + 7) / 8 > size_t(INT32_MAX)) return cudaErrorInvalidValue;
+    return dtype == COLL_BF16 ? launch_route_dt<COLL_BF16>(a, backward, s) : launch_route_dt<COLL_FP32>(a, backward, s);
+}
+
+}  // namespace simcomm

@@ -19,6 +19,8 @@ OPS = {"sum": 0, "min": 1, "max": 2, "avg": 3}
 ALGOS = {"direct": 0, "ring": 1, "rd": 2, "hd": 3, "tree": 4, "dbtree": 5, "ll": 6, "rd_ll": 7, "tree_ll": 8,
          "dbtree_ll": 9}
 
+PARALLEL = {"column": 0, "row": 1}
+
 _lib = None
 
 
@@ -104,6 +106,15 @@ def load_library(path=LIB_PATH):
     pp = ctypes.POINTER(ctypes.c_void_p)
     L.coll_moe_dispatch.argtypes = [vp, pp, pp, sz, i32, sz, i32, i32, pp, sz, pp, vp, vp, vp]
     L.coll_moe_combine.argtypes = [vp, pp, sz, pp, pp, pp, pp, sz, i32, sz, i32, i32, pp, vp]
+    L.coll_moe_route.argtypes = [vp, pp, sz, i32, i32, i32, i32, pp, pp, vp]
+    L.coll_moe_route_backward.argtypes = [vp, pp, pp, pp, sz, i32, i32, i32, i32, pp, vp]
+    L.coll_linear_w4.argtypes = [vp, pp, pp, pp, sz, sz, sz, i32, i32, i32, pp, vp]
+    L.coll_moe_layer.argtypes = [vp, pp, pp, pp, pp, sz, i32, sz, sz, i32, i32, i32, pp, pp, pp, pp, i32, pp, vp]
+    L.coll_logprobs.argtypes = [vp, pp, sz, vp, sz, sz, i32, pp, pp, pp, i32, pp, pp, vp]
+    L.coll_logprobs_backward.argtypes = [vp, pp, sz, vp, sz, sz, i32, pp, pp, vp, vp, pp, sz, vp]
+    for name in ("coll_moe_route", "coll_moe_route_backward", "coll_linear_w4", "coll_moe_layer", "coll_logprobs",
+                 "coll_logprobs_backward"):
+        getattr(L, name).restype = st
     for name in ("coll_allreduce", "coll_reduce", "coll_broadcast", "coll_reduce_scatter", "coll_allgather",
                  "coll_alltoall", "coll_alltoallv", "coll_scatter", "coll_gather", "coll_allreduce_ring_noalloc",
                  "coll_moe_dispatch", "coll_moe_combine", "sim_hbm_probe"):
@@ -150,6 +161,8 @@ class SimComm:
         self._h = ctypes.c_void_p(h)
         self.p = int(p)
         self.rank = None if rank is None else int(rank)
+        import torch
+        self._device = torch.cuda.current_device()
 
     # -- lifecycle ---------------------------------------------------------------------------------
     def close(self):
@@ -316,6 +329,164 @@ class SimComm:
             self._h, self._parr(y), y[0].shape[0], self._parr(topk_idx), self._parr(route_pos),
             self._parr(topk_weight), self._parr(residual), T, k, H, int(experts),
             self._resolve(dtype, list(y) + list(out)), self._parr(out), _stream(stream)))
+
+
+    # -- router, products with sharded weights, log probabilities ------------------------------------
+    def _tensors(self, what, tensors, dtype, numel, row=None, one=False):
+        """HOST array of the ranks' device pointers, after checking that every tensor is where and what
+        the kernels take it for: on the communicator's device, of `dtype` (a torch dtype), `numel`
+        elements, contiguous (or, with `row` = (ld, columns), rows at that distance). A rank view's
+        entries of other ranks may be None or addresses. `one`: a single tensor, its address."""
+        if tensors is None:
+            return None
+        out = []
+        for t in ((tensors,) if one else tensors):
+            if t is None or isinstance(t, int):
+                if self.rank is None:
+                    raise TypeError(f"{what}: a tensor for every rank is needed")
+                out.append(t)
+                continue
+            if t.dtype is not dtype:
+                raise TypeError(f"{what}: {t.dtype}, not {dtype}")
+            if t.get_device() != self._device:
+                raise ValueError(f"{what}: on {t.device}, not on the communicator's device")
+            if row is not None and t.shape[0] > 1:
+                if t.numel() != numel or t.stride(1) != 1 or t.stride(0) != row[0]:
+                    raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()} do not fit the call")
+            elif t.numel() != numel or not t.is_contiguous():
+                raise ValueError(f"{what}: {t.numel()} elements ({numel} are wanted), or not contiguous")
+            out.append(t.data_ptr())
+        if one:
+            return out[0]
+        if len(out) != self.p:
+            raise ValueError(f"{what}: {len(out)} entries for {self.p} ranks")
+        return (ctypes.c_void_p * self.p)(*out)
+
+    def _own(self, tensors):
+        """A tensor of this handle's own ranks, whose shape and type stand for all."""
+        return tensors[0 if self.rank is None else self.rank]
+
+    def moe_route(self, logits, topk_idx, topk_weight, normalise=True, stream=None):
+        """Softmax over logits[i] [T][E] (fp32 or bf16), the k best experts of every token into topk_idx[i]
+        [T][k] int32 and their weights (shares of the k when `normalise`) into topk_weight[i] [T][k] fp32:
+        what moe_dispatch, moe_combine and moe_layer take."""
+        import torch
+        x = self._own(logits)
+        T, E = x.shape
+        k = self._own(topk_idx).shape[1]
+        self._check(self._L.coll_moe_route(
+            self._h, self._tensors("logits", logits, x.dtype, T * E), T, k, E, DTYPES[_dtype_of(x)], 1 if normalise else 0,
+            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
+            self._tensors("topk_weight", topk_weight, torch.float32, T * k), _stream(stream)))
+
+    def moe_route_backward(self, logits, topk_idx, grad_weight, grad_logits, normalise=True, stream=None):
+        """Gradient of moe_route's scores into grad_logits[i] [T][E] (of the scores' type), from grad_weight[i]
+        [T][k] fp32, the gradient of its weights."""
+        import torch
+        x = self._own(logits)
+        T, E = x.shape
+        k = self._own(topk_idx).shape[1]
+        self._check(self._L.coll_moe_route_backward(
+            self._h, self._tensors("logits", logits, x.dtype, T * E),
+            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
+            self._tensors("grad_weight", grad_weight, torch.float32, T * k), T, k, E, DTYPES[_dtype_of(x)],
+            1 if normalise else 0, self._tensors("grad_logits", grad_logits, x.dtype, T * E), _stream(stream)))
+
+    def linear_w4(self, x, w, scale, out, parallel="row", stream=None):
+        """out = x W^T for few tokens, W of 4-bit weights (q - 8) * scale: w[r] uint8 [N_r][K_r/2] (element 2i in
+        the low half of byte i), scale[r] bf16 [N_r][K_r/group], x[r] bf16 [T][K_r]. parallel "column": the
+        ranks hold rows of W and out[r] is [T][N/p]; "row": they hold columns, the partial products are summed
+        and every out[r] is [T][N]. out fp32 or bf16."""
+        import torch
+        if parallel not in PARALLEL:
+            raise ValueError(f"parallel must be one of {sorted(PARALLEL)}")
+        o = self._own(out)
+        T, K = self._own(x).shape
+        N = self._own(w).shape[0]
+        groups = self._own(scale).shape[1]
+        if groups < 1 or K % groups:
+            raise ValueError(f"scale: {groups} groups do not divide rows of {K}")
+        row = parallel == "row"
+        self._check(self._L.coll_linear_w4(
+            self._h, self._tensors("x", x, torch.bfloat16, T * K), self._tensors("w", w, torch.uint8, N * (K // 2)),
+            self._tensors("scale", scale, torch.bfloat16, N * groups), T, N if row else N * self.p,
+            K * self.p if row else K, K // groups, PARALLEL[parallel], DTYPES[_dtype_of(o)],
+            self._tensors("out", out, o.dtype, T * N), _stream(stream)))
+
+    def moe_layer(self, x, topk_idx, topk_weight, experts, w_up, w_down, out, up_scale=None, down_scale=None,
+                  residual=None, stream=None):
+        """A whole expert layer for a few tokens: out[i][t] = residual[i][t] + sum_s w[i][t][s] * D_e (silu(G_e x) *
+        (U_e x)). x, residual, out bf16 [T][H]; w_up[j] [E/p][2F][H] (G's rows, then U's) and w_down[j]
+        [E/p][H][F] bf16, or, with up_scale [E/p][2F][H/group] and down_scale [E/p][H][F/group] (bf16), 4-bit:
+        uint8 with half as many columns."""
+        import torch
+        T, H = self._own(x).shape
+        k = self._own(topk_idx).shape[1]
+        el, rows = self._own(w_up).shape[:2]
+        F = rows // 2
+        q4 = up_scale is not None
+        if q4 != (down_scale is not None) or rows != 2 * F or el * self.p != experts:
+            raise ValueError("w_up must be [experts / p][2 F][...], and both scales or none be given")
+        group, wt, n, su, sd = 0, torch.bfloat16, el * F * H, None, None
+        if q4:
+            groups = self._own(up_scale).shape[2]
+            if groups < 1 or H % groups or F % (H // groups):
+                raise ValueError(f"up_scale: {groups} groups do not fit rows of {H} and {F}")
+            group, wt, n = H // groups, torch.uint8, el * F * (H // 2)
+            su = self._tensors("up_scale", up_scale, torch.bfloat16, el * rows * groups)
+            sd = self._tensors("down_scale", down_scale, torch.bfloat16, el * H * (F // group))
+        self._check(self._L.coll_moe_layer(
+            self._h, self._tensors("x", x, torch.bfloat16, T * H),
+            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
+            self._tensors("topk_weight", topk_weight, torch.float32, T * k),
+            self._tensors("residual", residual, torch.bfloat16, T * H), T, k, H, F, int(experts), 1 if q4 else 0, group,
+            self._tensors("w_up", w_up, wt, 2 * n), su, self._tensors("w_down", w_down, wt, n), sd, DTYPES["bf16"],
+            self._tensors("out", out, torch.bfloat16, T * H), _stream(stream)))
+
+    def logprobs(self, logits, tokens, vocab, logprob, entropy=None, lse=None, top_idx=None, top_logprob=None,
+                 stream=None):
+        """Log probabilities of `tokens` (int32 [R], -1: none) under rows of scores whose `vocab` columns are
+        sharded over the ranks: logits[r] [R][m], m = ceil(vocab / p), fp32 or bf16, rows at any distance. Every
+        rank gets logprob[r], entropy[r], lse[r] fp32 [R] and the n best columns and their log probabilities
+        in top_idx[r] int32 and top_logprob[r] fp32 [R][n]."""
+        import torch
+        x = self._own(logits)
+        R, m = x.shape
+        if m != -(-int(vocab) // self.p):
+            raise ValueError(f"logits: {m} columns per rank for a vocabulary of {vocab} on {self.p} ranks")
+        ld = x.stride(0) if R > 1 else m
+        f = torch.float32
+        n = 0 if top_idx is None else self._own(top_idx).shape[1]
+        if (top_idx is None) != (top_logprob is None):
+            raise ValueError("top_idx and top_logprob go together")
+        self._check(self._L.coll_logprobs(
+            self._h, self._tensors("logits", logits, x.dtype, R * m, row=(ld, m)), ld,
+            self._tensors("tokens", tokens, torch.int32, R, one=True), R, int(vocab), DTYPES[_dtype_of(x)],
+            self._tensors("logprob", logprob, f, R), self._tensors("entropy", entropy, f, R),
+            self._tensors("lse", lse, f, R), n, self._tensors("top_idx", top_idx, torch.int32, R * n),
+            self._tensors("top_logprob", top_logprob, f, R * n), _stream(stream)))
+
+    def logprobs_backward(self, logits, tokens, vocab, lse, grad_logprob, grad_logits, entropy=None,
+                          grad_entropy=None, stream=None):
+        """Gradient of logprobs' scores into grad_logits[r] [R][m] (of the scores' type, zeros in padding
+        columns), from grad_logprob and grad_entropy (fp32 [R], the latter with `entropy`) and the forward
+        call's lse[r] and entropy[r]."""
+        import torch
+        x, g = self._own(logits), self._own(grad_logits)
+        R, m = x.shape
+        if m != -(-int(vocab) // self.p):
+            raise ValueError(f"logits: {m} columns per rank for a vocabulary of {vocab} on {self.p} ranks")
+        ld, ldg = (x.stride(0), g.stride(0)) if R > 1 else (m, m)
+        f = torch.float32
+        if grad_entropy is not None and entropy is None:
+            raise ValueError("grad_entropy needs entropy")
+        self._check(self._L.coll_logprobs_backward(
+            self._h, self._tensors("logits", logits, x.dtype, R * m, row=(ld, m)), ld,
+            self._tensors("tokens", tokens, torch.int32, R, one=True), R, int(vocab), DTYPES[_dtype_of(x)],
+            self._tensors("lse", lse, f, R), self._tensors("entropy", entropy, f, R),
+            self._tensors("grad_logprob", grad_logprob, f, R, one=True),
+            None if grad_entropy is None else self._tensors("grad_entropy", grad_entropy, f, R, one=True),
+            self._tensors("grad_logits", grad_logits, x.dtype, R * m, row=(ldg, m)), ldg, _stream(stream)))
 
 
 def allreduce_ring_noalloc(sends, recvs, op="sum", n=None, dtype=None, status=None, stream=None):

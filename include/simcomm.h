@@ -397,6 +397,134 @@ coll_status_t coll_moe_combine(sim_comm_t comm, const void* const* y, size_t y_r
                                const void* const* residual, size_t tokens, int k, size_t hidden, int experts,
                                coll_dtype_t dtype, void* const* out, coll_stream_t stream);
 
+/* ---- MoE router ------------------------------------------------------------------------------- */
+
+/* Router of an expert layer: the step before the dispatch ([Primer] "Expert Parallel": the router picks
+ * the experts and their weights). Per token: P = softmax over the experts' scores, idx[s] = the expert of
+ * the s-th largest score (the lower id among equals), w[s] = P[idx[s]], divided by the sum of the k
+ * picked ones when `normalise` is not 0.
+ *   logits       HOST array of p DEVICE pointers, [T][E] scores, fp32 or bf16.
+ *   topk_idx     HOST array of p DEVICE pointers, output [T][k] int32: what coll_moe_dispatch,
+ *                coll_moe_combine and coll_moe_layer take.
+ *   topk_weight  HOST array of p DEVICE pointers, output [T][k] fp32.
+ * Computed in fp32. A score of -inf (a masked expert) has weight 0 and is picked only when fewer than k
+ * others are left; a row of nothing but -inf has weights 0 and ids 0..k-1. A NaN score is picked last; a
+ * row with a NaN or +inf has weights NaN. k in [1, 32], k <= E, E a multiple of p, at most 4096. int32
+ * scores: COLL_ERR_UNSUPPORTED. No output may overlap another buffer. T = 0 enqueues nothing. On a rank
+ * view only this rank's entries are used. */
+coll_status_t coll_moe_route(sim_comm_t comm, const void* const* logits, size_t tokens, int k, int experts,
+                             coll_dtype_t dtype, int normalise, int32_t* const* topk_idx, float* const* topk_weight,
+                             coll_stream_t stream);
+
+/* Gradient of coll_moe_route's scores, from the gradient of its weights (the picks themselves have none):
+ *   normalise:  grad_logits[e] = sum over s with idx[s] = e of w[s] (g[s] - sum_q g[q] w[q])
+ *   otherwise:  grad_logits[e] = P[e] (sum over s with idx[s] = e of g[s] - sum_q g[q] w[q])
+ * for every e (0 where the sum is empty). P and w are computed again from logits (unchanged since the
+ * forward call); an id that occurs twice in a row counts twice.
+ *   grad_weight  HOST array of p DEVICE pointers, [T][k] fp32.
+ *   grad_logits  HOST array of p DEVICE pointers, output [T][E] of the scores' type.
+ * Other arguments and refusals as for coll_moe_route. An id outside [0, E) is reported asynchronously as
+ * COLL_ERR_INVALID_ARG. */
+coll_status_t coll_moe_route_backward(sim_comm_t comm, const void* const* logits, const int32_t* const* topk_idx,
+                                      const float* const* grad_weight, size_t tokens, int k, int experts,
+                                      coll_dtype_t dtype, int normalise, void* const* grad_logits, coll_stream_t stream);
+
+/* ---- products with sharded weights -------------------------------------------------------------- */
+
+/* How a weight matrix [N][K] is held.
+ * BF16: row-major bf16.
+ * INT4: row-major 4-bit whole numbers q, two to a byte (element 2i in the low half of byte i), with one
+ *       bf16 scale per `group` consecutive elements of a row: W[n][k] = (q[n][k] - 8) * scale[n][k / group].
+ *       group is a power of two, 32 or more, and divides K. Weight pointers are 16-byte aligned. */
+typedef enum { COLL_WEIGHT_BF16 = 0, COLL_WEIGHT_INT4 = 1 } coll_weight_t;
+
+/* Where the ranks' shards of the matrix lie (the tensor-parallel mapping of [Primer]).
+ * COLUMN: rank r holds rows [r N/p, (r+1) N/p) of W and a copy of x; out[r] [T][N/p] is its block of the
+ *         result (Sharded: what coll_logprobs takes as scores).
+ * ROW:    rank r holds columns [r K/p, (r+1) K/p) of W and of x; the ranks' partial products are summed
+ *         (the AllReduce, inside the product's kernel) and every rank gets out[r] [T][N]. */
+typedef enum { COLL_PARALLEL_COLUMN = 0, COLL_PARALLEL_ROW = 1 } coll_parallel_t;
+
+/* Few tokens times a matrix of 4-bit weights: out = x W^T, W as COLL_WEIGHT_INT4. For one to some tens of
+ * tokens; any number works, every further 32 read the weights again.
+ *   x      HOST array of p DEVICE pointers, bf16 [T][K] (COLUMN) or [T][K/p] (ROW).
+ *   w      HOST array of p DEVICE pointers, the shards' packed weights.
+ *   scale  HOST array of p DEVICE pointers, bf16, a shard's rows x (its K / group).
+ *   n, k   rows and columns of the FULL matrix; N divisible by p (COLUMN) or K by p * group (ROW).
+ *   dtype  type of out: fp32 or bf16 (int32: COLL_ERR_UNSUPPORTED).
+ * Weights are not rounded: whole numbers times bf16 tokens are summed in fp32 per group and scaled in
+ * fp32; one rounding to the output's type. No output may overlap another buffer. T = 0 or N = 0 enqueues
+ * nothing; K = 0 is refused. On a rank view, COLUMN uses this rank's entries only; ROW reads every rank's
+ * x, w and scale as this process maps them and writes this rank's out. */
+coll_status_t coll_linear_w4(sim_comm_t comm, const void* const* x, const void* const* w, const void* const* scale,
+                             size_t tokens, size_t n, size_t k, int group, coll_parallel_t parallel, coll_dtype_t dtype,
+                             void* const* out, coll_stream_t stream);
+
+/* A whole expert layer for a few tokens (a decode step), in one kernel:
+ *   out[i][t] = residual[i][t] + sum_s w[i][t][s] * D_e (silu(G_e x[i][t]) * (U_e x[i][t])),  e = idx[i][t][s]
+ * with silu(a) = a / (1 + e^-a): what coll_moe_dispatch, the experts and coll_moe_combine compute, without
+ * moving a row. Expert e's matrices lie on rank e / (E/p).
+ *   x, residual, out   HOST arrays of p DEVICE pointers, bf16 [T][H]; residual NULL: none; residual[i] may
+ *                      equal out[i].
+ *   topk_idx, topk_weight  as coll_moe_route writes them, [T][k].
+ *   w_up     HOST array of p DEVICE pointers, [E/p][2F][H]: per expert F rows of G, then F rows of U.
+ *   w_down   HOST array of p DEVICE pointers, [E/p][H][F].
+ *   up_scale, down_scale  INT4: scales [E/p][2F][H/group], [E/p][H][F/group]; BF16: NULL (not read).
+ *   weight, group  COLL_WEIGHT_BF16 (group ignored) or COLL_WEIGHT_INT4 (group divides H and F).
+ *   dtype    of x, residual and out: COLL_BF16 (others: COLL_ERR_UNSUPPORTED).
+ * Products are summed in fp32; silu(g) u is rounded to bf16 (the type of the second product's operand);
+ * the weighted sum runs in slot order in fp32 like the combine's, rounded once. p * T * k (a rank view:
+ * T * k) may be at most 4096, else COLL_ERR_UNSUPPORTED: larger batches go through the dispatch. An expert
+ * id outside [0, E) is reported asynchronously as COLL_ERR_INVALID_ARG and nothing is written. Rows of
+ * whole 16-byte units at 16-byte aligned addresses take 16-byte loads, others element-wise ones. Needs a
+ * device with cooperative launches. On a rank view w_up and w_down (and scales) are every rank's as this
+ * process maps them, the other arrays use this rank's entry. */
+coll_status_t coll_moe_layer(sim_comm_t comm, const void* const* x, const int32_t* const* topk_idx,
+                             const float* const* topk_weight, const void* const* residual, size_t tokens, int k,
+                             size_t hidden, size_t ffn, int experts, coll_weight_t weight, int group,
+                             const void* const* w_up, const void* const* up_scale, const void* const* w_down,
+                             const void* const* down_scale, coll_dtype_t dtype, void* const* out, coll_stream_t stream);
+
+/* ---- log probabilities over a sharded vocabulary ------------------------------------------------ */
+
+/* Log probabilities of given tokens, entropy and top alternatives of rows of scores whose V columns are
+ * Sharded over the ranks: rank r holds columns [r m, (r+1) m), m = ceil(V / p), in logits[r] [rows][ld],
+ * ld >= m (the last shards may end in padding columns, which are not read as scores). The rows' statistics
+ * are reduced over the ranks inside the kernel and every rank gets every result (Replicated):
+ *   logprob[r][t] = x[tokens[t]] - lse,  lse = ln sum_v e^x[v],  entropy = -sum_v P[v] ln P[v]
+ *   tokens       DEVICE int32 [rows], the one array all ranks read; -1: no token, logprob 0.
+ *   logprob      HOST array of p DEVICE pointers, output fp32 [rows].
+ *   entropy, lse HOST arrays of p DEVICE pointers, outputs fp32 [rows], or NULL.
+ *   top_n        in [0, 32], at most V; the columns of the top_n largest scores (the lower column among
+ *                equals) and their log probabilities go to top_idx[r] [rows][top_n] int32 and
+ *                top_logprob[r] [rows][top_n] fp32 (both NULL when top_n is 0).
+ * Scores fp32 or bf16, computed in fp32. A score of -inf has probability 0; a row of nothing but -inf has
+ * lse and logprob -inf and entropy 0. NaN or +inf in a row makes its values NaN; a NaN is never an
+ * alternative, and places left over for want of numbers hold column -1 and NaN. A token outside [-1, V) is
+ * reported asynchronously as COLL_ERR_INVALID_ARG. V in [1, 2^31). No output may overlap another buffer.
+ * rows = 0 enqueues nothing. On a rank view logits holds every rank's buffers as this process maps them,
+ * the outputs only this rank's entry. */
+coll_status_t coll_logprobs(sim_comm_t comm, const void* const* logits, size_t ld, const int32_t* tokens, size_t rows,
+                            size_t vocab, coll_dtype_t dtype, float* const* logprob, float* const* entropy,
+                            float* const* lse, int top_n, int32_t* const* top_idx, float* const* top_logprob,
+                            coll_stream_t stream);
+
+/* Gradient of the scores, from the gradients gl of logprob and ge of entropy (the alternatives have none):
+ *   grad_logits[r][t][c] = gl[t] ([v = tokens[t]] - P[v]) - ge[t] P[v] (ln P[v] + entropy[t]),  v = r m + c
+ * for the shard's m columns, 0 in padding columns; gl counts as 0 where tokens[t] is -1.
+ *   logits, ld, tokens, rows, vocab, dtype  as in the forward call, unchanged since.
+ *   lse          HOST array of p DEVICE pointers: the forward call's output.
+ *   entropy      likewise; may be NULL when grad_entropy is NULL.
+ *   grad_logprob DEVICE fp32 [rows]; grad_entropy DEVICE fp32 [rows] or NULL.
+ *   grad_logits  HOST array of p DEVICE pointers, output [rows][ld_grad] of the scores' type, ld_grad >= m;
+ *                columns past m are left untouched. Never in place: no output may overlap another buffer.
+ * On a rank view every rank's logits are given (a row whose lse passes 1e5 in magnitude is summed again,
+ * over all of them), the rest is this rank's. */
+coll_status_t coll_logprobs_backward(sim_comm_t comm, const void* const* logits, size_t ld, const int32_t* tokens,
+                                     size_t rows, size_t vocab, coll_dtype_t dtype, const float* const* lse,
+                                     const float* const* entropy, const float* grad_logprob, const float* grad_entropy,
+                                     void* const* grad_logits, size_t ld_grad, coll_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------------------------------ */
 
 /* HBM access-pattern probe (not a collective; the pages have no counterpart): streams `bytes` through
