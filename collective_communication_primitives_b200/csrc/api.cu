@@ -1919,6 +1919,7 @@ static coll_status_t coll_linear_w4_impl(sim_comm_t c, const void* const* x, con
     a.group_shift = shift;
     a.out_bf16 = dt == COLL_BF16;
     a.x_vec = vec ? 1 : 0;
+    a.timeout_ns = uint64_t(c->timeout_ns);
     a.ctl = make_ctl(c);
     cudaError_t e = launch_linear(a, c->num_sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
@@ -2083,11 +2084,19 @@ static coll_status_t coll_logprobs_impl(sim_comm_t c, const void* const* logits,
     }
     if ((st = sp.check()) != COLL_OK) return st;
     a.n_top = top_n;
-    // Few rows: several CTAs per row, about four per SM in all, none with less than 4096 columns.
+    // CTAs per row: four run on an SM at a time, so that the time goes as the number of waves times a CTA's
+    // columns, a fixed cost of about 4096 columns' worth, and 64 for each part that the last one joins.
     a.parts = 1;
-    if (rows < size_t(c->num_sms) * 2 && rows <= size_t(kLogprobMaxSplitRows)) {
-        const size_t want = (size_t(c->num_sms) * 4 + rows - 1) / rows, most = std::max<size_t>(1, vocab / 4096);
-        a.parts = int(std::min({want, most, size_t(kLogprobMaxParts)}));
+    if (rows <= size_t(kLogprobMaxSplitRows)) {
+        const size_t wave = size_t(c->num_sms) * 4, most = std::min(size_t(kLogprobMaxParts), std::max<size_t>(1, vocab / 1024));
+        size_t best = SIZE_MAX;
+        for (size_t q = 1; q <= most; ++q) {
+            const size_t cost = (rows * q + wave - 1) / wave * (vocab / q + 4096 + (q > 1 ? 64 * q : 0));
+            if (cost < best) {
+                best = cost;
+                a.parts = int(q);
+            }
+        }
     }
     if (a.parts > 1) {
         const size_t b_stat = align_up(rows * a.parts * sizeof(float4), 256);

@@ -25,7 +25,7 @@ struct DevState {
     uint32_t comb_done;              // MoE combine: CTAs that left the token loop (the last one resets both)
     uint32_t layer_ctr;              // expert layer: grid-barrier arrivals (zero between calls)
     uint32_t layer_done;             // expert layer: CTAs that left (the last one resets both)
-    uint32_t row_ctr[1024];          // log probabilities: parts of a row that are done (zero between calls)
+    uint32_t row_ctr[4096];          // log probabilities: parts of a row that are done (zero between calls)
 };
 
 // What a kernel needs to report errors and notice an abort.
@@ -266,6 +266,8 @@ struct LinearArgs {
     int x_vec;                           // x rows are 16-byte aligned
     int splits, chunk_shift;             // set by the launcher: warps per row tile; log2 of chunks per group
     uint32_t tile_blocks, token_tiles;   // set by the launcher
+    int units;                           // set by the launcher
+    uint64_t timeout_ns;
     Ctl ctl;
 };
 
@@ -302,7 +304,7 @@ struct MoeLayerArgs {
 // ---- log probabilities over a sharded vocabulary ---------------------------------------------------
 
 constexpr int kLogprobMaxTop = 32;           // one lane per alternative
-constexpr int kLogprobMaxSplitRows = 1024;   // entries of DevState::row_ctr
+constexpr int kLogprobMaxSplitRows = 4096;   // entries of DevState::row_ctr
 constexpr int kLogprobMaxParts = 64;
 
 struct LogprobArgs {

@@ -9,116 +9,141 @@
 // over k, whose range one CTA's warps split between them, and the epilogue stores the finished value to
 // every rank's output. Bound by the weights' bytes; the warp-level product is in wprod.cuh.
 #include <algorithm>
+#include <type_traits>
 
 #include "wprod.cuh"
 
 namespace simcomm {
-
-constexpr int kLinWarps = 8;
-constexpr int kLinThreads = kLinWarps * 32;
 
 template <bool BF16> __device__ __forceinline__ void st_out(void* p, size_t i, float v) {
     if constexpr (BF16) static_cast<uint16_t*>(p)[i] = float_to_bf16_bits(v);
     else static_cast<float*>(p)[i] = v;
 }
 
-template <int WK, bool VEC, int NT>
-__global__ void __launch_bounds__(kLinThreads, 2) k_linear_q4(const __grid_constant__ LinearArgs a) {
-    using W = WTraits<WK>;
-    __shared__ float s_red[kLinWarps][4 * NT][32];
-    if (status_failed(a.ctl)) return;  // one word, the same for the whole CTA unless it is being set
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    // CTA -> (rank of a column-parallel call, block of row tiles, token tile); token tiles of one block
-    // are neighbours, so the second reads the block's weights from L2
-    uint32_t u = blockIdx.x;
-    const int tt = int(u % a.token_tiles);
-    u /= a.token_tiles;
-    const size_t blk = u % a.tile_blocks;
-    const int rank0 = a.row ? 0 : (a.view_rank >= 0 ? a.view_rank : int(u / a.tile_blocks));
-    const int per = kLinWarps / a.splits, split = warp % a.splits;
-    const size_t row0 = (blk * per + warp / a.splits) * 16;
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    if (row0 < a.N) {
-        const int cpr = int(a.K / W::kChunk);  // chunks of one rank's row
-        const int total = cpr * (a.row ? a.p : 1);
-        const int lo = int((long long)total * split / a.splits), hi = int((long long)total * (split + 1) / a.splits);
-        const size_t wrow = a.K / 2, srow = a.K >> a.group_shift;
-        const size_t r0 = row0 + g, r1 = row0 + g + 8;
-        for (int c = lo; c < hi;) {
-            const int q = c / cpr, rank = rank0 + q;
-            const int end = min(hi, (q + 1) * cpr);
-            LaneRows rows;
-            rows.w0 = r0 < a.N ? a.w[rank] + r0 * wrow : nullptr;
-            rows.w1 = r1 < a.N ? a.w[rank] + r1 * wrow : nullptr;
-            rows.s0 = a.scale[rank] + r0 * srow;
-            rows.s1 = a.scale[rank] + r1 * srow;
-            const uint16_t* x[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const size_t tok = size_t(tt) * (8 * NT) + n * 8 + g;
-                x[n] = tok < a.T ? a.x[rank] + tok * a.K : nullptr;
-            }
-            warp_product<WK, VEC, NT>(acc, rows, x, c - q * cpr, end - q * cpr, int(a.K), a.chunk_shift, t);
-            c = end;
-        }
+// Unit -> (rank of a column-parallel call, block of row tiles, token tile); token tiles of one block are
+// neighbours, so that the second reads the block's weights from L2.
+template <int WK, bool VEC, int MT, int NT> struct LinearJob {
+    static constexpr int kWK = WK, kMT = MT;
+    static constexpr bool kVecW = true, kVecX = VEC;
+    const LinearArgs& a;
+    int K, segments, splits, chunk_shift;
+
+    struct At { int rank; size_t row0, token0; };  // of the unit's first segment
+    __device__ __forceinline__ At at(int u) const {
+        At x;
+        x.token0 = size_t(uint32_t(u) % a.token_tiles) * (8 * NT);
+        const uint32_t b = uint32_t(u) / a.token_tiles;
+        x.row0 = size_t(b % a.tile_blocks) * (kProdWarps / splits) * (16 * MT);
+        x.rank = a.row ? 0 : a.view_rank >= 0 ? a.view_rank : int(b / a.tile_blocks);
+        return x;
     }
+    __device__ __forceinline__ size_t row_at(const At& x, int tile, int r) const {  // rows past the end: the last one
+        return min(x.row0 + tile * (16 * MT) + r, a.N - 1);
+    }
+    __device__ __forceinline__ void rows(int u, int seg, int tile, int g, const char* (&w)[MT][2]) const {
+        const At x = at(u);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_red[warp][4 * n + i][lane] = acc[n][i];
+            for (int i = 0; i < 2; ++i) w[m][i] = a.w[x.rank + seg] + row_at(x, tile, m * 16 + i * 8 + g) * (a.K / 2);
+    }
+    __device__ __forceinline__ void scales(int u, int seg, int tile, int g, int t, const uint16_t* (&s)[(MT + 1) / 2]) const {
+        const At x = at(u);
+#pragma unroll
+        for (int q = 0; q < (MT + 1) / 2; ++q)
+            s[q] = a.scale[x.rank + seg] +
+                   row_at(x, tile, (2 * q + (MT > 1 ? t / 2 : 0)) * 16 + t % 2 * 8 + g) * (a.K >> a.group_shift);
+    }
+    __device__ __forceinline__ const uint16_t* token(int u, int seg, int n) const {
+        const At x = at(u);
+        return x.token0 + n < a.T ? a.x[x.rank + seg] + (x.token0 + n) * a.K : nullptr;
+    }
+};
+
+template <int WK, bool VEC, int MT, int NT>
+__global__ void __launch_bounds__(kProdThreads, 2) k_linear_q4(const __grid_constant__ LinearArgs a) {
+    extern __shared__ __align__(128) unsigned char s_raw[];
+    __shared__ int s_fail;
+    const ProductSmem s = product_layout<MT>(s_raw);
+    if (threadIdx.x == 0) {
+        s_fail = status_failed(a.ctl);
+        init_panels(s);
+    }
     __syncthreads();
-    // every element of the CTA's tiles: the sum over its warps in order, stored to the ranks that get it
-    const int first = a.row ? (a.view_rank >= 0 ? a.view_rank : 0) : rank0;
-    const int last = a.row ? (a.view_rank >= 0 ? a.view_rank + 1 : a.p) : rank0 + 1;
-    for (int e = threadIdx.x; e < per * 16 * 8 * NT; e += kLinThreads) {
-        const int r = e % 16, tok = (e / 16) % (8 * NT), q = e / (16 * 8 * NT);
-        const size_t row = (blk * per + q) * 16 + r;
-        const size_t token = size_t(tt) * (8 * NT) + tok;
-        if (row >= a.N || token >= a.T) continue;
-        const int reg = 4 * (tok / 8) + (r / 8) * 2 + (tok & 1), ln = (r % 8) * 4 + (tok % 8) / 2;
-        float v = s_red[q * a.splits][reg][ln];
-        for (int s = 1; s < a.splits; ++s) v += s_red[q * a.splits + s][reg][ln];
-        for (int d = first; d < last; ++d) {
-            if (a.out_bf16) st_out<true>(a.out[d], token * a.N + row, v);
-            else st_out<false>(a.out[d], token * a.N + row, v);
-        }
+    if (s_fail) return;
+    using Job = LinearJob<WK, VEC, MT, NT>;
+    const Job job{a, int(a.K), a.row ? a.p : 1, a.splits, a.chunk_shift};
+    PanelCount pc;
+    if (threadIdx.x >= kProdWarps * 32) {
+        for (int u = blockIdx.x; u < a.units; u += gridDim.x)
+            if (!copy_tokens<NT>(job, a.ctl, a.timeout_ns, s, pc, u)) return;
+        return;
     }
+    Multiplier<Job> mul(job, s, blockIdx.x, a.units, gridDim.x);
+    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+        float acc[MT][NT][4];
+        if (!mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc)) break;
+        const typename Job::At x = job.at(u);
+        // stored to the ranks that get it
+        const int first = a.row ? (a.view_rank >= 0 ? a.view_rank : 0) : x.rank;
+        const int last = a.row ? (a.view_rank >= 0 ? a.view_rank + 1 : a.p) : x.rank + 1;
+        finish_unit<false, MT, NT>(s, a.splits, acc, [&](int tile, int r, int c, float v, float) {
+            const size_t row = x.row0 + tile * (16 * MT) + r, token = x.token0 + c;
+            if (row >= a.N || token >= a.T) return;
+            for (int d = first; d < last; ++d) {
+                if (a.out_bf16) st_out<true>(a.out[d], token * a.N + row, v);
+                else st_out<false>(a.out[d], token * a.N + row, v);
+            }
+        });
+    }
+    mul.drain();
 }
 
-template <int WK>
-static cudaError_t launch_linear_kind(LinearArgs& a, int nt, unsigned grid, cudaStream_t s) {
+template <int WK, int MT, int NT> static cudaError_t launch_linear_kind(const LinearArgs& a, int num_sms, cudaStream_t s) {
     auto go = [&](auto kernel) {
-        kernel<<<grid, kLinThreads, 0, s>>>(a);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem<MT>());
+        if (e != cudaSuccess) return e;
+        const unsigned grid = unsigned(std::min(a.units, 2 * num_sms));
+        kernel<<<grid, kProdThreads, product_smem<MT>(), s>>>(a);
         return cudaGetLastError();
     };
-    if (a.x_vec) return nt == 1 ? go(k_linear_q4<WK, true, 1>) : nt == 2 ? go(k_linear_q4<WK, true, 2>) : go(k_linear_q4<WK, true, 4>);
-    return nt == 1 ? go(k_linear_q4<WK, false, 1>) : nt == 2 ? go(k_linear_q4<WK, false, 2>) : go(k_linear_q4<WK, false, 4>);
+    return a.x_vec ? go(k_linear_q4<WK, true, MT, NT>) : go(k_linear_q4<WK, false, MT, NT>);
 }
 
 cudaError_t launch_linear(const LinearArgs& args, int num_sms, cudaStream_t s) {
     LinearArgs a = args;
     const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    const size_t tiles = (a.N + 15) / 16;
     a.token_tiles = uint32_t((a.T + 8 * nt - 1) / (8 * nt));
-    const size_t jobs = tiles * a.token_tiles * (a.row || a.view_rank >= 0 ? 1 : size_t(a.p));
-    // warps of a CTA on one row tile: more, the fewer tiles there are to fill the GPU with
-    int splits = 1;
-    while (splits < kLinWarps && jobs * splits < size_t(num_sms) * 8 * kLinWarps) splits *= 2;
-    a.splits = splits;
-    const size_t per = kLinWarps / splits;
-    a.tile_blocks = uint32_t((tiles + per - 1) / per);
-    const size_t ctas = size_t(a.tile_blocks) * a.token_tiles * (a.row || a.view_rank >= 0 ? 1 : size_t(a.p));
-    if (ctas > size_t(INT32_MAX)) return cudaErrorInvalidValue;
+    const size_t shards = a.row || a.view_rank >= 0 ? 1 : size_t(a.p);
+    // Row tiles of a warp: more use every staged token more often, and as many as fill the GPU's warps.
+    const size_t units = (a.N + 15) / 16 * a.token_tiles * shards, warps = size_t(num_sms) * 2 * kProdWarps;
+    const int mt = units * 4 >= warps ? 2 : 1;
+    const size_t tiles = (a.N + 16 * mt - 1) / (16 * mt), jobs = tiles * a.token_tiles * shards;
+    // warps of a CTA on one row tile: more, the fewer tiles there are
     const int group = 1 << a.group_shift;
+    const int stages = int(a.K / 128), panel = kPanelK / nt / 128;
+    int splits = 1;
+    while (splits < std::min(kProdWarps, panel) && splits * 2 <= stages && jobs * splits < size_t(num_sms) * 2 * kProdWarps)
+        splits *= 2;
+    a.splits = splits;
+    const size_t per = kProdWarps / splits;
+    const size_t blocks = (tiles + per - 1) / per, ctas = blocks * a.token_tiles * shards;
+    if (ctas > size_t(INT32_MAX) / 2) return cudaErrorInvalidValue;  // unit numbers step past the last by a grid
+    a.units = int(ctas);
+    a.tile_blocks = uint32_t(blocks);
     a.chunk_shift = 0;
     while ((128 << a.chunk_shift) < group) ++a.chunk_shift;
-    if (group >= 128) return launch_linear_kind<W_Q4X4>(a, nt, unsigned(ctas), s);
-    if (group == 64) return launch_linear_kind<W_Q4X2>(a, nt, unsigned(ctas), s);
-    return launch_linear_kind<W_Q4X1>(a, nt, unsigned(ctas), s);
+    auto kind = [&](auto wk) {
+        constexpr int WK = decltype(wk)::value;
+        if (mt == 1)
+            return nt == 1 ? launch_linear_kind<WK, 1, 1>(a, num_sms, s) : nt == 2 ? launch_linear_kind<WK, 1, 2>(a, num_sms, s)
+                                                                                : launch_linear_kind<WK, 1, 4>(a, num_sms, s);
+        return nt == 1 ? launch_linear_kind<WK, 2, 1>(a, num_sms, s) : nt == 2 ? launch_linear_kind<WK, 2, 2>(a, num_sms, s)
+                                                                            : launch_linear_kind<WK, 2, 4>(a, num_sms, s);
+    };
+    if (group >= 128) return kind(std::integral_constant<int, W_Q4X4>());
+    if (group == 64) return kind(std::integral_constant<int, W_Q4X2>());
+    return kind(std::integral_constant<int, W_Q4X1>());
 }
 
 }  // namespace simcomm

@@ -12,10 +12,12 @@
 // CTA each; the last part to finish joins them all. Bound by the scores' bytes, then, for 2-byte scores,
 // by the one exponential per score.
 //
-// Alternatives: each warp keeps its n best as 64-bit keys (the score's order, then the complement of the
-// column, so that the lower column wins among equals), one per lane, sorted. A vector whose maximum does
-// not pass the n-th key is dismissed by one comparison; the warps of a CTA share the highest n-th score
-// found, below which no score can matter.
+// Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
+// column wins among equals. The scan itself keeps nothing for them but each thread's maximum, which it has
+// anyway: the n-th largest of the CTA's 256 maxima is a bound that n scores reach, so only threads whose maximum
+// reaches it can hold one of the n best. There are n of them, ties aside, and their n / 256 of the columns are
+// read again, the scores that reach the bound gathered in shared memory and sorted out. If more do than it
+// holds (many equal scores), all columns are gone through again with a sorted list of the n best per warp.
 //
 // The exponentials are powers of two, 2^(x log2e - B) with B = M log2e rounded to fp32, so that a score
 // costs one fused multiply-add and one ex2: S and U refer to B, and the rounding of B is put back at the
@@ -34,6 +36,7 @@ namespace simcomm {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpUnroll = 4;            // 16-byte loads in flight per thread
+constexpr int kLpGather = 768;          // keys of scores that passed the bound
 constexpr float kLpLog2e = 1.4426950408889634f;
 constexpr float kLpLn2 = 0.6931471805599453f;
 constexpr float kLpFloor = -0x1p100f;   // scores below count as this in the sums (x log2e is exact at a power of two)
@@ -68,9 +71,22 @@ __device__ __forceinline__ Stat stat_join(const Stat& a, const Stat& b) {
     r.raw = max_nan(a.raw, b.raw);
     return r;
 }
-__device__ __forceinline__ Stat stat_shfl_xor(const Stat& a, int d) {
-    return Stat{__shfl_xor_sync(0xffffffffu, a.m, d), __shfl_xor_sync(0xffffffffu, a.s, d),
-                __shfl_xor_sync(0xffffffffu, a.u, d), __shfl_xor_sync(0xffffffffu, a.raw, d)};
+// The join of a warp's lanes, on every lane: all relative to the largest maximum, then plain sums.
+__device__ __forceinline__ Stat stat_warp(Stat a) {
+    float m = a.m, raw = a.raw;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        raw = max_nan(raw, __shfl_xor_sync(0xffffffffu, raw, d));
+    }
+    const float da = log2_base(a.m) - log2_base(m), fa = ex2(da);
+    float s = a.s * fa, u = __fmaf_rn(s, da, a.u * fa);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, d);
+        u += __shfl_xor_sync(0xffffffffu, u, d);
+    }
+    return Stat{m, s, u, raw};
 }
 
 __device__ __forceinline__ uint32_t score_order(float x) {
@@ -87,7 +103,6 @@ __device__ __forceinline__ unsigned long long top_key(float x, uint32_t col) {
 // A warp's n best keys, one per lane, largest in lane 0; nth: the n-th (0 while fewer are held).
 struct TopList {
     unsigned long long mine, nth;
-    float nth_score;
 };
 
 // Takes every lane's key (0: none) into the warp's list; whether the list changed (the same for every lane).
@@ -109,101 +124,229 @@ __device__ __forceinline__ bool top_insert(TopList& l, unsigned long long key, i
     return changed;
 }
 
-// Offers every lane's `cnt` scores at columns col, col + 1, ... to the warp's list. Warp-collective.
-template <int L>
-__device__ __forceinline__ void top_offer(TopList& l, const float (&x)[L], int cnt, uint32_t col, int n, uint32_t* s_nth) {
-    const int lane = threadIdx.x & 31;
-    bool changed = false;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const unsigned long long key = (j < cnt && x[j] == x[j]) ? top_key(x[j], col + j) : 0ull;
-        changed |= top_insert(l, key, n);
-    }
-    if (changed && l.nth) {
-        l.nth_score = order_score(uint32_t(l.nth >> 32));
-        if (lane == 0) atomicMax(s_nth, uint32_t(l.nth >> 32));
+// What a CTA knows of its best scores.
+struct TopShared {
+    uint32_t bound;   // order of a score that n of the CTA reach
+    uint32_t count;   // keys gathered (more than kLpGather: some were dropped)
+    uint32_t max[kLpThreads];       // order of each thread's maximum, 0: none, all ones: it met a NaN
+    uint32_t threads;               // threads that reach the bound
+    uint8_t thread[kLpThreads];
+    unsigned long long key[kLpGather];
+};
+
+__device__ __forceinline__ void top_gather(TopShared& top, float x, uint32_t col) {
+    if (x == x && score_order(x) >= top.bound) {
+        const uint32_t at = atomicAdd(&top.count, 1u);
+        if (at < uint32_t(kLpGather)) top.key[at] = top_key(x, col);
     }
 }
 
-// Adds `x` (missing scores are -inf) to a thread's sums.
-template <int L> __device__ __forceinline__ float stat_feed(Stat& st, const float (&x)[L]) {
-    float top = x[0];
+// The n-th largest of the keys that the warp's lanes hold (0: none), by n rounds of "largest that is left".
+template <int N> __device__ __forceinline__ uint32_t warp_nth(uint32_t (&key)[N], int n) {
+    uint32_t m = 0u;
+    for (int i = 0; i < n; ++i) {
+        uint32_t best = key[0];
 #pragma unroll
-    for (int j = 1; j < L; ++j) top = max_nan(top, x[j]);
-    st.raw = max_nan(st.raw, top);
-    if (!(top <= st.m)) {  // larger, or NaN
-        const float m = top == INFINITY ? __int_as_float(0x7fffffff) : top;
-        const float d = log2_base(st.m) - log2_base(m), f = ex2(d);
-        st.u = __fmaf_rn(st.s * f, d, st.u * f);
-        st.s *= f;
-        st.m = m;
-    }
-    const float base = log2_base(st.m);
+        for (int j = 1; j < N; ++j) best = max(best, key[j]);
+        m = __reduce_max_sync(0xffffffffu, best);
+        const unsigned who = __ballot_sync(0xffffffffu, best == m);
+        if ((threadIdx.x & 31) == __ffs(who) - 1) {
+            bool gone = false;
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const float d = __fmaf_rn(fmaxf(x[j], kLpFloor), kLpLog2e, -base);
-        const float e = ex2(d);
-        st.s += e;
-        st.u = __fmaf_rn(e, d, st.u);
-    }
-    return top;
-}
-
-template <int DT, bool TOP>
-__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, size_t v0, size_t v1, Stat& st, TopList& l,
-                                             uint32_t* s_nth) {
-    using P = Pack16<DT>;
-    constexpr int L = P::L, D = Elem<DT>::kBytes;
-    auto offer = [&](const float (&x)[L], float top, int cnt, uint32_t col) {
-        if constexpr (TOP) {
-            const bool may = cnt > 0 && (l.nth == 0ull || (top > l.nth_score && score_order(top) >= *(volatile uint32_t*)s_nth) ||
-                                         top != top);
-            if (__any_sync(0xffffffffu, may)) top_offer<L>(l, x, cnt, col, a.n_top, s_nth);
+            for (int j = 0; j < N; ++j)
+                if (!gone && key[j] == m) {
+                    key[j] = 0u;
+                    gone = true;
+                }
         }
-    };
-    for (size_t v = v0; v < v1;) {
-        const size_t r = v / a.m, end = min(v1, (r + 1) * a.m);
-        const char* base = static_cast<const char*>(a.logits[r]) + (row * a.ld + (v - r * a.m)) * D;
-        const size_t n = end - v;
-        const size_t head = min(n, size_t((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / D);
-        const size_t vecs = (n - head) / L, tail = n - head - vecs * L;
-        // less than a vector at either end, one score per lane of the first warp. A warp meets its scores in
-        // column order, so a later one that only equals its n-th best does not belong in its list.
-        auto ends = [&](size_t from, size_t count) {
-            if (count == 0 || threadIdx.x >= 32) return;
-            const int cnt = threadIdx.x < count ? 1 : 0;
-            float x[L];
+    }
+    return m;
+}
+
+// Two fp32 values in a 64-bit register, for the two-at-a-time arithmetic of sm_100.
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A thread's running sums, two lanes of each.
+struct Feed {
+    float m, raw;
+    unsigned long long s, u;
+};
+__device__ __forceinline__ Feed feed_none() { return Feed{kLpFloor, -INFINITY, 0ull, 0ull}; }
+__device__ __forceinline__ Stat feed_stat(const Feed& f) {
+    float s0, s1, u0, u1;
+    unpack2(f.s, s0, s1);
+    unpack2(f.u, u0, u1);
+    return Stat{f.m, s0 + s1, u0 + u1, f.raw};
+}
+
+// Adds one 16-byte vector of scores to a thread's sums.
+template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uint4& v) {
+    constexpr int L = 16 / Elem<DT>::kBytes;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[L], top;
+    if constexpr (DT == COLL_BF16) {  // maximum and clamp on pairs
+        const uint32_t p = max_nan_bf16x2(max_nan_bf16x2(w[0], w[1]), max_nan_bf16x2(w[2], w[3]));
+        top = max_nan(bf16_bits_to_float(p), __uint_as_float(p & 0xffff0000u));
+        constexpr uint32_t kFloor2 = 0xF180F180u;  // kLpFloor twice
 #pragma unroll
-            for (int j = 0; j < L; ++j) x[j] = -INFINITY;
-            if (cnt) x[0] = load_elem<DT>(base, from + threadIdx.x);
-            const float top = stat_feed<L>(st, x);
-            offer(x, top, cnt, uint32_t(v + from + threadIdx.x));
-        };
-        ends(0, head);
-        const char* body = base + head * D;
-        for (size_t i0 = 0; i0 < vecs; i0 += kLpThreads * kLpUnroll) {
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t c = max_nan_bf16x2(w[q], kFloor2);
+            x[2 * q] = bf16_bits_to_float(c);
+            x[2 * q + 1] = __uint_as_float(c & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = __uint_as_float(w[q]);
+        top = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = fmaxf(x[q], kLpFloor);
+    }
+    f.raw = max_nan(f.raw, top);
+    if (!(top <= f.m)) {  // larger, or NaN
+        const float m = top == INFINITY ? __int_as_float(0x7fffffff) : top;
+        const float d = log2_base(f.m) - log2_base(m), scale = ex2(d);
+        const unsigned long long dd = pack2(d, d), ss = pack2(scale, scale), zero = 0ull;
+        f.s = fma2(f.s, ss, zero);
+        f.u = fma2(f.s, dd, fma2(f.u, ss, zero));
+        f.m = m;
+    }
+    const float base = -log2_base(f.m);
+    const unsigned long long bb = pack2(base, base), ll = pack2(kLpLog2e, kLpLog2e);
+#pragma unroll
+    for (int q = 0; q < L; q += 2) {
+        const unsigned long long d = fma2(pack2(x[q], x[q + 1]), ll, bb);
+        float d0, d1;
+        unpack2(d, d0, d1);
+        const unsigned long long e = pack2(ex2(d0), ex2(d1));
+        f.s = add2(f.s, e);
+        f.u = fma2(e, d, f.u);
+    }
+}
+
+// A shard's part of the columns [v, v1): how it lies in vectors.
+template <int DT> struct Piece {
+    static constexpr int L = Pack16<DT>::L, D = Elem<DT>::kBytes;
+    const char* base;             // column v
+    uint32_t end;                 // the next piece's first column
+    uint32_t head, vecs, tail;    // scores before the first whole vector, vectors, scores after the last
+    __device__ __forceinline__ Piece(const LogprobArgs& a, size_t row, uint32_t v, uint32_t v1) {
+        const uint32_t m = uint32_t(a.m), r = v / m;  // a vocabulary has fewer than 2^31 columns
+        end = min(v1, (r + 1) * m);
+        base = static_cast<const char*>(a.logits[r]) + (row * a.ld + (v - r * m)) * D;
+        const uint32_t n = end - v;
+        head = min(n, uint32_t((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / D);
+        vecs = (n - head) / L;
+        tail = n - head - vecs * L;
+    }
+    __device__ __forceinline__ const char* vector(uint32_t i) const { return base + size_t(head) * D + size_t(i) * 16; }
+    // Score k of the head + tail at the ends, and its place in the piece.
+    __device__ __forceinline__ uint32_t end_at(uint32_t k) const { return k < head ? k : k + vecs * L; }
+};
+
+// Calls take(raw vector, scores in it, column of the first) for all columns [v0, v1) of a row; vector i of a
+// piece falls to thread i modulo kLpThreads. Scores at the ends of pieces come as vectors of one score, one per
+// lane of the first warp; missing scores are -inf.
+template <int DT, typename Take>
+__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, Take take) {
+    constexpr int L = Pack16<DT>::L;
+    constexpr uint32_t kNone = DT == COLL_BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    const uint32_t warp0 = threadIdx.x & ~31u;
+    for (uint32_t v = v0; v < v1;) {
+        const Piece<DT> pc(a, row, v, v1);
+        if (pc.head + pc.tail && threadIdx.x < 32) {
+            const int cnt = threadIdx.x < pc.head + pc.tail ? 1 : 0;
+            const uint32_t at = pc.end_at(threadIdx.x);
+            uint4 raw = make_uint4(kNone, kNone, kNone, kNone);
+            if (cnt) {
+                if constexpr (DT == COLL_BF16) raw.x = (kNone & 0xffff0000u) | reinterpret_cast<const uint16_t*>(pc.base)[at];
+                else raw.x = reinterpret_cast<const uint32_t*>(pc.base)[at];
+            }
+            take(raw, cnt, v + at);
+        }
+        for (uint32_t i0 = 0; i0 < pc.vecs; i0 += kLpThreads * kLpUnroll) {
             uint4 raw[kLpUnroll];
 #pragma unroll
             for (int q = 0; q < kLpUnroll; ++q) {
-                const size_t i = i0 + q * kLpThreads + threadIdx.x;
-                if (i < vecs) raw[q] = ld_stream_v4(body + i * 16);
+                const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
+                raw[q] = i < pc.vecs ? ld_stream_v4(pc.vector(i)) : make_uint4(kNone, kNone, kNone, kNone);
             }
 #pragma unroll
             for (int q = 0; q < kLpUnroll; ++q) {
-                const size_t i = i0 + q * kLpThreads + threadIdx.x;
-                if (i0 + q * kLpThreads + (threadIdx.x & ~31u) >= vecs) break;  // none of this warp's
-                float x[L];
-#pragma unroll
-                for (int j = 0; j < L; ++j) x[j] = -INFINITY;
-                const int cnt = i < vecs ? L : 0;
-                if (cnt) P::unpack(raw[q], x);
-                const float top = stat_feed<L>(st, x);
-                offer(x, top, cnt, uint32_t(v + head + i * L));
+                const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
+                if (i0 + q * kLpThreads + warp0 >= pc.vecs) break;  // none of this warp's
+                take(raw[q], i < pc.vecs ? L : 0, v + pc.head + i * L);
             }
         }
-        ends(n - tail, tail);
-        v = end;
+        v = pc.end;
     }
+}
+
+// Gathers the scores that may be among the n best, given every thread's maximum in top.max. CTA-collective.
+template <int DT>
+__device__ __forceinline__ void gather_best(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, TopShared& top) {
+    using P = Pack16<DT>;
+    constexpr int L = P::L;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 0) {
+        uint32_t key[kLpWarps];
+#pragma unroll
+        for (int j = 0; j < kLpWarps; ++j) {
+            const uint32_t k = top.max[j * 32 + lane];
+            key[j] = k == 0xffffffffu ? 0u : k;  // behind a NaN a thread's maximum is not known
+        }
+        const uint32_t nth = warp_nth<kLpWarps>(key, a.n_top);  // 0: fewer than n threads have one
+        if (lane == 0) {
+            top.bound = nth;
+            top.count = top.threads = 0u;
+        }
+    }
+    __syncthreads();
+    if (top.max[threadIdx.x] >= top.bound) top.thread[atomicAdd(&top.threads, 1u)] = uint8_t(threadIdx.x);
+    __syncthreads();
+    const uint32_t nt = top.threads;
+    for (uint32_t v = v0; v < v1;) {
+        const Piece<DT> pc(a, row, v, v1);
+        if (threadIdx.x < pc.head + pc.tail) {
+            const uint32_t at = pc.end_at(threadIdx.x);
+            top_gather(top, load_elem<DT>(pc.base, at), v + at);
+        }
+        const uint32_t turns = (pc.vecs + kLpThreads - 1) / kLpThreads;
+        const int shift = turns > 1 ? 32 - __clz(turns - 1) : 0;  // turns as a power of two: no division by item
+        for (uint32_t w = threadIdx.x; w < nt << shift; w += kLpThreads) {
+            const uint32_t i = (w & ((1u << shift) - 1u)) * kLpThreads + top.thread[w >> shift];
+            if (i >= pc.vecs) continue;
+            float x[L];
+            P::unpack(ld_stream_v4(pc.vector(i)), x);
+            const uint32_t col = v + pc.head + i * L;
+#pragma unroll
+            for (int j = 0; j < L; ++j) top_gather(top, x[j], col + j);
+        }
+        v = pc.end;
+    }
+    __syncthreads();
 }
 
 __device__ __forceinline__ float score_at(const LogprobArgs& a, int dtype, size_t row, size_t v) {
@@ -250,76 +393,109 @@ __device__ __noinline__ float careful_log_sum(const LogprobArgs& a, int dtype, s
     return logf(s);
 }
 
+// The n best of the CTA's columns from a sorted list per warp, into key[0, kLpWarps * n), unsorted; the way
+// that takes any number of ties. CTA-collective.
+template <int DT>
+__device__ __noinline__ void top_by_lists(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, unsigned long long* key) {
+    constexpr int L = Pack16<DT>::L;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TopList l{0ull, 0ull};
+    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int cnt, uint32_t col) {
+        float x[L];
+        Pack16<DT>::unpack(raw, x);
+#pragma unroll
+        for (int j = 0; j < L; ++j) top_insert(l, j < cnt && x[j] == x[j] ? top_key(x[j], col + j) : 0ull, a.n_top);
+    });
+    __syncthreads();
+    if (lane < a.n_top) key[warp * a.n_top + lane] = l.mine;
+    __syncthreads();
+}
+
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constant__ LogprobArgs a) {
     __shared__ Stat s_stat[kLpWarps];
-    __shared__ unsigned long long s_key[kLpWarps * 32];
+    __shared__ TopShared s_top;
     __shared__ float s_w[kLpWarps];
-    __shared__ uint32_t s_nth;
     __shared__ int s_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t row = blockIdx.x / a.parts;
     const int part = int(blockIdx.x % a.parts);
-    if (threadIdx.x == 0) {
-        s_nth = 0u;
-        s_flag = status_failed(a.ctl);
-    }
+    if (threadIdx.x == 0) s_flag = status_failed(a.ctl);
     __syncthreads();
     if (s_flag) return;
-    const size_t v0 = a.V * part / a.parts, v1 = a.V * (part + 1) / a.parts;
-    Stat st = stat_none();
-    TopList l{0ull, 0ull, 0.0f};
-    scan_columns<DT, TOP>(a, row, v0, v1, st, l, &s_nth);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const Stat o = stat_shfl_xor(st, d);
-        st = (lane & d) ? stat_join(o, st) : stat_join(st, o);  // lower lane first: the same on both sides
-    }
+    const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
+    Feed f = feed_none();
+    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); });
+    if constexpr (TOP) s_top.max[threadIdx.x] = f.raw != f.raw ? 0xffffffffu : f.raw == -INFINITY ? 0u : score_order(f.raw);
+    Stat st = stat_warp(feed_stat(f));
     if (lane == 0) s_stat[warp] = st;
-    if constexpr (TOP)
-        if (lane < a.n_top) s_key[warp * a.n_top + lane] = l.mine;
     __syncthreads();
-    st = s_stat[0];
-    for (int w = 1; w < kLpWarps; ++w) st = stat_join(st, s_stat[w]);
-    const int nkeys = kLpWarps * a.n_top;
-    // the place of key i among the CTA's lists (keys are distinct but for 0, which names no score)
+    int nkeys = 0;
+    if constexpr (TOP) {
+        gather_best<DT>(a, row, v0, v1, s_top);
+        nkeys = int(s_top.count);
+        if (nkeys > kLpGather) {
+            top_by_lists<DT>(a, row, v0, v1, s_top.key);
+            nkeys = kLpWarps * a.n_top;
+        }
+    }
+    // the place of a key among the CTA's (keys are distinct but for 0, which names no score)
     auto place = [&](unsigned long long k) {
         int above = 0;
-        for (int q = 0; q < nkeys; ++q) above += s_key[q] > k;
+        for (int q = 0; q < nkeys; ++q) above += s_top.key[q] > k;
         return above;
+    };
+    // numbers among the keys; n at most counts
+    auto held = [&]() {
+        int n = 0;
+        for (int i = threadIdx.x; i < nkeys; i += kLpThreads) n += s_top.key[i] != 0ull;
+        return __syncthreads_count(n > 0) >= a.n_top ? a.n_top : min(a.n_top, int(cta_sum(float(n), s_w)));
     };
     if (a.parts > 1) {
         // the parts' results meet in scratch; the row's last CTA joins them in part order
         if constexpr (TOP) {
             unsigned long long* mine = a.part_keys + (row * a.parts + part) * a.n_top;
             for (int i = threadIdx.x; i < nkeys; i += kLpThreads) {
-                const unsigned long long k = s_key[i];
+                const unsigned long long k = s_top.key[i];
                 const int at = k ? place(k) : a.n_top;
                 if (at < a.n_top) mine[at] = k;
             }
-            const int held = __syncthreads_count(threadIdx.x < nkeys && s_key[threadIdx.x] != 0ull);
-            for (int i = held + int(threadIdx.x); i < a.n_top; i += kLpThreads) mine[i] = 0ull;
+            const int n = held();
+            for (int i = n + int(threadIdx.x); i < a.n_top; i += kLpThreads) mine[i] = 0ull;
         }
-        if (threadIdx.x == 0) a.part_stat[row * a.parts + part] = make_float4(st.m, st.s, st.u, st.raw);
+        if (threadIdx.x == 0) {
+            st = s_stat[0];
+            for (int w = 1; w < kLpWarps; ++w) st = stat_join(st, s_stat[w]);
+            a.part_stat[row * a.parts + part] = make_float4(st.m, st.s, st.u, st.raw);
+        }
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) s_flag = atomicAdd(&a.st->row_ctr[row], 1u) == uint32_t(a.parts - 1);
         __syncthreads();
         if (!s_flag) return;
         __threadfence();
-        st = stat_none();
-        for (int q = 0; q < a.parts; ++q) {
-            const float4 f = __ldcg(&a.part_stat[row * a.parts + q]);
-            st = stat_join(st, Stat{f.x, f.y, f.z, f.w});
-        }
         if (threadIdx.x == 0) a.st->row_ctr[row] = 0u;
+        if (warp == 0) {  // a lane's parts in order, then the lanes
+            st = stat_none();
+            for (int q = lane; q < a.parts; q += 32) {
+                const float4 v = __ldcg(&a.part_stat[row * a.parts + q]);
+                st = stat_join(st, Stat{v.x, v.y, v.z, v.w});
+            }
+            st = stat_warp(st);
+            if (lane == 0) s_stat[0] = st;
+        }
         if constexpr (TOP) {  // each warp joins its share of the parts' lists
-            l = TopList{0ull, 0ull, 0.0f};
+            TopList l{0ull, 0ull};
             for (int q = warp; q < a.parts; q += kLpWarps)
                 top_insert(l, lane < a.n_top ? __ldcg(a.part_keys + (row * a.parts + q) * a.n_top + lane) : 0ull, a.n_top);
-            if (lane < a.n_top) s_key[warp * a.n_top + lane] = l.mine;
-            __syncthreads();
+            if (lane < a.n_top) s_top.key[warp * a.n_top + lane] = l.mine;
+            nkeys = kLpWarps * a.n_top;
         }
+        __syncthreads();
+        st = s_stat[0];
+    } else {
+        st = s_stat[0];
+        for (int w = 1; w < kLpWarps; ++w) st = stat_join(st, s_stat[w]);
     }
     // P = e^((x - m) - ln_s)
     float m = st.m, ln_s, entropy;
@@ -349,7 +525,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     }
     if constexpr (TOP) {
         for (int i = threadIdx.x; i < nkeys; i += kLpThreads) {
-            const unsigned long long k = s_key[i];
+            const unsigned long long k = s_top.key[i];
             const int at = k ? place(k) : a.n_top;
             if (at >= a.n_top) continue;
             const float lp = log_prob(order_score(uint32_t(k >> 32)));
@@ -359,8 +535,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
             }
         }
         // fewer scores than n are numbers: the places left name no column
-        const int held = __syncthreads_count(threadIdx.x < nkeys && s_key[threadIdx.x] != 0ull);
-        for (int i = held + int(threadIdx.x); i < a.n_top; i += kLpThreads)
+        const int n = held();
+        for (int i = n + int(threadIdx.x); i < a.n_top; i += kLpThreads)
             for (int r = first; r < last; ++r) {
                 a.top_idx[r][row * a.n_top + i] = -1;
                 a.top_logprob[r][row * a.n_top + i] = __int_as_float(0x7fffffff);
@@ -370,15 +546,49 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
 
 // ---- gradient ------------------------------------------------------------------------------------
 
+// With d = x log2e - B, B = (m + ln_s) log2e rounded: P = 2^d c, c = 2^-(what the rounding of B left out), and
+// ln P = d ln 2 + ln c. So dx = -P (gl + ge (ln P + H)) = 2^d (a0 + a1 d), two constants of the row.
 struct RowGrad {
-    float m, ln_s;  // P = e^((x - m) - ln_s): the stored lse and 0, or the row's maximum and its sum's logarithm
-    float gl, ge, entropy;
+    float base, a0, a1;
 };
-__device__ __forceinline__ float grad_of(const RowGrad& g, float x) {
-    const float lp = (x - g.m) - g.ln_s;
-    const float prob = ex2(lp * kLpLog2e);
-    // dx / P = -(gl + ge (ln P + H)); a score of probability 0 has no gradient, whatever its logarithm
-    return prob > 0.0f ? -prob * __fmaf_rn(g.ge, lp + g.entropy, g.gl) : prob == 0.0f ? 0.0f : prob;
+__device__ __forceinline__ RowGrad row_grad(float m, float ln_s, float gl, float ge, float entropy) {
+    RowGrad g;
+    const float b_m = m * kLpLog2e, b_s = ln_s * kLpLog2e;
+    g.base = b_m + b_s;
+    // the sum's rounding, then the products'
+    const float sum_lo = (b_m - g.base) + b_s;
+    const float lo = sum_lo + __fmaf_rn(m, kLpLog2e, -b_m) + __fmaf_rn(ln_s, kLpLog2e, -b_s);
+    const float c = exp2f(-lo);
+    g.a0 = -c * (gl + ge * (entropy - lo * kLpLn2));
+    g.a1 = -c * ge * kLpLn2;
+    return g;
+}
+// The gradients of a vector of scores, without the given token's own term.
+template <int DT> __device__ __forceinline__ uint4 grad_vector(const RowGrad& g, const uint4& v) {
+    constexpr int L = Pack16<DT>::L;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float x[L];
+    if constexpr (DT == COLL_BF16) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t c = max_nan_bf16x2(w[q], 0xF180F180u);  // kLpFloor: a masked score's 2^d is 0 and d finite
+            x[2 * q] = bf16_bits_to_float(c);
+            x[2 * q + 1] = __uint_as_float(c & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = max_nan(__uint_as_float(w[q]), kLpFloor);
+    }
+    const unsigned long long ll = pack2(kLpLog2e, kLpLog2e), bb = pack2(-g.base, -g.base), a0 = pack2(g.a0, g.a0),
+                             a1 = pack2(g.a1, g.a1), zero = 0ull;
+#pragma unroll
+    for (int q = 0; q < L; q += 2) {
+        const unsigned long long d = fma2(pack2(x[q], x[q + 1]), ll, bb);
+        float d0, d1;
+        unpack2(d, d0, d1);
+        unpack2(fma2(pack2(ex2(d0), ex2(d1)), fma2(a1, d, a0), zero), x[q], x[q + 1]);
+    }
+    return Pack16<DT>::pack(x);
 }
 
 template <int DT>
@@ -399,40 +609,41 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_grad(const __grid_const
     const size_t all = v0 < a.V ? min(a.m, a.V - v0) : 0;                  // its columns; the rest is padding
     const char* in = static_cast<const char*>(a.logits[r]) + row * a.ld * D;
     char* out = static_cast<char*>(a.grad_logits[r]) + row * a.ld_grad * D;
-    RowGrad g;
-    g.m = a.lse_in[r][row];
-    g.ln_s = 0.0f;
-    g.ge = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
-    g.entropy = a.grad_entropy ? a.entropy_in[r][row] : 0.0f;
+    float m = a.lse_in[r][row], ln_s = 0.0f;
+    const float ge = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
+    float entropy = a.grad_entropy ? a.entropy_in[r][row] : 0.0f;
     const int tok = a.tokens[row];
     if ((tok < -1 || (tok >= 0 && size_t(tok) >= a.V)) && threadIdx.x == 0) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
-    g.gl = tok >= 0 ? a.grad_logprob[row] : 0.0f;
-    const bool none = g.m == -INFINITY;  // a row without a distribution: zeros whatever its scores
-    if (!none && !(fabsf(g.m) <= kLpFar)) {  // an fp32 lse that far out has lost the sum: take it again
+    const float gl = tok >= 0 ? a.grad_logprob[row] : 0.0f;
+    const bool none = m == -INFINITY;  // a row without a distribution: zeros whatever its scores
+    if (!none && !(fabsf(m) <= kLpFar)) {  // an fp32 lse that far out has lost the sum: take it again
         __shared__ float s_w[kLpWarps];
-        float top = -INFINITY, entropy;
+        float top = -INFINITY, h;
         for (size_t v = threadIdx.x; v < a.V; v += kLpThreads) top = max_nan(top, score_at(a, DT, row, v));
-        g.m = cta_max(top, s_w);
-        g.ln_s = careful_log_sum(a, DT, row, g.m, &entropy, s_w);
-        g.entropy = a.grad_entropy ? entropy : 0.0f;
+        m = cta_max(top, s_w);
+        ln_s = careful_log_sum(a, DT, row, m, &h, s_w);
+        if (a.grad_entropy) entropy = h;
     }
-    const size_t own = tok >= 0 && size_t(tok) >= v0 && size_t(tok) < v0 + all && !none && g.gl != 0.0f ? size_t(tok) - v0 : SIZE_MAX;
+    const bool far = !(fabsf(m) <= kLpFar);  // the scores' differences from m need more than a fused product
+    const RowGrad g = row_grad(m, ln_s, gl, ge, entropy);
+    const size_t own = tok >= 0 && size_t(tok) >= v0 && size_t(tok) < v0 + all && !none && gl != 0.0f ? size_t(tok) - v0 : SIZE_MAX;
     const size_t have = none ? 0 : all;
     const size_t c0 = a.m * piece / a.parts, c1 = a.m * (piece + 1) / a.parts;
-    auto value = [&](size_t c, float x) {
-        float d = c < have ? grad_of(g, x) : 0.0f;
-        if (c == own) d += g.gl;
-        return d;
+    auto value = [&](size_t c) {  // one column's gradient
+        if (c >= have) return 0.0f;
+        const float x = load_elem<DT>(in, c), lp = (x - m) - ln_s, prob = ex2(lp * kLpLog2e);
+        const float d = prob > 0.0f ? -prob * __fmaf_rn(ge, lp + entropy, gl) : prob == 0.0f ? 0.0f : prob;
+        return c == own ? d + gl : d;
     };
     const uintptr_t ia = reinterpret_cast<uintptr_t>(in + c0 * D), oa = reinterpret_cast<uintptr_t>(out + c0 * D);
-    const bool together = ((ia ^ oa) & 15) == 0;  // 16-byte boundaries fall on the same columns
+    const bool together = ((ia ^ oa) & 15) == 0 && !far;  // 16-byte boundaries fall on the same columns
     const size_t n = c1 - c0;
     const size_t head = together ? min(n, size_t((16 - (ia & 15)) & 15) / D) : n;
-    const size_t vecs = together ? (n - head) / L : 0, tail = n - head - vecs * L;
-    for (size_t i = threadIdx.x; i < head + tail; i += kLpThreads) {
+    // whole vectors of the shard's own columns; what is left of them and the padding go one by one
+    const size_t vecs = together && have > c0 + head ? (min(c1, have) - c0 - head) / L : 0, rest = n - head - vecs * L;
+    for (size_t i = threadIdx.x; i < head + rest; i += kLpThreads) {
         const size_t c = c0 + (i < head ? i : i + vecs * L);
-        const float x = c < have ? load_elem<DT>(in, c) : 0.0f;
-        store_elem<DT>(out, c, value(c, x));
+        store_elem<DT>(out, c, value(c));
     }
     const size_t body = c0 + head;
     for (size_t i0 = 0; i0 < vecs; i0 += kLpThreads * kLpUnroll) {
@@ -447,16 +658,8 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs_grad(const __grid_const
             const size_t i = i0 + q * kLpThreads + threadIdx.x;
             if (i >= vecs) break;
             const size_t c = body + i * L;
-            float x[L];
-            P::unpack(raw[q], x);
-#pragma unroll
-            for (int j = 0; j < L; ++j) x[j] = c + j < have ? grad_of(g, x[j]) : 0.0f;
-            if (own - c < size_t(L)) {
-#pragma unroll
-                for (int j = 0; j < L; ++j)
-                    if (own == c + j) x[j] += g.gl;
-            }
-            st_v4(out + c * D, P::pack(x));
+            st_v4(out + c * D, grad_vector<DT>(g, raw[q]));
+            if (own - c < size_t(L)) store_elem<DT>(out, own, value(own));
         }
     }
 }

@@ -17,18 +17,17 @@
 //      sum rounded to fp32 as in the combine, rounded once.
 // Bound by the bytes of the picked experts' weights; the warp-level product is in wprod.cuh.
 #include <algorithm>
+#include <type_traits>
 
 #include "wprod.cuh"
 
 namespace simcomm {
 
-constexpr int kLayWarps = 8;
-constexpr int kLayThreads = kLayWarps * 32;
 constexpr int kLayTokens = 32;  // assignments of an expert that one unit covers
 
-__device__ __forceinline__ bool layer_barrier(const MoeLayerArgs& a, uint32_t k) {
+__device__ __forceinline__ bool layer_barrier(const MoeLayerArgs& a, uint32_t k, bool ok) {
     __shared__ int s_ok;
-    __syncthreads();
+    if (!__syncthreads_and(ok)) return false;  // a wait ran out: the status is set
     if (threadIdx.x == 0) {
         red_release_add_gpu(&a.st->layer_ctr, 1u);
         const uint32_t want = k * gridDim.x;
@@ -57,7 +56,8 @@ __device__ __forceinline__ int warp_incl_sum(int v, int lane) {
 
 // Exclusive prefix over the CTA of three counts per thread; their totals in tot.
 __device__ __forceinline__ void cta_prefix3(int (&v)[3], int (&tot)[3]) {
-    __shared__ int s_w[3][kLayWarps];
+    constexpr int kWarps = kProdThreads / 32;
+    __shared__ int s_w[3][kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int incl[3];
 #pragma unroll
@@ -70,7 +70,7 @@ __device__ __forceinline__ void cta_prefix3(int (&v)[3], int (&tot)[3]) {
     for (int q = 0; q < 3; ++q) {
         int before = 0;
         tot[q] = 0;
-        for (int w = 0; w < kLayWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += s_w[q][w];
             tot[q] += s_w[q][w];
         }
@@ -83,10 +83,10 @@ __device__ __forceinline__ void cta_prefix3(int (&v)[3], int (&tot)[3]) {
 __device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const LayerLists& l) {
     __shared__ int s_bad;
     const int per = int(a.T) * a.k;
-    for (int e = threadIdx.x; e < a.E; e += kLayThreads) l.offset[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += kProdThreads) l.offset[e] = 0;
     if (threadIdx.x == 0) s_bad = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.A; i += kLayThreads) {
+    for (int i = threadIdx.x; i < a.A; i += kProdThreads) {
         const int e = a.idx[a.rank0 + i / per][i % per];
         if (e < 0 || e >= a.E) s_bad = 1;
         else atomicAdd(&l.offset[e], 1);
@@ -96,7 +96,7 @@ __device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const Lay
         if (threadIdx.x == 0) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
         return -1;
     }
-    const int share = (a.E + kLayThreads - 1) / kLayThreads;
+    const int share = (a.E + kProdThreads - 1) / kProdThreads;
     const int e0 = min(a.E, int(threadIdx.x) * share), e1 = min(a.E, e0 + share);
     int v[3] = {0, 0, 0}, tot[3];
     for (int e = e0; e < e1; ++e) {
@@ -122,18 +122,18 @@ __device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const Lay
         l.act_tile[tot[0]] = tot[2];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.A; i += kLayThreads)
+    for (int i = threadIdx.x; i < a.A; i += kProdThreads)
         l.list[atomicAdd(&l.offset[a.idx[a.rank0 + i / per][i % per]], 1)] = uint16_t(i);
     __syncthreads();
     // The atomics leave an expert's assignments in an order that differs from CTA to CTA. That does not
     // matter inside one token tile (an assignment's result does not depend on its column), but every CTA
     // must cut an expert's assignments into the same tiles: those with more than one are put in order, a
     // warp per expert, by a bitmap of the assignments.
-    __shared__ uint32_t s_bits[kLayWarps][kLayerMaxAssignments / 32];
+    __shared__ uint32_t s_bits[kProdThreads / 32][kLayerMaxAssignments / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t* bits = s_bits[warp];
     constexpr int kWords = kLayerMaxAssignments / 32 / 32;  // bitmap words per lane
-    for (int q = warp; q < tot[0]; q += kLayWarps) {
+    for (int q = warp; q < tot[0]; q += kProdThreads / 32) {
         const int start = l.act_start[q], n = l.act_start[q + 1] - start;
         if (n <= kLayTokens) continue;
         for (int w = lane; w < kLayerMaxAssignments / 32; w += 32) bits[w] = 0u;
@@ -154,127 +154,148 @@ __device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const Lay
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
-// One unit of phase 1 (UP) or 2: up to 8 NT assignments of one expert against the CTA's row tiles.
-template <int WK, bool VEC, int NT, bool UP>
-__device__ __forceinline__ void layer_unit(const MoeLayerArgs& a, const LayerLists& l, float* s_red, int e, int first,
-                                           int count, int blk) {
-    using W = WTraits<WK>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int splits = UP ? a.splits_up : a.splits_down, per = kLayWarps / splits, split = warp % splits;
-    const int K = UP ? a.H : a.F, rows = UP ? a.F : a.H, tile_rows = UP ? 8 : 16;
-    const int rank = e / a.E_loc, el = e % a.E_loc;
-    const int row0 = (blk * per + warp / splits) * tile_rows;
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    if (row0 < rows) {
-        const int chunks = (K + W::kChunk - 1) / W::kChunk;
-        const int lo = int((long long)chunks * split / splits), hi = int((long long)chunks * (split + 1) / splits);
-        const size_t wrow = W::kQ4 ? size_t(K) / 2 : size_t(K) * 2;
-        const size_t base = size_t(el) * (UP ? 2 * a.F : a.H);
-        const size_t r0 = base + row0 + g, r1 = UP ? r0 + a.F : r0 + 8;
-        const bool in0 = row0 + g < rows, in1 = UP ? in0 : row0 + g + 8 < rows;
-        const char* w = UP ? a.up[rank] : a.down[rank];
-        LaneRows lr;
-        lr.w0 = in0 ? w + r0 * wrow : nullptr;
-        lr.w1 = in1 ? w + r1 * wrow : nullptr;
-        lr.s0 = lr.s1 = nullptr;
-        if constexpr (W::kQ4) {
-            const uint16_t* sc = UP ? a.up_scale[rank] : a.down_scale[rank];
-            const size_t srow = size_t(K) >> a.group_shift;
-            lr.s0 = sc + r0 * srow;
-            lr.s1 = sc + r1 * srow;
-        }
-        const uint16_t* x[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int c = n * 8 + g;
-            x[n] = nullptr;
-            if (c < count) {
-                const int asg = l.list[first + c];
-                if constexpr (UP) {
-                    const int tok = asg / a.k;
-                    x[n] = a.x[a.rank0 + tok / int(a.T)] + size_t(tok % int(a.T)) * a.H;
-                } else {
-                    x[n] = a.h + size_t(asg) * a.h_stride;
-                }
-            }
-        }
-        warp_product<WK, VEC, NT>(acc, lr, x, lo, hi, K, a.chunk_shift, t);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_red[(warp * 4 * NT + 4 * n + i) * 32 + lane] = acc[n][i];
-    __syncthreads();
-    for (int x = threadIdx.x; x < per * tile_rows * 8 * NT; x += kLayThreads) {
-        const int r = x % tile_rows, c = (x / tile_rows) % (8 * NT), q = x / (tile_rows * 8 * NT);
-        const int row = (blk * per + q) * tile_rows + r;
-        if (row >= rows || c >= count) continue;
-        const int asg = l.list[first + c];
-        const int ln = (r % 8) * 4 + (c % 8) / 2, reg = 4 * (c / 8) + (c & 1) + (r / 8) * 2;
-        float v = 0.0f, v2 = 0.0f;
-        for (int s = 0; s < splits; ++s) {
-            const float* red = s_red + (q * splits + s) * 4 * NT * 32 + ln;
-            v += red[reg * 32];
-            if (UP) v2 += red[(reg + 2) * 32];
-        }
-        if constexpr (UP) a.h[size_t(asg) * a.h_stride + row] = float_to_bf16_bits(silu_mul(v, v2));
-        else a.y[size_t(asg) * a.H + row] = v;
-    }
-    __syncthreads();  // the next unit writes s_red
-}
+// The units of phase 1 (UP) or 2: (picked expert, block of row tiles, up to 32 of its assignments). A warp's
+// two row tiles hold rows f..f+7 of G in their upper and of U in their lower halves (UP), or 32 rows of D.
+constexpr int kLayTiles = 2;
 
-template <int WK, bool VEC, bool UP>
-__device__ __forceinline__ void layer_phase(const MoeLayerArgs& a, const LayerLists& l, float* s_red, int nact) {
-    const int blocks = UP ? a.blocks_up : a.blocks_down;
-    const int units = l.act_tile[nact] * blocks;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+template <int WK, bool VEC, bool UP> struct LayerJob {
+    static constexpr int kWK = WK, kMT = kLayTiles;
+    static constexpr bool kVecW = WTraits<WK>::kQ4 || VEC, kVecX = VEC;
+    static constexpr int kTile = (UP ? 8 : 16) * kMT;  // rows of the output in a group of row tiles
+    const MoeLayerArgs& a;
+    const LayerLists& l;
+    int nact;
+    int K, segments, splits, chunk_shift, rows_all, blocks;
+
+    __device__ __forceinline__ LayerJob(const MoeLayerArgs& a_, const LayerLists& l_, int nact_)
+        : a(a_), l(l_), nact(nact_), K(UP ? a_.H : a_.F), segments(1), splits(UP ? a_.splits_up : a_.splits_down),
+          chunk_shift(a_.chunk_shift), rows_all(UP ? a_.F : a_.H), blocks(UP ? a_.blocks_up : a_.blocks_down) {}
+
+    __device__ __forceinline__ int units() const { return l.act_tile[nact] * blocks; }
+    struct At { int e, row0, first, count; };
+    __device__ __forceinline__ At at(int u) const {
         int lo = 0, hi = nact - 1;  // the last picked expert whose units start at or before u
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (l.act_tile[mid] * blocks <= u) lo = mid;
             else hi = mid - 1;
         }
-        const int tiles = l.act_tile[lo + 1] - l.act_tile[lo];
-        const int rel = u - l.act_tile[lo] * blocks;
-        const int blk = rel / tiles, tile = rel % tiles;
-        const int first = l.act_start[lo] + tile * kLayTokens;
-        const int count = min(kLayTokens, l.act_start[lo + 1] - first);
-        const int e = l.act[lo];
-        if (count <= 8) layer_unit<WK, VEC, 1, UP>(a, l, s_red, e, first, count, blk);
-        else if (count <= 16) layer_unit<WK, VEC, 2, UP>(a, l, s_red, e, first, count, blk);
-        else layer_unit<WK, VEC, 4, UP>(a, l, s_red, e, first, count, blk);
+        const int tiles = l.act_tile[lo + 1] - l.act_tile[lo], rel = u - l.act_tile[lo] * blocks;
+        At x;
+        x.e = l.act[lo];
+        x.row0 = rel / tiles * (kProdWarps / splits) * kTile;
+        x.first = l.act_start[lo] + rel % tiles * kLayTokens;
+        x.count = min(kLayTokens, l.act_start[lo + 1] - x.first);
+        return x;
     }
+    // Row g of the upper (i = 0) or lower half of the m-th row tile; rows past the end: the last one.
+    __device__ __forceinline__ size_t row_at(const At& x, int tile, int m, int i, int g) const {
+        const int r = min(x.row0 + tile * kTile + (UP ? m * 8 : m * 16 + i * 8) + g, rows_all - 1);
+        return size_t(x.e % a.E_loc) * (UP ? 2 * a.F : a.H) + r + (UP ? size_t(i) * a.F : 0);
+    }
+    __device__ __forceinline__ void rows(int u, int, int tile, int g, const char* (&w)[kMT][2]) const {
+        const At x = at(u);
+        const char* base = UP ? a.up[x.e / a.E_loc] : a.down[x.e / a.E_loc];
+        const size_t row_bytes = WTraits<WK>::kQ4 ? size_t(K) / 2 : size_t(K) * 2;
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[m][i] = base + row_at(x, tile, m, i, g) * row_bytes;
+    }
+    __device__ __forceinline__ void scales(int u, int, int tile, int g, int t, const uint16_t* (&s)[(kMT + 1) / 2]) const {
+        const At x = at(u);
+        s[0] = (UP ? a.up_scale[x.e / a.E_loc] : a.down_scale[x.e / a.E_loc]) +
+               row_at(x, tile, t / 2, t % 2, g) * (size_t(K) >> a.group_shift);
+    }
+    __device__ __forceinline__ const uint16_t* token(int u, int, int n) const {
+        const At x = at(u);
+        if (n >= x.count) return nullptr;
+        const int asg = l.list[x.first + n];
+        if constexpr (UP) {
+            const int tok = asg / a.k;
+            return a.x[a.rank0 + tok / int(a.T)] + size_t(tok % int(a.T)) * a.H;
+        } else {
+            return a.h + size_t(asg) * a.h_stride;
+        }
+    }
+};
+
+// Runs f with the number of 8-token tiles that a count of assignments needs.
+template <typename F> __device__ __forceinline__ bool with_tiles(int count, F f) {
+    if (count <= 8) return f(std::integral_constant<int, 1>());
+    if (count <= 16) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 4>());
+}
+
+template <int WK, bool VEC, bool UP>
+__device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLists& l, const ProductSmem& s, PanelCount& pc,
+                                            int nact) {
+    using Job = LayerJob<WK, VEC, UP>;
+    const Job job(a, l, nact);
+    const int units = job.units();
+    if (threadIdx.x >= kProdWarps * 32) {
+        for (int u = blockIdx.x; u < units; u += gridDim.x)
+            if (!with_tiles(job.at(u).count, [&](auto nt) {
+                    return copy_tokens<decltype(nt)::value>(job, a.ctl, a.timeout_ns, s, pc, u);
+                }))
+                return false;
+        return true;
+    }
+    Multiplier<Job> mul(job, s, blockIdx.x, units, gridDim.x);
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const typename Job::At x = job.at(u);
+        const bool ok = with_tiles(x.count, [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            float acc[kLayTiles][NT][4];
+            if (!mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc)) return false;
+            finish_unit<UP, kLayTiles, NT>(s, job.splits, acc, [&](int tile, int r, int c, float v, float v2) {
+                const int row = x.row0 + tile * Job::kTile + (UP ? r / 16 * 8 + r % 8 : r);
+                if (row >= job.rows_all || c >= x.count) return;
+                const int asg = l.list[x.first + c];
+                if constexpr (UP) a.h[size_t(asg) * a.h_stride + row] = float_to_bf16_bits(silu_mul(v, v2));
+                else a.y[size_t(asg) * a.H + row] = v;
+            });
+            return true;
+        });
+        if (!ok) {
+            mul.drain();
+            return false;
+        }
+    }
+    mul.drain();
+    return true;
 }
 
 template <int WK, bool VEC>
-__global__ void __launch_bounds__(kLayThreads, 2) k_moe_layer(const __grid_constant__ MoeLayerArgs a) {
+__global__ void __launch_bounds__(kProdThreads, 2) k_moe_layer(const __grid_constant__ MoeLayerArgs a) {
     extern __shared__ __align__(16) unsigned char s_raw[];
-    __shared__ float s_red[kLayWarps * 4 * (kLayTokens / 8) * 32];
     __shared__ int s_fail;
     if (threadIdx.x == 0) s_fail = status_failed(a.ctl);
     __syncthreads();
     if (s_fail) return;
     const int most = min(a.E, a.A);
     LayerLists l;
-    l.offset = reinterpret_cast<int*>(s_raw);
+    l.offset = reinterpret_cast<int*>(s_raw + product_smem<kLayTiles>());
     l.act_start = l.offset + a.E;
     l.act_tile = l.act_start + most + 1;
     l.act = reinterpret_cast<uint16_t*>(l.act_tile + most + 1);
     l.list = l.act + most;
+    const ProductSmem s = product_layout<kLayTiles>(s_raw);
+    if (threadIdx.x == 0) init_panels(s);
     const int nact = sort_assignments(a, l);
     if (nact < 0) return;
-    layer_phase<WK, VEC, true>(a, l, s_red, nact);
-    if (!layer_barrier(a, 1)) return;
-    layer_phase<WK, VEC, false>(a, l, s_red, nact);
-    if (!layer_barrier(a, 2)) return;
+    PanelCount pc;
+    bool ok = layer_phase<WK, VEC, true>(a, l, s, pc, nact);
+    if (!layer_barrier(a, 1, ok)) return;
+    if constexpr (VEC) {  // h was written by ordinary stores and is read by bulk copies
+        asm volatile("fence.proxy.async;" ::: "memory");
+    }
+    ok = layer_phase<WK, VEC, false>(a, l, s, pc, nact);
+    if (!layer_barrier(a, 2, ok)) return;
     // the weighted sum: a thread per token and column
     const int tokens = a.A / a.k;
     const size_t total = size_t(tokens) * a.H;
-    for (size_t i = size_t(blockIdx.x) * kLayThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kLayThreads) {
+    for (size_t i = size_t(blockIdx.x) * kProdThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kProdThreads) {
         const int tok = int(i / a.H), col = int(i % a.H);
         const int rank = a.rank0 + tok / int(a.T);
         const size_t at = size_t(tok % int(a.T)) * a.H + col;
@@ -291,35 +312,36 @@ __global__ void __launch_bounds__(kLayThreads, 2) k_moe_layer(const __grid_const
     if (threadIdx.x == 0) leave_tasks(&a.st->layer_ctr, &a.st->layer_done);
 }
 
-size_t moe_layer_lists_bytes(int E, int A) {
+static size_t moe_layer_lists_bytes(int E, int A) {
     const size_t most = size_t(std::min(E, A));
     return size_t(E) * 4 + (most + 1) * 8 + most * 2 + size_t(A) * 2;
 }
 
 template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int num_sms, cudaStream_t s) {
     auto* kernel = k_moe_layer<WK, VEC>;
-    const size_t smem = moe_layer_lists_bytes(a.E, a.A);
-    cudaError_t e = cudaSuccess;
-    if (smem > 32 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const size_t smem = product_smem<kLayTiles>() + moe_layer_lists_bytes(a.E, a.A);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kLayThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kProdThreads, smem);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorNotSupported;
     const size_t resident = size_t(num_sms) * per_sm;
     const size_t picked = size_t(std::min(a.E, a.A)) + size_t(a.A) / kLayTokens;  // at most this many token tiles
     // warps of a CTA on one row tile: more, the fewer tiles there are to fill the GPU with
-    auto plan = [&](size_t tiles, int* splits, int* blocks) {
+    auto plan = [&](size_t tiles, int K, int* splits, int* blocks) {
+        const int stages = K / WTraits<WK>::kStageK;
         int sp = 1;
-        while (sp < kLayWarps && picked * tiles * sp < resident * 8 * kLayWarps) sp *= 2;
+        while (sp < max_splits<WK, kLayTokens / 8>() && sp * 2 <= stages && picked * tiles * sp < resident * 4 * kProdWarps)
+            sp *= 2;
         *splits = sp;
-        const size_t per = kLayWarps / sp;
+        const size_t per = kProdWarps / sp;
         *blocks = int((tiles + per - 1) / per);
     };
-    plan((size_t(a.F) + 7) / 8, &a.splits_up, &a.blocks_up);
-    plan((size_t(a.H) + 15) / 16, &a.splits_down, &a.blocks_down);
+    plan((size_t(a.F) + 8 * kLayTiles - 1) / (8 * kLayTiles), a.H, &a.splits_up, &a.blocks_up);
+    plan((size_t(a.H) + 16 * kLayTiles - 1) / (16 * kLayTiles), a.F, &a.splits_down, &a.blocks_down);
     const size_t units = picked * size_t(std::max(a.blocks_up, a.blocks_down));
-    dim3 grid(unsigned(std::max<size_t>(1, std::min(resident, units)))), block(kLayThreads);
+    dim3 grid(unsigned(std::max<size_t>(1, std::min(resident, units)))), block(kProdThreads);
     void* args[] = {&a};
     e = cudaLaunchCooperativeKernel(reinterpret_cast<void*>(kernel), grid, block, args, smem, s);
     return e != cudaSuccess ? e : cudaGetLastError();

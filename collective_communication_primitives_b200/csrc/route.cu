@@ -99,109 +99,147 @@ template <int LPT, int VPL> __device__ __forceinline__ float softmax_terms(float
     return group_sum<LPT>(sum);
 }
 
+// A warp's tokens and their picks. Picks of consecutive tokens lie together in memory, so a warp's are moved
+// by all its lanes at once, through shared memory: [tokens of the warp][k] of each of up to three words.
+template <int LPT> struct RouteWarp {
+    static constexpr int kTokens = 32 / LPT;
+    int lane, sub, grp;
+    size_t first, token;  // the warp's first token, the group's
+    int count;            // tokens of the warp
+    bool live;
+    int rank;
+    size_t t;
+    uint32_t* picks;      // [3][kTokens * k]
+
+    __device__ __forceinline__ RouteWarp(const RouteArgs& a, uint32_t* smem) {
+        lane = threadIdx.x & 31;
+        sub = lane % LPT;
+        grp = lane / LPT;
+        first = ((size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5) * kTokens;
+        token = first + grp;
+        count = first < a.tokens ? int(min(size_t(kTokens), a.tokens - first)) : 0;
+        live = token < a.tokens;
+        rank = a.rank0 + int(live ? token / a.T : 0);
+        t = live ? token % a.T : 0;
+        picks = smem + (threadIdx.x >> 5) * 3 * kTokens * a.k;
+    }
+    __device__ __forceinline__ uint32_t* word(const RouteArgs& a, int w) const { return picks + w * kTokens * a.k; }
+    // f(place in the warp's picks, rank, place in the rank's [T][k]) for every pick of the warp, spread over the lanes.
+    template <typename F> __device__ __forceinline__ void each_pick(const RouteArgs& a, F f) const {
+        const int n = count * a.k;
+        const size_t r0 = first / a.T, base = (first - r0 * a.T) * a.k, per = a.T * a.k;
+        for (int i = lane; i < n; i += 32) {  // a warp's tokens may run on into the next ranks
+            size_t at = base + i;
+            int r = a.rank0 + int(r0);
+            while (at >= per) {
+                at -= per;
+                ++r;
+            }
+            f(i, r, at);
+        }
+    }
+};
+
 template <int DT, int LPT, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) k_route(const __grid_constant__ RouteArgs a) {
+    extern __shared__ uint32_t s_picks[];
     if (status_failed(a.ctl)) return;
-    constexpr int kPerWarp = 32 / LPT;
-    const int lane = threadIdx.x & 31, sub = lane % LPT, grp = lane / LPT;
-    const unsigned gmask = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (grp * LPT);
-    const size_t warp = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
-    const size_t token = warp * kPerWarp + grp;
-    const bool live = token < a.tokens;
-    const int rank = a.rank0 + int(live ? token / a.T : 0);
-    const size_t t = live ? token % a.T : 0;
-    const char* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
-    const int e0 = sub * VPL;
+    const RouteWarp<LPT> w(a, s_picks);
+    const unsigned gmask = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (w.grp * LPT);
+    const char* row = static_cast<const char*>(a.logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
+    const int e0 = w.sub * VPL;
     float v[VPL];
-    ld_scores<DT, VPL>(v, row, e0, live ? a.E : 0, a.vec, -INFINITY);
+    ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
     uint32_t key[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) key[j] = e0 + j < a.E ? order_key(v[j]) : 0u;
     float top;
     const float sum = softmax_terms<LPT, VPL>(v, &top);
-    // k rounds: lane s of the group keeps pick s (k may exceed the group: pick s is kept by lane s % LPT)
-    float picked = 0.0f;  // sum of the picked terms
+    uint32_t* ids = w.word(a, 0) + w.grp * a.k;
+    float* terms = reinterpret_cast<float*>(w.word(a, 1)) + w.grp * a.k;
+    float picked = 0.0f;  // sum of the picked terms, on every lane of the group
     for (int s = 0; s < a.k; ++s) {
         uint32_t best = key[0];
 #pragma unroll
         for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
         const uint32_t all = group_umax<LPT>(best);
-        const unsigned who = __ballot_sync(0xffffffffu, best == all) & gmask;
-        const int winner = __ffs(who) - 1;
-        int at = 0;
+        const int winner = __ffs(__ballot_sync(0xffffffffu, best == all) & gmask) - 1;
         float term = 0.0f;
+        if (w.lane == winner) {
+            int at = 0;
 #pragma unroll
-        for (int j = VPL - 1; j >= 0; --j)
-            if (key[j] == all) {
-                at = j;
-                term = v[j];
-            }
-        if (lane == winner) {
+            for (int j = VPL - 1; j >= 0; --j)
+                if (key[j] == all) {
+                    at = j;
+                    term = v[j];
+                }
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
                 if (j == at) key[j] = 0u;
+            ids[s] = uint32_t(e0 + at);
+            terms[s] = term;
         }
-        const int e = __shfl_sync(0xffffffffu, e0 + at, winner);
-        term = __shfl_sync(0xffffffffu, term, winner);
-        picked += term;
-        if (live && sub == 0) {
-            a.idx_out[rank][t * a.k + s] = e;
-            a.weight[rank][t * a.k + s] = term;  // scaled below, by the same lane
-        }
+        __syncwarp();
     }
-    if (live && sub == 0) {
-        const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
-        for (int s = 0; s < a.k; ++s) {
-            float* w = a.weight[rank] + t * a.k + s;
-            *w = total == 0.0f ? 0.0f : *w / total;
-        }
-    }
+    for (int s = 0; s < a.k; ++s) picked += terms[s];
+    const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
+    for (int s = w.sub; s < a.k; s += LPT) terms[s] = total == 0.0f ? 0.0f : terms[s] / total;
+    __syncwarp();
+    const uint32_t* all_ids = w.word(a, 0);
+    const float* all_terms = reinterpret_cast<const float*>(w.word(a, 1));
+    w.each_pick(a, [&](int i, int r, size_t at) {
+        a.idx_out[r][at] = int32_t(all_ids[i]);
+        a.weight[r][at] = all_terms[i];
+    });
 }
 
 template <int DT, int LPT, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_constant__ RouteArgs a) {
+    extern __shared__ uint32_t s_picks[];
     if (status_failed(a.ctl)) return;
-    constexpr int kPerWarp = 32 / LPT;
-    const int lane = threadIdx.x & 31, sub = lane % LPT, grp = lane / LPT;
-    const size_t warp = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
-    const size_t token = warp * kPerWarp + grp;
-    const bool live = token < a.tokens;
-    const int rank = a.rank0 + int(live ? token / a.T : 0);
-    const size_t t = live ? token % a.T : 0;
-    const char* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
-    const int32_t* idx = a.idx_in[rank] + t * a.k;
-    const float* gw = a.grad_weight[rank] + t * a.k;
-    const int e0 = sub * VPL;
-    const int k = live ? a.k : 0;
+    const RouteWarp<LPT> w(a, s_picks);
+    const char* row = static_cast<const char*>(a.logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
+    const int e0 = w.sub * VPL;
     float v[VPL], G[VPL];
+    if (!a.normalise) ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
+    bool bad = false;
+    uint32_t* ids_all = w.word(a, 0);
+    float* g_all = reinterpret_cast<float*>(w.word(a, 1));
+    float* x_all = reinterpret_cast<float*>(w.word(a, 2));
+    w.each_pick(a, [&](int i, int r, size_t at) {
+        const int e = a.idx_in[r][at];
+        const bool ok = e >= 0 && e < a.E;
+        bad = bad || !ok;
+        ids_all[i] = ok ? uint32_t(e) : 0xffffffffu;  // held by no lane
+        g_all[i] = a.grad_weight[r][at];
+        if (a.normalise)
+            x_all[i] = ok ? ld_score<DT>(static_cast<const char*>(a.logits[r]) + (at / a.k) * a.E * Elem<DT>::kBytes, e) : -INFINITY;
+    });
+    if (bad) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+    __syncwarp();
+    const uint32_t* ids = ids_all + w.grp * a.k;
+    const float* gw = g_all + w.grp * a.k;
+    const float* xs = x_all + w.grp * a.k;
+    const int k = w.live ? a.k : 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) G[j] = 0.0f;
     float total, dot = 0.0f;  // the weights' divisor, and sum_q g[q] * term[q]
-    bool bad = false;
     if (a.normalise) {
-        // only the picked scores matter: every lane of the group reads all k of them
+        // only the picked scores matter: every lane of the group goes over all k of them
         float top = -INFINITY;
-        for (int s = 0; s < k; ++s) {
-            const int e = idx[s];
-            if (e < 0 || e >= a.E) bad = true;
-            else {
-                const float x = ld_score<DT>(row, e);
-                top = x > top || x != x ? x : top;
-            }
-        }
+        for (int s = 0; s < k; ++s) top = xs[s] > top || xs[s] != xs[s] ? xs[s] : top;
         const float base = top == -INFINITY ? 0.0f : top;
         total = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) v[j] = 0.0f;
         for (int s = 0; s < k; ++s) {
-            const int e = idx[s];
-            if (e < 0 || e >= a.E) continue;
-            const float term = exp2_fast((ld_score<DT>(row, e) - base) * kLog2e), g = gw[s];
+            const int at = int(ids[s]) - e0;
+            const float term = exp2_fast((xs[s] - base) * kLog2e), g = gw[s];
             total += term;
             dot = __fmaf_rn(g, term, dot);
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (e == e0 + j) {
+                if (at == j) {
                     v[j] += term;
                     G[j] = __fmaf_rn(g, term, G[j]);
                 }
@@ -212,20 +250,16 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
 #pragma unroll
         for (int j = 0; j < VPL; ++j) G[j] = (G[j] - v[j] * mean) * inv;
     } else {
-        ld_scores<DT, VPL>(v, row, e0, live ? a.E : 0, a.vec, -INFINITY);
         float top;
         total = softmax_terms<LPT, VPL>(v, &top);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         for (int s = 0; s < k; ++s) {
-            const int e = idx[s];
-            if (e < 0 || e >= a.E) {
-                bad = true;
-                continue;
-            }
+            const int at = int(ids[s]) - e0;
+            if (at < 0 || at >= VPL) continue;
             const float g = gw[s];
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
-                if (e == e0 + j) {
+                if (at == j) {
                     G[j] += g;
                     dot = __fmaf_rn(g, v[j], dot);
                 }
@@ -234,9 +268,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
 #pragma unroll
         for (int j = 0; j < VPL; ++j) G[j] = v[j] * inv * (G[j] - mean);
     }
-    if (bad) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
-    if (!live) return;
-    char* out = static_cast<char*>(a.grad_logits[rank]) + t * a.E * Elem<DT>::kBytes;
+    if (!w.live) return;
+    char* out = static_cast<char*>(a.grad_logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
     if (a.vec) {
         using P = Pack16<DT>;
 #pragma unroll
@@ -352,8 +385,9 @@ template <int DT> static cudaError_t launch_route_dt(const RouteArgs& a, bool ba
     };
 #define SIMCOMM_ROUTE(LPT, VPL)                                                          \
     do {                                                                                 \
-        if (backward) k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 0, s>>>(a); \
-        else k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 0, s>>>(a);               \
+        const size_t smem = size_t(kRouteThreads / LPT) * a.k * 12;                         \
+        if (backward) k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a); \
+        else k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a);               \
         return cudaGetLastError();                                                       \
     } while (0)
     if (a.E <= 8) SIMCOMM_ROUTE(1, 8);

@@ -1,24 +1,29 @@
 // Products of a weight matrix with few tokens, streamed: the device code that the 4-bit linear and
 // the expert layer share.
 //
-//   D[r][n] = sum_k W[r][k] X[n][k],   16 weight rows x 8 NT tokens per warp
+//   D[r][n] = sum_k W[r][k] X[n][k],   16 MT weight rows x 8 NT tokens per warp
 //
 // With few tokens the weights' bytes bound the time: every weight is used once per token, so the job
-// is to keep enough 16-byte loads in flight and to spend few instructions per byte. The weights go
-// from memory straight into the registers of the matrix instruction (mma.sync m16n8k16, weights as
-// its 16-row operand and tokens as its 8 columns, so that one token wastes no more than 7 columns):
-// no pass through shared memory. That works because a sum over k may be taken in any order as long
-// as both operands use the same one: lane (g, t) (g = lane / 4, t = lane % 4) of the instruction owns
-// rows g and g + 8 and four k's of every step, so it is given 8 consecutive k's of both rows, one
-// 16-byte load each for bf16, and the tokens' lanes load the same k's of their rows. A step of the
-// warp ("chunk") covers 32 k's of bf16 weights, or 8 LW x 4 of 4-bit ones, LW words of eight weights
-// per lane, so that a chunk never crosses a scale group.
+// is to keep enough loads in flight and to spend few instructions per byte. Weights are the 16-row
+// operand of the matrix instruction (mma.sync m16n8k16) and tokens its 8 columns, so that one token
+// wastes no more than 7 columns. A sum over k may be taken in any order as long as both operands use
+// the same one, so no weight is ever moved between lanes for the instruction's sake: lane (g, t)
+// (g = lane / 4, t = lane % 4) owns rows g and g + 8 of a row tile and whole runs of 8 k's.
+//
+// Every warp streams its own weights: 64 bytes of each of its rows per stage (32 k's of bf16, 128 of
+// 4-bit weights) through a ring of stages in shared memory, copied 16 bytes per lane and row
+// (cp.async). The ring costs no registers and no synchronisation between warps, and its copies run on
+// from one unit of work into the next. The tokens of a unit are shared by the CTA's warps: a ninth warp
+// copies a panel of k's of their rows ahead (one bulk copy per token, completing on an mbarrier), and the
+// eight others hand a panel back when they have used it. Rows of a panel are padded so that the lanes'
+// 16-byte reads spread over the banks (2-way for 32 consecutive k's per lane, free otherwise). Columns
+// without a token hold whatever the panel held before: a column's sums depend on that column alone.
 //
 // 4-bit weights: word bits 4i..4i+3 hold weight i of eight, value q - 8. (w & 0x000F000F) | 0x43004300
 // is the pair (128 + q_0, 128 + q_4) of bf16 values, and subtracting 136 is exact; shifts by 4 give
-// the pairs (1,5), (2,6), (3,7), and the tokens' words are paired the same way. A chunk's sum is
-// taken over the whole numbers q - 8 (bf16 holds them, the products are exact in fp32) and scaled
-// once per chunk in fp32, so the weights are never rounded.
+// the pairs (1,5), (2,6), (3,7); the tokens' words are paired the same way as they are read. A chunk's sum is taken
+// over the whole numbers q - 8 (bf16 holds them, the products are exact in fp32) and scaled once per
+// chunk in fp32, so the weights are never rounded.
 //
 // Sums are held in fp32 throughout: the matrix instruction's accumulator, then plain adds over the
 // warps that share a row tile, in warp order.
@@ -32,161 +37,462 @@ enum WeightKind { W_BF16 = 0, W_Q4X4 = 1, W_Q4X2 = 2, W_Q4X1 = 3 };
 
 template <int WK> struct WTraits {
     static constexpr bool kQ4 = WK != W_BF16;
-    static constexpr int kWords = WK == W_Q4X4 ? 4 : WK == W_Q4X2 ? 2 : WK == W_Q4X1 ? 1 : 0;  // 4-bit: words per lane
-    static constexpr int kLaneK = kQ4 ? 8 * kWords : 8;  // k's of one lane in a chunk
-    static constexpr int kChunk = 4 * kLaneK;            // k's of a warp's chunk
+    static constexpr int kWords = WK == W_Q4X4 ? 4 : WK == W_Q4X2 ? 2 : 1;  // 16-byte token pieces of a lane in a chunk
+    static constexpr int kLaneK = 8 * kWords;    // k's of one lane in a chunk
+    static constexpr int kChunk = 4 * kLaneK;    // k's of a warp's chunk
+    static constexpr int kLaneBytes = kQ4 ? 4 * kWords : 16;  // weight bytes of one lane and row in a chunk
+    static constexpr int kChunks = 16 / kLaneBytes;           // chunks of a stage (64 bytes of a row)
+    static constexpr int kStageK = kChunks * kChunk;          // k's of a stage
+    static constexpr int kPieces = kChunks * kWords;          // 16-byte token pieces of a lane in a stage
 };
+
+constexpr int kProdWarps = 8;                       // warps that multiply
+constexpr int kProdThreads = (kProdWarps + 1) * 32;  // and one that copies tokens
+constexpr int kRing = 4;                            // stages of a warp's weight ring
+constexpr int kPanelK = 1024;                       // a panel: 8 NT tokens x kPanelK / NT k's
+constexpr int kPanels = 2;
+constexpr int kMaxNT = 4;
+template <int WK> constexpr int panel_pad() { return WK == W_Q4X4 ? 32 : WK == W_Q4X2 ? 16 : 64; }  // bytes per row
+template <int WK, int NT> constexpr int panel_pitch() { return kPanelK / NT * 2 + panel_pad<WK>(); }
+constexpr int kPanelBytes = 8 * kPanelK * 2 + 8 * kMaxNT * 64;
+constexpr int kSumTokens = 16;  // tokens whose sums are exchanged at a time where warps share a row tile
+template <int MT> constexpr int sums_bytes() { return kProdWarps * MT * 16 * kSumTokens * 4; }
+// Shared memory: panels, rings, exchanged sums, mbarriers.
+template <int MT> constexpr int product_smem() {
+    return kPanels * kPanelBytes + kProdWarps * kRing * MT * 1024 + sums_bytes<MT>() + 2 * kPanels * 8;
+}
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights are read once: streaming loads that leave L1 to the tokens.
-__device__ __forceinline__ uint2 ld_stream_v2(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
+// The same with a zero addend.
+__device__ __forceinline__ void mma_bf16_from0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ uint32_t ld_stream_u32(const void* p) {
-    uint32_t v;
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
+
+// 16 bytes from global to shared memory, `bytes` of them read (0: zeros).
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* g, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" :: "r"(smem), "l"(g), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
 // Eight consecutive bf16 values from element k of a row of K, zero past the end. VEC: K and the row
 // are multiples of 16 bytes; otherwise one element at a time.
 template <bool VEC> __device__ __forceinline__ uint4 ld_row8(const uint16_t* row, int k, int K) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (!row || k >= K) return v;
+    if (!row || k >= K) return make_uint4(0u, 0u, 0u, 0u);
     if constexpr (VEC) {
         return *reinterpret_cast<const uint4*>(row + k);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = row[k + 2 * i < K ? k + 2 * i : k], hi = row[k + 2 * i + 1 < K ? k + 2 * i + 1 : k];
-            w[i] = (k + 2 * i < K ? lo : 0u) | (k + 2 * i + 1 < K ? hi << 16 : 0u);
+            const uint32_t lo = k + 2 * i < K ? row[k + 2 * i] : 0u, hi = k + 2 * i + 1 < K ? row[k + 2 * i + 1] : 0u;
+            w[i] = lo | hi << 16;
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-template <bool VEC> __device__ __forceinline__ uint4 ld_weight8(const uint16_t* row, int k, int K) {
-    if constexpr (VEC) return (row && k < K) ? ld_stream_v4(row + k) : make_uint4(0u, 0u, 0u, 0u);
-    else return ld_row8<false>(row, k, K);
-}
 
+// The constants of the 4-bit form, held in registers: a logic instruction takes one immediate, and the
+// mask and the bias go into one.
+struct Q4Consts { uint32_t mask, bias; };
+__device__ __forceinline__ Q4Consts q4_consts() {
+    Q4Consts c;
+    asm volatile("mov.u32 %0, 0x000F000F; mov.u32 %1, 0x43004300;" : "=r"(c.mask), "=r"(c.bias));
+    return c;
+}
 // Two bf16 values q - 8 of the nibble pair (i, i + 4) of a word shifted right by 4 i.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w) {
-    const uint32_t biased = (w & 0x000F000Fu) | 0x43004300u;
-    uint32_t r;
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, const Q4Consts& c) {
+    uint32_t biased, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(biased) : "r"(w), "r"(c.mask), "r"(c.bias));  // (w & mask) | bias
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43084308u));
     return r;
 }
 
-// One lane's view of a warp's product: rows g and g + 8 of the row tile and NT token rows.
-struct LaneRows {
-    const char* w0;          // weight row g (null: past the matrix, reads as zero)
-    const char* w1;          // weight row g + 8
-    const uint16_t* s0;      // 4-bit: scales of the rows, one per group
-    const uint16_t* s1;
-};
+// The place of 16-byte piece p of row (m, i, g) in a ring stage. Rows lie 64 bytes apart; the pieces of a
+// row are permuted by g so that reads of 4, 8 and 16 bytes per lane all spread over the banks.
+__device__ __forceinline__ uint32_t ring_at(int m, int i, int g, int p) {
+    const int swz = ((g >> 1) & 1) << 1 | g >> 2;
+    return uint32_t(((m * 2 + i) * 8 + g) * 64 + ((p ^ swz) << 4));
+}
 
-// acc += the product over chunks [c0, c1) of a row of K.
-template <int WK, bool VEC, int NT>
-__device__ __forceinline__ void warp_product(float (&acc)[NT][4], const LaneRows& r, const uint16_t* const (&x)[NT],
-                                             int c0, int c1, int K, int groups_per_chunk_shift, int t) {
+// Starts the copy of one stage of the warp's weights (64 bytes of each row) into the ring.
+template <int WK, bool VEC, int MT>
+__device__ __forceinline__ void fetch_stage(uint32_t ring, const char* const (&w)[MT][2], int stage, int K, int g, int t) {
     using W = WTraits<WK>;
-    if constexpr (!W::kQ4) {
-        constexpr int U = 4;  // chunks in flight per lane
-        const uint16_t* w0 = reinterpret_cast<const uint16_t*>(r.w0);
-        const uint16_t* w1 = reinterpret_cast<const uint16_t*>(r.w1);
-        for (int c = c0; c < c1; c += U) {
-            uint4 a[U], b[U];
+    const int k = stage * W::kStageK + t * (W::kStageK / 4);  // first k of the lane's 16 bytes
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = c + u < c1 ? (c + u) * W::kChunk + t * 8 : K;
-                a[u] = ld_weight8<VEC>(w0, k, K);
-                b[u] = ld_weight8<VEC>(w1, k, K);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t to = ring + ring_at(m, i, g, t);
+            if constexpr (VEC) {
+                cp_async16(to, w[m][i] + (k < K ? size_t(stage) * 64 + t * 16 : 0), k < K ? 16u : 0u);
+            } else {
+                const uint4 v = ld_row8<false>(reinterpret_cast<const uint16_t*>(w[m][i]), k, K);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
             }
+        }
+}
+
+// The scales of a stage's rows, one per chunk, Lane t of a quad loads those of rows (2 q + t / 2,
+// t % 2) (with one row tile: (0, t % 2)), a stage ahead (a row's scales lie together, so that most of these loads hit L1), and they
+// are exchanged when they are used.
+template <int WK, int MT> struct StageScales { uint16_t v[(MT + 1) / 2][WTraits<WK>::kChunks]; };
+
+template <int WK, int MT>
+__device__ __forceinline__ void load_scales(StageScales<WK, MT>& sc, const uint16_t* const (&s)[(MT + 1) / 2], int stage, int groups, int shift) {
+    using W = WTraits<WK>;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = c + u < c1 ? (c + u) * W::kChunk + t * 8 : K;
+    for (int u = 0; u < W::kChunks; ++u) {
+        const int grp = min((stage * W::kChunks + u) >> shift, groups - 1);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 xv = ld_row8<VEC>(x[n], k, K);
-                    mma_bf16(acc[n], a[u].x, b[u].x, a[u].y, b[u].y, xv.x, xv.y);
-                    mma_bf16(acc[n], a[u].z, b[u].z, a[u].w, b[u].w, xv.z, xv.w);
-                }
+        for (int q = 0; q < (MT + 1) / 2; ++q) sc.v[q][u] = __ldg(s[q] + grp);
+    }
+}
+
+template <int BYTES> __device__ __forceinline__ void lds(uint32_t (&v)[4], const unsigned char* at) {
+    if constexpr (BYTES == 16) {
+        const uint4 q = *reinterpret_cast<const uint4*>(at);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else if constexpr (BYTES == 8) {
+        const uint2 q = *reinterpret_cast<const uint2*>(at);
+        v[0] = q.x; v[1] = q.y;
+    } else {
+        v[0] = *reinterpret_cast<const uint32_t*>(at);
+    }
+}
+
+// acc += one stage, whose tokens' k's start at `tok` of the panel (at this lane's token and first k).
+template <int WK, int MT, int NT>
+__device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigned char* ring, const StageScales<WK, MT>& sc,
+                                          const unsigned char* tok, int g, int t, const Q4Consts& qc) {
+    using W = WTraits<WK>;
+    constexpr int kPitch = panel_pitch<WK, NT>();
+    auto token8 = [&](int n, int u, int j) {  // run j of 8 k's of chunk u
+        return *reinterpret_cast<const uint4*>(tok + n * 8 * kPitch + u * W::kChunk * 2 + j * 16);
+    };
+    auto paired = [](uint4 v) {  // (0,4) (1,5) (2,6) (3,7)
+        return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                          __byte_perm(v.y, v.w, 0x7632));
+    };
+    if constexpr (!W::kQ4) {
+        uint4 x[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n] = token8(n, 0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) lds<16>(a[i], ring + ring_at(m, i, g, t));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_bf16(acc[m][n], a[0][0], a[1][0], a[0][1], a[1][1], x[n].x, x[n].y);
+                mma_bf16(acc[m][n], a[0][2], a[1][2], a[0][3], a[1][3], x[n].z, x[n].w);
             }
         }
     } else {
-        constexpr int U = W::kWords == 4 ? 4 : W::kWords == 2 ? 8 : 8;
-        for (int c = c0; c < c1; c += U) {
-            uint32_t a[U][W::kWords], b[U][W::kWords];
-            float sa[U], sb[U];
+        // a chunk's tokens are held for all row tiles, unless they are too many registers
+        constexpr bool kHold = W::kWords * NT <= 8;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool in = c + u < c1;
-                const size_t off = (size_t(c + u) * 4 + t) * (4 * W::kWords);
-                const int grp = (c + u) >> groups_per_chunk_shift;
+        for (int u = 0; u < W::kChunks; ++u) {
+            uint4 x[kHold ? W::kWords : 1][NT];
+            if constexpr (kHold) {
 #pragma unroll
-                for (int j = 0; j < W::kWords; ++j) a[u][j] = b[u][j] = 0u;
-                sa[u] = sb[u] = 0.0f;
-                if (in && r.w0) {
-                    if constexpr (W::kWords == 4) {
-                        const uint4 v = ld_stream_v4(r.w0 + off);
-                        a[u][0] = v.x; a[u][1] = v.y; a[u][2] = v.z; a[u][3] = v.w;
-                    } else if constexpr (W::kWords == 2) {
-                        const uint2 v = ld_stream_v2(r.w0 + off);
-                        a[u][0] = v.x; a[u][1] = v.y;
-                    } else a[u][0] = *reinterpret_cast<const uint32_t*>(r.w0 + off);
-                    sa[u] = bf16_bits_to_float(r.s0[grp]);
-                }
-                if (in && r.w1) {
-                    if constexpr (W::kWords == 4) {
-                        const uint4 v = ld_stream_v4(r.w1 + off);
-                        b[u][0] = v.x; b[u][1] = v.y; b[u][2] = v.z; b[u][3] = v.w;
-                    } else if constexpr (W::kWords == 2) {
-                        const uint2 v = ld_stream_v2(r.w1 + off);
-                        b[u][0] = v.x; b[u][1] = v.y;
-                    } else b[u][0] = *reinterpret_cast<const uint32_t*>(r.w1 + off);
-                    sb[u] = bf16_bits_to_float(r.s1[grp]);
-                }
+                for (int j = 0; j < W::kWords; ++j)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) x[j][n] = paired(token8(n, u, j));
             }
+            const int byte = (4 * u + t) * W::kLaneBytes;  // of the row's 64
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int m = 0; m < MT; ++m) {
+                uint32_t w[2][4];
                 float d[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-                const int k0 = c + u < c1 ? (c + u) * W::kChunk + t * W::kLaneK : K;
+                for (int i = 0; i < 2; ++i) lds<W::kLaneBytes>(w[i], ring + ring_at(m, i, g, byte >> 4) + (byte & 15));
 #pragma unroll
                 for (int j = 0; j < W::kWords; ++j) {
-                    const uint32_t wa = a[u][j], wb = b[u][j];
-                    const uint32_t a0 = q4_pair(wa), a1 = q4_pair(wa >> 4), a2 = q4_pair(wa >> 8), a3 = q4_pair(wa >> 12);
-                    const uint32_t b0 = q4_pair(wb), b1 = q4_pair(wb >> 4), b2 = q4_pair(wb >> 8), b3 = q4_pair(wb >> 12);
+                    if constexpr (!kHold) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) x[0][n] = paired(token8(n, u, j));
+                    }
+                    const uint32_t wa = w[0][j], wb = w[1][j];
+                    const uint32_t a0 = q4_pair(wa, qc), a1 = q4_pair(wa >> 4, qc), a2 = q4_pair(wa >> 8, qc), a3 = q4_pair(wa >> 12, qc);
+                    const uint32_t b0 = q4_pair(wb, qc), b1 = q4_pair(wb >> 4, qc), b2 = q4_pair(wb >> 8, qc), b3 = q4_pair(wb >> 12, qc);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const uint4 xv = ld_row8<VEC>(x[n], k0 + 8 * j, K);
-                        // pairs (k, k + 4): halves of words (0, 2), then (1, 3)
-                        const uint32_t x04 = __byte_perm(xv.x, xv.z, 0x5410), x15 = __byte_perm(xv.x, xv.z, 0x7632);
-                        const uint32_t x26 = __byte_perm(xv.y, xv.w, 0x5410), x37 = __byte_perm(xv.y, xv.w, 0x7632);
-                        mma_bf16(d[n], a0, b0, a1, b1, x04, x15);
-                        mma_bf16(d[n], a2, b2, a3, b3, x26, x37);
+                        const uint4 v = x[kHold ? j : 0][n];
+                        if (j == 0) mma_bf16_from0(d[n], a0, b0, a1, b1, v.x, v.y);
+                        else mma_bf16(d[n], a0, b0, a1, b1, v.x, v.y);
+                        mma_bf16(d[n], a2, b2, a3, b3, v.z, v.w);
                     }
                 }
+                const int from = (threadIdx.x & 28) + 2 * (m % 2);  // the quad's lane that holds row (m, 0)
+                const float sa = bf16_bits_to_float(__shfl_sync(0xffffffffu, uint32_t(sc.v[m / 2][u]), from));
+                const float sb = bf16_bits_to_float(__shfl_sync(0xffffffffu, uint32_t(sc.v[m / 2][u]), from + 1));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    acc[n][0] = __fmaf_rn(sa[u], d[n][0], acc[n][0]);
-                    acc[n][1] = __fmaf_rn(sa[u], d[n][1], acc[n][1]);
-                    acc[n][2] = __fmaf_rn(sb[u], d[n][2], acc[n][2]);
-                    acc[n][3] = __fmaf_rn(sb[u], d[n][3], acc[n][3]);
+                    acc[m][n][0] = __fmaf_rn(sa, d[n][0], acc[m][n][0]);
+                    acc[m][n][1] = __fmaf_rn(sa, d[n][1], acc[m][n][1]);
+                    acc[m][n][2] = __fmaf_rn(sb, d[n][2], acc[m][n][2]);
+                    acc[m][n][3] = __fmaf_rn(sb, d[n][3], acc[m][n][3]);
                 }
             }
+        }
+    }
+}
+
+// ---- the work of a CTA -----------------------------------------------------------------------------
+//
+// A Job describes a sequence of units; the CTA takes units first, first + step, ... A unit is a block of row
+// tiles against up to 8 NT tokens, summed over `segments` rows of K each (the ranks of a sum over ranks).
+// `splits` warps share each row tile, the stages of a segment dealt to them in turn. A Job has
+//   static kWK, kVecW, kVecX, kMT;   int K, segments, splits, chunk_shift
+//   void rows(unit, seg, tile, g, w)     the lane's weight rows of the CTA's tile-th row tile group
+//   void scales(unit, seg, tile, g, t, s)
+//   const uint16_t* token(unit, seg, n)  row of the n-th token, null for none
+
+// Most warps that can share a row tile: every panel has a stage for each.
+template <int WK, int NT> constexpr int max_splits() {
+    return kPanelK / NT / WTraits<WK>::kStageK < kProdWarps ? kPanelK / NT / WTraits<WK>::kStageK : kProdWarps;
+}
+
+struct ProductSmem {
+    unsigned char* base;
+    int rings, sums;  // bytes from base
+    uint64_t* full;   // [kPanels]: the panel's tokens are in
+    uint64_t* empty;  // [kPanels]: every multiplying warp has used it
+};
+template <int MT> __device__ __forceinline__ ProductSmem product_layout(unsigned char* smem) {
+    ProductSmem s;
+    s.base = smem;
+    s.rings = kPanels * kPanelBytes;
+    s.sums = s.rings + kProdWarps * kRing * MT * 1024;
+    s.full = reinterpret_cast<uint64_t*>(smem + s.sums + sums_bytes<MT>());
+    s.empty = s.full + kPanels;
+    return s;
+}
+// By one thread, before a __syncthreads.
+__device__ __forceinline__ void init_panels(const ProductSmem& s) {
+    for (int i = 0; i < kPanels; ++i) {
+        mbar_init(&s.full[i], 1);
+        mbar_init(&s.empty[i], kProdWarps);
+    }
+    fence_barrier_init();
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+
+// How many panels have gone by, the same for both sides.
+struct PanelCount {
+    uint32_t n = 0;
+    __device__ int buf() const { return int(n % kPanels); }
+    __device__ uint32_t parity() const { return n / kPanels & 1u; }
+};
+
+// The copying warp's side of a unit. False after a wait that ran out.
+template <int NT, typename Job>
+__device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint64_t timeout_ns, const ProductSmem& s,
+                                            PanelCount& pc, int unit) {
+    using W = WTraits<Job::kWK>;
+    constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kSpan = kPanelK / NT;
+    const int lane = threadIdx.x & 31;
+    for (int seg = 0; seg < job.segments; ++seg) {
+        const uint16_t* row = lane < 8 * NT ? job.token(unit, seg, lane) : nullptr;
+        const uint32_t rows = __popc(__ballot_sync(0xffffffffu, row != nullptr));
+        for (int k0 = 0; k0 < job.K; k0 += kSpan, ++pc.n) {
+            const int buf = pc.buf(), n = min(kSpan, job.K - k0);
+            const int padded = (n + W::kStageK - 1) / W::kStageK * W::kStageK;  // a stage is read whole
+            if (!mbar_wait_bounded(ctl, &s.empty[buf], pc.parity() ^ 1u, timeout_ns)) return false;
+            unsigned char* to = s.base + buf * kPanelBytes + lane * kPitch;
+            if constexpr (Job::kVecX) {
+                if (padded > n) {  // zeros past the row's end, before the copies that follow
+                    if (row)
+                        for (int k = n; k < padded; k += 8) *reinterpret_cast<uint4*>(to + k * 2) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&s.full[buf], rows * uint32_t(n) * 2u);
+                __syncwarp();
+                if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, &s.full[buf]);
+            } else {  // rows at odd addresses: a warp-wide copy, row after row
+                for (uint32_t i = 0; i < rows; ++i) {
+                    const uint16_t* from = job.token(unit, seg, int(i));
+                    unsigned char* dst = s.base + buf * kPanelBytes + i * kPitch;
+                    for (int k = lane * 8; k < padded; k += 256) *reinterpret_cast<uint4*>(dst + k * 2) = ld_row8<false>(from, k0 + k, job.K);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.full[buf]);
+            }
+        }
+    }
+    return true;
+}
+
+// Where a multiplying warp's copies have got to: a stage of a segment of a unit.
+template <int MT> struct Ahead {
+    const char* w[MT][2];
+    int unit, seg, next, slot;
+};
+
+template <typename Job> struct Multiplier {
+    using W = WTraits<Job::kWK>;
+    static constexpr int MT = Job::kMT;
+    const Job& job;
+    const ProductSmem& s;
+    int units, step;           // of the CTA's sequence: units below `units`, every `step`-th
+    int warp, lane, g, t, tile, split, stages;
+    uint32_t ring;
+    int slot = 0;
+    Ahead<MT> ahead;
+    Q4Consts qc;
+
+    __device__ __forceinline__ Multiplier(const Job& j, const ProductSmem& sm, int first, int units_, int step_)
+        : job(j), s(sm), units(units_), step(step_) {
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        g = lane >> 2;
+        t = lane & 3;
+        tile = warp / job.splits;
+        split = warp % job.splits;
+        stages = (job.K + W::kStageK - 1) / W::kStageK;
+        ring = smem_u32(s.base) + s.rings + warp * (kRing * MT * 1024);
+        qc = q4_consts();
+        ahead.unit = first;
+        ahead.seg = 0;
+        ahead.next = split;
+        ahead.slot = 0;
+        if (first < units) job.rows(first, 0, tile, g, ahead.w);
+        __syncwarp();  // an earlier use of the ring by this warp is over
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) fetch();
+    }
+
+    // Starts the next copy of the sequence; past its end an empty group keeps the count of groups in step.
+    __device__ __forceinline__ void fetch() {
+        while (ahead.next >= stages && ahead.unit < units) {
+            ahead.next = split;
+            if (++ahead.seg == job.segments) {
+                ahead.seg = 0;
+                ahead.unit += step;
+            }
+            if (ahead.unit < units) job.rows(ahead.unit, ahead.seg, tile, g, ahead.w);
+        }
+        if (ahead.unit < units) {
+            fetch_stage<Job::kWK, Job::kVecW, MT>(ring + ahead.slot * (MT * 1024), ahead.w, ahead.next, job.K, g, t);
+            ahead.next += job.splits;
+            ahead.slot = ahead.slot + 1 == kRing ? 0 : ahead.slot + 1;
+        }
+        cp_async_commit();
+    }
+
+    // The warp's sums of a unit over its share of the stages. False after a wait that ran out.
+    template <int NT>
+    __device__ __forceinline__ bool unit(const Ctl& ctl, uint64_t timeout_ns, PanelCount& pc, int u, float (&acc)[MT][NT][4]) {
+        constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kPanelStages = kPanelK / NT / W::kStageK;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        const int groups = (((job.K + W::kChunk - 1) / W::kChunk - 1) >> job.chunk_shift) + 1;
+        for (int seg = 0; seg < job.segments; ++seg) {
+            const uint16_t* sp[(MT + 1) / 2];
+            StageScales<Job::kWK, MT> next;
+            if constexpr (W::kQ4) {
+                job.scales(u, seg, tile, g, t, sp);
+                load_scales<Job::kWK, MT>(next, sp, split, groups, job.chunk_shift);
+            }
+            int st = split;
+            for (int p0 = 0; p0 < stages; p0 += kPanelStages, ++pc.n) {
+                const int buf = pc.buf(), end = min(p0 + kPanelStages, stages);
+                if (!mbar_wait_bounded(ctl, &s.full[buf], pc.parity(), timeout_ns)) return false;
+                const unsigned char* tok = s.base + buf * kPanelBytes + g * kPitch + t * W::kLaneK * 2;
+                for (; st < end; st += job.splits) {
+                    const StageScales<Job::kWK, MT> sc = next;
+                    if constexpr (W::kQ4) load_scales<Job::kWK, MT>(next, sp, st + job.splits, groups, job.chunk_shift);
+                    cp_async_wait<kRing - 2>();
+                    __syncwarp();  // the stage is in for every lane, and the slot refilled next has been read
+                    fetch();
+                    use_stage<Job::kWK, MT, NT>(acc, s.base + s.rings + (warp * kRing + slot) * (MT * 1024), sc,
+                                                tok + (st - p0) * (W::kStageK * 2), g, t, qc);
+                    slot = slot + 1 == kRing ? 0 : slot + 1;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.empty[buf]);
+            }
+        }
+        return true;
+    }
+
+    // Waits for the warp's copies in flight (none after a whole sequence but empty groups).
+    __device__ __forceinline__ void drain() { cp_async_wait<0>(); }
+};
+
+__device__ __forceinline__ void sync_multipliers() { asm volatile("bar.sync 1, %0;" :: "n"(kProdWarps * 32) : "memory"); }
+
+// Calls out(row tile group, row, token, value) for every finished sum of the CTA's unit: row of the 16 MT of a
+// group of row tiles, token below 8 NT. With one warp per group straight from its registers; otherwise the
+// warps' sums meet in shared memory and are added in warp order. PAIR: value2 is the sum 8 rows below, for
+// rows with bit 3 clear (the others are not called).
+template <bool PAIR, int MT, int NT, typename Out>
+__device__ __forceinline__ void finish_unit(const ProductSmem& s, int splits, const float (&acc)[MT][NT][4], Out out) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    if (splits == 1) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = n * 8 + 2 * t + j;
+                    if constexpr (PAIR) {
+                        out(warp, m * 16 + g, c, acc[m][n][j], acc[m][n][2 + j]);
+                    } else {
+                        out(warp, m * 16 + g, c, acc[m][n][j], 0.0f);
+                        out(warp, m * 16 + 8 + g, c, acc[m][n][2 + j], 0.0f);
+                    }
+                }
+        return;
+    }
+    float* sums = reinterpret_cast<float*>(s.base + s.sums);
+    constexpr int NB = NT < kSumTokens / 8 ? NT : kSumTokens / 8;  // token tiles at a time
+#pragma unroll
+    for (int n0 = 0; n0 < NT; n0 += NB) {
+        sync_multipliers();  // the last exchange has been read
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sums[(((warp * MT + m) * NB + n) * 4 + i) * 32 + lane] = acc[m][n0 + n][i];
+        sync_multipliers();
+        constexpr int kPerGroup = MT * NB * 2 * 32 * (PAIR ? 1 : 2);  // sums of a group of row tiles
+        const int all = kProdWarps / splits * kPerGroup;
+        for (int e = threadIdx.x; e < all; e += kProdWarps * 32) {
+            const int q = e / kPerGroup, rest = e % kPerGroup, ln = rest % 32, reg = rest / 32;
+            const int j = reg % 2, half = PAIR ? 0 : reg / 2 % 2, n = reg / (PAIR ? 2 : 4) % NB, m = reg / (PAIR ? 2 : 4) / NB;
+            const float* at = sums + (((q * splits * MT + m) * NB + n) * 4 + half * 2 + j) * 32 + ln;
+            float v = 0.0f, v2 = 0.0f;
+            for (int w = 0; w < splits; ++w) {
+                v += at[w * (MT * NB * 128)];
+                if (PAIR) v2 += at[w * (MT * NB * 128) + 64];
+            }
+            out(q, m * 16 + half * 8 + ln / 4, (n0 + n) * 8 + ln % 4 * 2 + j, v, v2);
         }
     }
 }

@@ -7,6 +7,7 @@ creating a communicator raises.
 """
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsimcomm.so")
@@ -106,12 +107,13 @@ def load_library(path=LIB_PATH):
     pp = ctypes.POINTER(ctypes.c_void_p)
     L.coll_moe_dispatch.argtypes = [vp, pp, pp, sz, i32, sz, i32, i32, pp, sz, pp, vp, vp, vp]
     L.coll_moe_combine.argtypes = [vp, pp, sz, pp, pp, pp, pp, sz, i32, sz, i32, i32, pp, vp]
-    L.coll_moe_route.argtypes = [vp, pp, sz, i32, i32, i32, i32, pp, pp, vp]
-    L.coll_moe_route_backward.argtypes = [vp, pp, pp, pp, sz, i32, i32, i32, i32, pp, vp]
-    L.coll_linear_w4.argtypes = [vp, pp, pp, pp, sz, sz, sz, i32, i32, i32, pp, vp]
-    L.coll_moe_layer.argtypes = [vp, pp, pp, pp, pp, sz, i32, sz, sz, i32, i32, i32, pp, pp, pp, pp, i32, pp, vp]
-    L.coll_logprobs.argtypes = [vp, pp, sz, vp, sz, sz, i32, pp, pp, pp, i32, pp, pp, vp]
-    L.coll_logprobs_backward.argtypes = [vp, pp, sz, vp, sz, sz, i32, pp, pp, vp, vp, pp, sz, vp]
+    pa = vp  # a HOST array of pointers, given as the bytes of SimComm._tensors
+    L.coll_moe_route.argtypes = [vp, pa, sz, i32, i32, i32, i32, pa, pa, vp]
+    L.coll_moe_route_backward.argtypes = [vp, pa, pa, pa, sz, i32, i32, i32, i32, pa, vp]
+    L.coll_linear_w4.argtypes = [vp, pa, pa, pa, sz, sz, sz, i32, i32, i32, pa, vp]
+    L.coll_moe_layer.argtypes = [vp, pa, pa, pa, pa, sz, i32, sz, sz, i32, i32, i32, pa, pa, pa, pa, i32, pa, vp]
+    L.coll_logprobs.argtypes = [vp, pa, sz, vp, sz, sz, i32, pa, pa, pa, i32, pa, pa, vp]
+    L.coll_logprobs_backward.argtypes = [vp, pa, sz, vp, sz, sz, i32, pa, pa, vp, vp, pa, sz, vp]
     for name in ("coll_moe_route", "coll_moe_route_backward", "coll_linear_w4", "coll_moe_layer", "coll_logprobs",
                  "coll_logprobs_backward"):
         getattr(L, name).restype = st
@@ -162,7 +164,9 @@ class SimComm:
         self.p = int(p)
         self.rank = None if rank is None else int(rank)
         import torch
+        self._torch = torch
         self._device = torch.cuda.current_device()
+        self._pack = struct.Struct(f"{self.p}P").pack
 
     # -- lifecycle ---------------------------------------------------------------------------------
     def close(self):
@@ -333,22 +337,31 @@ class SimComm:
 
     # -- router, products with sharded weights, log probabilities ------------------------------------
     def _tensors(self, what, tensors, dtype, numel, row=None, one=False):
-        """HOST array of the ranks' device pointers, after checking that every tensor is where and what
+        """HOST array of the ranks' device pointers (its bytes), after checking that every tensor is where and what
         the kernels take it for: on the communicator's device, of `dtype` (a torch dtype), `numel`
         elements, contiguous (or, with `row` = (ld, columns), rows at that distance). A rank view's
         entries of other ranks may be None or addresses. `one`: a single tensor, its address."""
         if tensors is None:
             return None
+        dev = self._device
+        if not one:
+            try:  # the usual call in one sweep; anything else takes the slow way, which says what is wrong
+                out = [t.data_ptr() for t in tensors
+                       if t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous()]
+            except AttributeError:
+                out = ()
+            if len(out) == self.p == len(tensors) and (row is None or row[0] == row[1]):
+                return self._pack(*out)
         out = []
         for t in ((tensors,) if one else tensors):
             if t is None or isinstance(t, int):
                 if self.rank is None:
                     raise TypeError(f"{what}: a tensor for every rank is needed")
-                out.append(t)
+                out.append(t or 0)
                 continue
             if t.dtype is not dtype:
                 raise TypeError(f"{what}: {t.dtype}, not {dtype}")
-            if t.get_device() != self._device:
+            if t.get_device() != dev:
                 raise ValueError(f"{what}: on {t.device}, not on the communicator's device")
             if row is not None and t.shape[0] > 1:
                 if t.numel() != numel or t.stride(1) != 1 or t.stride(0) != row[0]:
@@ -360,7 +373,13 @@ class SimComm:
             return out[0]
         if len(out) != self.p:
             raise ValueError(f"{what}: {len(out)} entries for {self.p} ranks")
-        return (ctypes.c_void_p * self.p)(*out)
+        return self._pack(*out)
+
+    def _launch_stream(self, stream):
+        """The stream's handle; by default the current stream of the communicator's device."""
+        if stream is None:
+            return self._torch._C._cuda_getCurrentRawStream(self._device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _own(self, tensors):
         """A tensor of this handle's own ranks, whose shape and type stand for all."""
@@ -370,19 +389,19 @@ class SimComm:
         """Softmax over logits[i] [T][E] (fp32 or bf16), the k best experts of every token into topk_idx[i]
         [T][k] int32 and their weights (shares of the k when `normalise`) into topk_weight[i] [T][k] fp32:
         what moe_dispatch, moe_combine and moe_layer take."""
-        import torch
+        torch = self._torch
         x = self._own(logits)
         T, E = x.shape
         k = self._own(topk_idx).shape[1]
         self._check(self._L.coll_moe_route(
             self._h, self._tensors("logits", logits, x.dtype, T * E), T, k, E, DTYPES[_dtype_of(x)], 1 if normalise else 0,
             self._tensors("topk_idx", topk_idx, torch.int32, T * k),
-            self._tensors("topk_weight", topk_weight, torch.float32, T * k), _stream(stream)))
+            self._tensors("topk_weight", topk_weight, torch.float32, T * k), self._launch_stream(stream)))
 
     def moe_route_backward(self, logits, topk_idx, grad_weight, grad_logits, normalise=True, stream=None):
         """Gradient of moe_route's scores into grad_logits[i] [T][E] (of the scores' type), from grad_weight[i]
         [T][k] fp32, the gradient of its weights."""
-        import torch
+        torch = self._torch
         x = self._own(logits)
         T, E = x.shape
         k = self._own(topk_idx).shape[1]
@@ -390,14 +409,14 @@ class SimComm:
             self._h, self._tensors("logits", logits, x.dtype, T * E),
             self._tensors("topk_idx", topk_idx, torch.int32, T * k),
             self._tensors("grad_weight", grad_weight, torch.float32, T * k), T, k, E, DTYPES[_dtype_of(x)],
-            1 if normalise else 0, self._tensors("grad_logits", grad_logits, x.dtype, T * E), _stream(stream)))
+            1 if normalise else 0, self._tensors("grad_logits", grad_logits, x.dtype, T * E), self._launch_stream(stream)))
 
     def linear_w4(self, x, w, scale, out, parallel="row", stream=None):
         """out = x W^T for few tokens, W of 4-bit weights (q - 8) * scale: w[r] uint8 [N_r][K_r/2] (element 2i in
         the low half of byte i), scale[r] bf16 [N_r][K_r/group], x[r] bf16 [T][K_r]. parallel "column": the
         ranks hold rows of W and out[r] is [T][N/p]; "row": they hold columns, the partial products are summed
         and every out[r] is [T][N]. out fp32 or bf16."""
-        import torch
+        torch = self._torch
         if parallel not in PARALLEL:
             raise ValueError(f"parallel must be one of {sorted(PARALLEL)}")
         o = self._own(out)
@@ -411,7 +430,7 @@ class SimComm:
             self._h, self._tensors("x", x, torch.bfloat16, T * K), self._tensors("w", w, torch.uint8, N * (K // 2)),
             self._tensors("scale", scale, torch.bfloat16, N * groups), T, N if row else N * self.p,
             K * self.p if row else K, K // groups, PARALLEL[parallel], DTYPES[_dtype_of(o)],
-            self._tensors("out", out, o.dtype, T * N), _stream(stream)))
+            self._tensors("out", out, o.dtype, T * N), self._launch_stream(stream)))
 
     def moe_layer(self, x, topk_idx, topk_weight, experts, w_up, w_down, out, up_scale=None, down_scale=None,
                   residual=None, stream=None):
@@ -419,7 +438,7 @@ class SimComm:
         (U_e x)). x, residual, out bf16 [T][H]; w_up[j] [E/p][2F][H] (G's rows, then U's) and w_down[j]
         [E/p][H][F] bf16, or, with up_scale [E/p][2F][H/group] and down_scale [E/p][H][F/group] (bf16), 4-bit:
         uint8 with half as many columns."""
-        import torch
+        torch = self._torch
         T, H = self._own(x).shape
         k = self._own(topk_idx).shape[1]
         el, rows = self._own(w_up).shape[:2]
@@ -441,7 +460,7 @@ class SimComm:
             self._tensors("topk_weight", topk_weight, torch.float32, T * k),
             self._tensors("residual", residual, torch.bfloat16, T * H), T, k, H, F, int(experts), 1 if q4 else 0, group,
             self._tensors("w_up", w_up, wt, 2 * n), su, self._tensors("w_down", w_down, wt, n), sd, DTYPES["bf16"],
-            self._tensors("out", out, torch.bfloat16, T * H), _stream(stream)))
+            self._tensors("out", out, torch.bfloat16, T * H), self._launch_stream(stream)))
 
     def logprobs(self, logits, tokens, vocab, logprob, entropy=None, lse=None, top_idx=None, top_logprob=None,
                  stream=None):
@@ -449,7 +468,7 @@ class SimComm:
         sharded over the ranks: logits[r] [R][m], m = ceil(vocab / p), fp32 or bf16, rows at any distance. Every
         rank gets logprob[r], entropy[r], lse[r] fp32 [R] and the n best columns and their log probabilities
         in top_idx[r] int32 and top_logprob[r] fp32 [R][n]."""
-        import torch
+        torch = self._torch
         x = self._own(logits)
         R, m = x.shape
         if m != -(-int(vocab) // self.p):
@@ -464,14 +483,14 @@ class SimComm:
             self._tensors("tokens", tokens, torch.int32, R, one=True), R, int(vocab), DTYPES[_dtype_of(x)],
             self._tensors("logprob", logprob, f, R), self._tensors("entropy", entropy, f, R),
             self._tensors("lse", lse, f, R), n, self._tensors("top_idx", top_idx, torch.int32, R * n),
-            self._tensors("top_logprob", top_logprob, f, R * n), _stream(stream)))
+            self._tensors("top_logprob", top_logprob, f, R * n), self._launch_stream(stream)))
 
     def logprobs_backward(self, logits, tokens, vocab, lse, grad_logprob, grad_logits, entropy=None,
                           grad_entropy=None, stream=None):
         """Gradient of logprobs' scores into grad_logits[r] [R][m] (of the scores' type, zeros in padding
         columns), from grad_logprob and grad_entropy (fp32 [R], the latter with `entropy`) and the forward
         call's lse[r] and entropy[r]."""
-        import torch
+        torch = self._torch
         x, g = self._own(logits), self._own(grad_logits)
         R, m = x.shape
         if m != -(-int(vocab) // self.p):
@@ -486,7 +505,7 @@ class SimComm:
             self._tensors("lse", lse, f, R), self._tensors("entropy", entropy, f, R),
             self._tensors("grad_logprob", grad_logprob, f, R, one=True),
             None if grad_entropy is None else self._tensors("grad_entropy", grad_entropy, f, R, one=True),
-            self._tensors("grad_logits", grad_logits, x.dtype, R * m, row=(ldg, m)), ldg, _stream(stream)))
+            self._tensors("grad_logits", grad_logits, x.dtype, R * m, row=(ldg, m)), ldg, self._launch_stream(stream)))
 
 
 def allreduce_ring_noalloc(sends, recvs, op="sum", n=None, dtype=None, status=None, stream=None):
