@@ -64,6 +64,7 @@ struct sim_comm {
     long long ring_task_bytes = 0;  // bytes of the wire type one ring / tree task moves; 0 = by message size
     long long moe_tma = 0;          // MoE dispatch copy: 0 loads and stores (faster, measured), 1 bulk copies
     long long moe_fused = 1;        // MoE dispatch: 1 one cooperative kernel, 0 three kernels
+    long long moe_layer_tensor = -1;  // expert layer: -1 by the number of assignments, 0 streamed, 1 tensor kernel
     unsigned long long launches = 0;
     int ring_ctas_max = 0;
     bool capturing = false;               // the current call's stream is being captured into a graph
@@ -773,7 +774,8 @@ uint32_t chunks_of(size_t seg, size_t chunk) { return uint32_t(std::max<size_t>(
 
 constexpr const char* kOptionKeys[] = {"chunk_bytes", "ring_ctas", "ring_task_bytes", "timeout_ns",
                                        "fault_skip_rank", "copy_variant", "copy_order", "direct_pack",
-                                       "direct_ctas_per_sm", "l2_hint", "moe_tma", "moe_fused", "trace"};
+                                       "direct_ctas_per_sm", "l2_hint", "moe_tma", "moe_fused", "moe_layer_tensor",
+                                       "trace"};
 
 coll_status_t set_option_impl(sim_comm* c, const char* key, long long value) {
     std::string k(key);
@@ -815,6 +817,9 @@ coll_status_t set_option_impl(sim_comm* c, const char* key, long long value) {
     } else if (k == "moe_fused") {
         if (value != 0 && value != 1) return fail(COLL_ERR_INVALID_ARG, "moe_fused must be 0 or 1");
         c->moe_fused = value;
+    } else if (k == "moe_layer_tensor") {
+        if (value < -1 || value > 1) return fail(COLL_ERR_INVALID_ARG, "moe_layer_tensor must be -1, 0 or 1");
+        c->moe_layer_tensor = value;
     } else if (k == "trace") {
         if (value != 0 && value != 1) return fail(COLL_ERR_INVALID_ARG, "trace must be 0 or 1");
         c->trace = value;
@@ -1114,6 +1119,7 @@ coll_status_t sim_comm_get_option(sim_comm_t c, const char* key, long long* valu
     else if (k == "direct_ctas_per_sm") *value = c->direct_ctas_per_sm;
     else if (k == "moe_tma") *value = c->moe_tma;
     else if (k == "moe_fused") *value = c->moe_fused;
+    else if (k == "moe_layer_tensor") *value = c->moe_layer_tensor;
     else if (k == "ring_task_bytes") *value = c->ring_task_bytes;
     else if (k == "trace") *value = c->trace;
     else return fail(COLL_ERR_INVALID_ARG, "unknown option " + k);
@@ -2005,6 +2011,7 @@ static coll_status_t coll_moe_layer_impl(sim_comm_t c, const void* const* x, con
     a.weight_kind = int(weight);
     a.group_shift = shift;
     a.vec = vec ? 1 : 0;
+    a.tensor = int(c->moe_layer_tensor);
     a.T = tokens;
     a.h_stride = round_up(ffn, 8);
     const size_t b_h = align_up(A * a.h_stride * 2, 256);

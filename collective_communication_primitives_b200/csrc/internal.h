@@ -291,6 +291,7 @@ struct MoeLayerArgs {
     int weight_kind;                     // coll_weight_t
     int group_shift;
     int vec;                             // every row is whole 16-byte units at an aligned address
+    int tensor;                          // option moe_layer_tensor
     int splits_up, splits_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
     size_t T;
     uint16_t* h;                         // scratch: bf16 [A][h_stride]

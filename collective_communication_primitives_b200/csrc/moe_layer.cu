@@ -19,140 +19,12 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "moe_layer.cuh"
 #include "wprod.cuh"
 
 namespace simcomm {
 
 constexpr int kLayTokens = 32;  // assignments of an expert that one unit covers
-
-__device__ __forceinline__ bool layer_barrier(const MoeLayerArgs& a, uint32_t k, bool ok) {
-    __shared__ int s_ok;
-    if (!__syncthreads_and(ok)) return false;  // a wait ran out: the status is set
-    if (threadIdx.x == 0) {
-        red_release_add_gpu(&a.st->layer_ctr, 1u);
-        const uint32_t want = k * gridDim.x;
-        s_ok = wait_counter(a.ctl, &a.st->layer_ctr, want, a.timeout_ns) && !status_failed(a.ctl);
-    }
-    __syncthreads();
-    return s_ok != 0;
-}
-
-struct LayerLists {
-    int* offset;      // [E] while counting: count, then next free place of the expert in list
-    int* act_start;   // [nact + 1] first place of the i-th picked expert in list
-    int* act_tile;    // [nact + 1] its first token tile
-    uint16_t* act;    // [nact] its id
-    uint16_t* list;   // [A] assignments, expert by expert
-};
-
-__device__ __forceinline__ int warp_incl_sum(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
-}
-
-// Exclusive prefix over the CTA of three counts per thread; their totals in tot.
-__device__ __forceinline__ void cta_prefix3(int (&v)[3], int (&tot)[3]) {
-    constexpr int kWarps = kProdThreads / 32;
-    __shared__ int s_w[3][kWarps];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int incl[3];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        incl[q] = warp_incl_sum(v[q], lane);
-        if (lane == 31) s_w[q][warp] = incl[q];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-        int before = 0;
-        tot[q] = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s_w[q][w];
-            tot[q] += s_w[q][w];
-        }
-        v[q] = before + incl[q] - v[q];
-    }
-    __syncthreads();
-}
-
-// Phase 0. Returns the number of picked experts, or -1 after an expert id out of range.
-__device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const LayerLists& l) {
-    __shared__ int s_bad;
-    const int per = int(a.T) * a.k;
-    for (int e = threadIdx.x; e < a.E; e += kProdThreads) l.offset[e] = 0;
-    if (threadIdx.x == 0) s_bad = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.A; i += kProdThreads) {
-        const int e = a.idx[a.rank0 + i / per][i % per];
-        if (e < 0 || e >= a.E) s_bad = 1;
-        else atomicAdd(&l.offset[e], 1);
-    }
-    __syncthreads();
-    if (s_bad) {
-        if (threadIdx.x == 0) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
-        return -1;
-    }
-    const int share = (a.E + kProdThreads - 1) / kProdThreads;
-    const int e0 = min(a.E, int(threadIdx.x) * share), e1 = min(a.E, e0 + share);
-    int v[3] = {0, 0, 0}, tot[3];
-    for (int e = e0; e < e1; ++e) {
-        const int c = l.offset[e];
-        v[0] += c > 0;
-        v[1] += c;
-        v[2] += (c + kLayTokens - 1) / kLayTokens;
-    }
-    cta_prefix3(v, tot);
-    for (int e = e0; e < e1; ++e) {
-        const int c = l.offset[e];
-        l.offset[e] = v[1];
-        if (c == 0) continue;
-        l.act[v[0]] = uint16_t(e);
-        l.act_start[v[0]] = v[1];
-        l.act_tile[v[0]] = v[2];
-        v[0] += 1;
-        v[1] += c;
-        v[2] += (c + kLayTokens - 1) / kLayTokens;
-    }
-    if (threadIdx.x == 0) {
-        l.act_start[tot[0]] = tot[1];
-        l.act_tile[tot[0]] = tot[2];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.A; i += kProdThreads)
-        l.list[atomicAdd(&l.offset[a.idx[a.rank0 + i / per][i % per]], 1)] = uint16_t(i);
-    __syncthreads();
-    // The atomics leave an expert's assignments in an order that differs from CTA to CTA. That does not
-    // matter inside one token tile (an assignment's result does not depend on its column), but every CTA
-    // must cut an expert's assignments into the same tiles: those with more than one are put in order, a
-    // warp per expert, by a bitmap of the assignments.
-    __shared__ uint32_t s_bits[kProdThreads / 32][kLayerMaxAssignments / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t* bits = s_bits[warp];
-    constexpr int kWords = kLayerMaxAssignments / 32 / 32;  // bitmap words per lane
-    for (int q = warp; q < tot[0]; q += kProdThreads / 32) {
-        const int start = l.act_start[q], n = l.act_start[q + 1] - start;
-        if (n <= kLayTokens) continue;
-        for (int w = lane; w < kLayerMaxAssignments / 32; w += 32) bits[w] = 0u;
-        __syncwarp();
-        for (int i = lane; i < n; i += 32) atomicOr(&bits[l.list[start + i] >> 5], 1u << (l.list[start + i] & 31));
-        __syncwarp();
-        int mine = 0;
-        for (int w = 0; w < kWords; ++w) mine += __popc(bits[lane * kWords + w]);
-        int at = start + warp_incl_sum(mine, lane) - mine;
-        for (int w = 0; w < kWords; ++w)
-            for (uint32_t b = bits[lane * kWords + w]; b; b &= b - 1)
-                l.list[at++] = uint16_t((lane * kWords + w) * 32 + __ffs(b) - 1);
-        __syncwarp();
-    }
-    __syncthreads();
-    return tot[0];
-}
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
 // The units of phase 1 (UP) or 2: (picked expert, block of row tiles, up to 32 of its assignments). A warp's
 // two row tiles hold rows f..f+7 of G in their upper and of U in their lower halves (UP), or 32 rows of D.
@@ -273,16 +145,10 @@ __global__ void __launch_bounds__(kProdThreads, 2) k_moe_layer(const __grid_cons
     if (threadIdx.x == 0) s_fail = status_failed(a.ctl);
     __syncthreads();
     if (s_fail) return;
-    const int most = min(a.E, a.A);
-    LayerLists l;
-    l.offset = reinterpret_cast<int*>(s_raw + product_smem<kLayTiles>());
-    l.act_start = l.offset + a.E;
-    l.act_tile = l.act_start + most + 1;
-    l.act = reinterpret_cast<uint16_t*>(l.act_tile + most + 1);
-    l.list = l.act + most;
+    const LayerLists l = layer_lists(a, s_raw + product_smem<kLayTiles>());
     const ProductSmem s = product_layout<kLayTiles>(s_raw);
     if (threadIdx.x == 0) init_panels(s);
-    const int nact = sort_assignments(a, l);
+    const int nact = sort_assignments<kProdThreads>(a, l, kLayTokens);
     if (nact < 0) return;
     PanelCount pc;
     bool ok = layer_phase<WK, VEC, true>(a, l, s, pc, nact);
@@ -292,34 +158,14 @@ __global__ void __launch_bounds__(kProdThreads, 2) k_moe_layer(const __grid_cons
     }
     ok = layer_phase<WK, VEC, false>(a, l, s, pc, nact);
     if (!layer_barrier(a, 2, ok)) return;
-    // the weighted sum: a thread per token and column
-    const int tokens = a.A / a.k;
-    const size_t total = size_t(tokens) * a.H;
-    for (size_t i = size_t(blockIdx.x) * kProdThreads + threadIdx.x; i < total; i += size_t(gridDim.x) * kProdThreads) {
-        const int tok = int(i / a.H), col = int(i % a.H);
-        const int rank = a.rank0 + tok / int(a.T);
-        const size_t at = size_t(tok % int(a.T)) * a.H + col;
-        const float* w = a.weight[rank] + size_t(tok % int(a.T)) * a.k;
-        const float* y = a.y + size_t(tok) * a.k * a.H + col;
-        float v = a.has_res ? bf16_bits_to_float(a.res[rank][at]) : 0.0f;
-        for (int s = 0; s < a.k; ++s) {
-            const float term = w[s] * y[size_t(s) * a.H];
-            v = (s == 0 && !a.has_res) ? term : v + term;
-        }
-        a.out[rank][at] = float_to_bf16_bits(v);
-    }
+    weighted_sum<kProdThreads>(a);
     __syncthreads();
     if (threadIdx.x == 0) leave_tasks(&a.st->layer_ctr, &a.st->layer_done);
 }
 
-static size_t moe_layer_lists_bytes(int E, int A) {
-    const size_t most = size_t(std::min(E, A));
-    return size_t(E) * 4 + (most + 1) * 8 + most * 2 + size_t(A) * 2;
-}
-
 template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int num_sms, cudaStream_t s) {
     auto* kernel = k_moe_layer<WK, VEC>;
-    const size_t smem = product_smem<kLayTiles>() + moe_layer_lists_bytes(a.E, a.A);
+    const size_t smem = product_smem<kLayTiles>() + layer_lists_bytes(a.E, a.A);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     int per_sm = 0;
@@ -347,8 +193,16 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The kernel on the fifth-generation tensor cores needs bf16 weights and rows of 16-byte units. By itself it is
+// taken from TODO assignments per expert up.
+static bool layer_takes_tensor(const MoeLayerArgs& a) {
+    if (a.tensor == 0 || a.weight_kind != COLL_WEIGHT_BF16 || !a.vec || !layer_tensor_fits(a)) return false;
+    return a.tensor == 1 || a.A >= 8 * a.E;
+}
+
 cudaError_t launch_moe_layer(const MoeLayerArgs& args, int num_sms, cudaStream_t s) {
     MoeLayerArgs a = args;
+    if (layer_takes_tensor(a)) return launch_layer_tensor(a, num_sms, s);
     if (a.weight_kind == 0)
         return a.vec ? launch_layer<W_BF16, true>(a, num_sms, s) : launch_layer<W_BF16, false>(a, num_sms, s);
     const int group = 1 << a.group_shift;

@@ -227,6 +227,9 @@ const char* coll_status_string(coll_status_t status);
  *   "moe_tma"      copy kernel of the three-kernel coll_moe_dispatch: 0 = 32/16-byte loads and stores
  *                  (default, measured faster), 1 = bulk copies through shared memory (rows of whole
  *                  16-byte units at 16-byte aligned bases; otherwise the load/store kernel runs)
+ *   "moe_layer_tensor"  products of coll_moe_layer with bf16 weights in rows of 16-byte units: 1 = on the
+ *                  tcgen05 tensor cores, 0 = streamed through the warps' matrix instructions, -1 = by the
+ *                  number of assignments per expert (default)
  *   "trace"        1 = keep a record of every call (sim_comm_trace_read), 0 = off (default).
  *                  Every entry point also opens an NVTX range named after its collective, whatever
  *                  this option says (a no-op unless a profiler collects NVTX).

@@ -108,6 +108,38 @@ def test_layer(p, T, E, k, H, F, group, residual):
     a.check()
 
 
+TENSOR_CASES = [
+    # p, T, E, k, H, F, residual: rows of 16-byte units
+    (1, 1, 1, 1, 8, 8, False), (1, 1, 8, 2, 64, 32, True), (2, 3, 8, 2, 40, 24, True), (8, 1, 64, 2, 256, 128, True),
+    (4, 9, 16, 4, 104, 72, False), (2, 40, 4, 3, 136, 88, True), (1, 300, 8, 4, 64, 48, True), (4, 33, 16, 4, 1000, 712, False),
+    (1, 700, 4, 4, 200, 264, True), (64, 1, 128, 8, 32, 16, True), (2, 64, 8, 8, 512, 384, True), (1, 20, 2, 1, 2048, 1024, True),
+]
+
+
+@pytest.mark.parametrize("p,T,E,k,H,F,residual", TENSOR_CASES)
+def test_layer_on_the_tensor_cores(p, T, E, k, H, F, residual):
+    a = Layer(p, T, E, k, H, F, 0, residual, seed=p + T + E + H)
+    with SC.SimComm(p) as c:
+        c.set_option("moe_layer_tensor", 1)
+        for _ in range(2):
+            a.run(c)
+            torch.cuda.synchronize()
+            assert c.async_error() == SC.OK
+            a.check()
+
+
+def test_both_kernels_take_turns_on_one_communicator():
+    a, b = Layer(2, 40, 4, 3, 136, 88, seed=1), Layer(2, 64, 8, 4, 256, 128, seed=2)
+    with SC.SimComm(2) as c:
+        for option in (0, 1, 0, 1, -1):
+            c.set_option("moe_layer_tensor", option)
+            for x in (a, b):
+                x.run(c)
+            torch.cuda.synchronize()
+            a.check()
+            b.check()
+
+
 @pytest.mark.parametrize("group", [0, 32])
 def test_every_token_on_one_expert_and_an_id_twice(group):
     T, E, k = 67, 8, 2
