@@ -292,6 +292,7 @@ struct MoeLayerArgs {
     int group_shift;
     int vec;                             // every row is whole 16-byte units at an aligned address
     int tensor;                          // option moe_layer_tensor
+    int tensor_ring;                     // set by the launcher: bytes of the tensor kernel's ring of stages
     int splits_up, splits_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
     size_t T;
     uint16_t* h;                         // scratch: bf16 [A][h_stride]

@@ -194,15 +194,19 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
 }
 
 // The kernel on the fifth-generation tensor cores needs bf16 weights and rows of 16-byte units. By itself it is
-// taken from TODO assignments per expert up.
-static bool layer_takes_tensor(const MoeLayerArgs& a) {
+// taken where its units of 128 rows give every third SM one. Its stages of 64 k's go by at 0.4 us at best, so that
+// it wants the work spread; measured on B200, streamed against tensor: 35 and 62 us with 2 picked experts of 4096 x
+// 2048 (32 units), 22 and 31 with 8 of 1024 x 512 (32), 40 and 37 with 8 of 1024 x 1024 (64), 82 and 45 with 16 of
+// 1000 x 712 and 33 assignments each (96), 153 and 144 with 16 of 4096 x 2048 (256), 1837 and 594 with 64 of
+// them and 64 assignments each.
+static bool layer_takes_tensor(const MoeLayerArgs& a, int num_sms) {
     if (a.tensor == 0 || a.weight_kind != COLL_WEIGHT_BF16 || !a.vec || !layer_tensor_fits(a)) return false;
-    return a.tensor == 1 || a.A >= 8 * a.E;
+    return a.tensor == 1 || std::min(a.E, a.A) * ((a.F + 127) / 128) >= num_sms / 3;
 }
 
 cudaError_t launch_moe_layer(const MoeLayerArgs& args, int num_sms, cudaStream_t s) {
     MoeLayerArgs a = args;
-    if (layer_takes_tensor(a)) return launch_layer_tensor(a, num_sms, s);
+    if (layer_takes_tensor(a, num_sms)) return launch_layer_tensor(a, num_sms, s);
     if (a.weight_kind == 0)
         return a.vec ? launch_layer<W_BF16, true>(a, num_sms, s) : launch_layer<W_BF16, false>(a, num_sms, s);
     const int group = 1 << a.group_shift;

@@ -26,9 +26,9 @@ constexpr int kTcThreads = (kTcEpilogue + 1 + kTcCopy) * 32;
 constexpr int kTcTokens = 128;                                    // assignments of a unit
 constexpr int kTcK = 64;                                          // k's of a stage
 constexpr int kTcTileBytes = 128 * kTcK * 2;                      // 128 rows of a stage
-template <int M> constexpr int tc_stages() { return M == 2 ? 4 : 6; }
-template <int M> constexpr int tc_stage_bytes() { return (M + 1) * kTcTileBytes; }  // weights, then tokens
-template <int M> constexpr int tc_smem() { return tc_stages<M>() * tc_stage_bytes<M>() + 1024; }  // and alignment
+constexpr int kTcTiles = 2;                                       // row tiles of a unit, at most
+constexpr int kTcStages = 16;                                     // stages, at most
+constexpr int kTcRing = 192 * 1024;                               // bytes of the ring of stages, at least
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -64,19 +64,24 @@ __device__ __forceinline__ void tc_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// Barriers of a CTA: stages copied and free, accumulators finished and read.
-template <int M> struct TcBars {
-    uint64_t full[tc_stages<M>()], empty[tc_stages<M>()], done[2], read[2];
+// Barriers of a CTA: stages copied and free, one set for each phase, accumulators finished and read.
+struct TcBars {
+    uint64_t full[2][kTcStages], empty[2][kTcStages], done[2], read[2];
 };
 
 // A unit: `span` rows from row0 of an expert's output, assignments [first, first + count). The span is a
 // multiple of 16, at most 64 M (UP) or 128 M rows.
-template <int M, bool UP> struct TcPhase {
+template <bool UP> struct TcPhase {
+    static constexpr int M = kTcTiles;
     const MoeLayerArgs& a;
     const LayerLists& l;
     int nact, K, rows, span, blocks;
+    // A stage: the span's weight rows (128 bytes each), then up to 128 token rows. A last row tile of fewer than
+    // 128 rows is read by the matrix instruction as if it were whole: what follows it in the ring gives rows of
+    // the accumulator that nobody reads. So small spans have short stages, and many of them.
+    int weight_bytes, slot_bytes, stages;
     static constexpr int kTile = UP ? 64 : 128;  // rows of the output in a row tile
-    __device__ __forceinline__ TcPhase(const MoeLayerArgs& a_, const LayerLists& l_, int n)
+    __device__ __forceinline__ TcPhase(const MoeLayerArgs& a_, const LayerLists& l_, int n, int most)
         : a(a_), l(l_), nact(n), K(UP ? a_.H : a_.F), rows(UP ? a_.F : a_.H) {
         // Where whole row tiles would leave CTAs without a unit, the smallest span that still takes one round.
         // With more units than CTAs whole tiles are best, ragged rounds and all: the CTAs of a last, partial round
@@ -87,6 +92,9 @@ template <int M, bool UP> struct TcPhase {
         span = kTile * M;
         while (span > 16 && (rows + span - 17) / (span - 16) * tiles <= grid) span -= 16;
         blocks = (rows + span - 1) / span;
+        weight_bytes = span * (UP ? 256 : 128);
+        slot_bytes = weight_bytes + min(kTcTokens / 16, (most + 15) / 16) * 2048;
+        stages = min(kTcStages, (a.tensor_ring - (weight_bytes % kTcTileBytes ? kTcTileBytes : 0)) / slot_bytes);
     }
     __device__ __forceinline__ int units() const { return l.act_tile[nact] * blocks; }
     __device__ __forceinline__ int row_tiles() const { return (span + kTile - 1) / kTile; }
@@ -108,19 +116,16 @@ template <int M, bool UP> struct TcPhase {
     }
 };
 
-// The copying warps' side of a phase. it: stages begun, the same count on every role's side.
-template <int M, bool UP>
-__device__ __forceinline__ bool tc_copy(const TcPhase<M, UP>& ph, uint32_t smem, TcBars<M>& bars, uint32_t& it) {
-    constexpr int S = tc_stages<M>(), kLag = S - 2;  // stages whose copies are in flight behind the newest
+// The copying warps' side of a phase.
+template <bool UP>
+__device__ __forceinline__ bool tc_copy(const TcPhase<UP>& ph, uint32_t smem, TcBars& bars) {
+    constexpr int M = kTcTiles;
     const MoeLayerArgs& a = ph.a;
+    uint64_t *full = bars.full[UP], *empty = bars.empty[UP];
     const int i = threadIdx.x - (kTcEpilogue + 1) * 32, c = i & 7, r0 = i >> 3;  // this thread's piece and first row
     const uint32_t off = uint32_t(r0 * 128 + ((c ^ (r0 & 7)) << 4));            // rows r0 + 16 j lie 2048 j further
-    uint32_t given = it;  // stages handed on
-    auto hand_on = [&]() {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tensor cores read what was copied
-        tc_arrive(&bars.full[given % S]);
-        ++given;
-    };
+    int slot = 0;
+    uint32_t parity = 1u;  // of the wait for a free slot: flips with each turn of the ring
     const int units = ph.units(), kbs = (ph.K + kTcK - 1) / kTcK;
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
@@ -157,9 +162,8 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<M, UP>& ph, uint32_t smem,
         // Every CTA begins at another k: rows are often a power of two apart, and CTAs that read the same columns of
         // their rows at the same time would keep asking the same part of the memory.
         const int turn = u * 5 % kbs;
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-            const uint32_t slot = it % S;
-            if (!mbar_wait_bounded(a.ctl, &bars.empty[slot], (it / S & 1u) ^ 1u, a.timeout_ns)) {
+        for (int kb = 0; kb < kbs; ++kb) {
+            if (!mbar_wait_bounded(a.ctl, &empty[slot], parity, a.timeout_ns)) {
                 ok = false;
                 break;
             }
@@ -167,7 +171,7 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<M, UP>& ph, uint32_t smem,
             const bool in = k * kTcK + c * 8 < ph.K;
             const size_t at = in ? size_t(k) * (kTcK * 2) : 0;
             const ptrdiff_t back = in ? 0 : -ptrdiff_t(c) * 16;  // past the end nothing is read; stay in the row
-            const uint32_t to = smem + slot * tc_stage_bytes<M>() + off, bytes = in ? 16u : 0u;
+            const uint32_t to = smem + slot * ph.slot_bytes + off, bytes = in ? 16u : 0u;
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -176,21 +180,21 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<M, UP>& ph, uint32_t smem,
                         tc_copy16(to + m * kTcTileBytes + j * 2048, w[m][j] + at + back, bytes);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < nb) tc_copy16(to + M * kTcTileBytes + j * 2048, b[j] + at + back, bytes);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (it - given >= uint32_t(kLag)) {
-                asm volatile("cp.async.wait_group %0;" :: "n"(kLag) : "memory");
-                hand_on();
+                if (j < nb) tc_copy16(to + ph.weight_bytes + j * 2048, b[j] + at + back, bytes);
+            // the barrier hears from this thread when its copies are in; many stages are in flight at a time
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full[slot])) : "memory");
+            if (++slot == ph.stages) {
+                slot = 0;
+                parity ^= 1u;
             }
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    while (ok && given != it) hand_on();
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return ok;
 }
 
 // Asks for the first weights of the next phase's first unit before the grid barrier: they do not depend on it.
-template <int M, bool UP> __device__ __forceinline__ void tc_prefetch(const TcPhase<M, UP>& ph) {
+template <bool UP> __device__ __forceinline__ void tc_prefetch(const TcPhase<UP>& ph) {
     constexpr int kLines = 6;  // of 128 bytes a row
     if (int(blockIdx.x) >= ph.units()) return;
     const MoeLayerArgs& a = ph.a;
@@ -207,11 +211,13 @@ template <int M, bool UP> __device__ __forceinline__ void tc_prefetch(const TcPh
 }
 
 // The issuing thread's side of a phase. acc: accumulators begun.
-template <int M, bool UP>
-__device__ __forceinline__ bool tc_issue(const TcPhase<M, UP>& ph, uint32_t smem, TcBars<M>& bars, uint32_t tmem, uint32_t& it,
-                                         uint32_t& acc) {
-    constexpr int S = tc_stages<M>();
+template <bool UP>
+__device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, TcBars& bars, uint32_t tmem, uint32_t& acc) {
+    constexpr int M = kTcTiles;
     const MoeLayerArgs& a = ph.a;
+    uint64_t *full = bars.full[UP], *empty = bars.empty[UP];
+    int slot = 0;
+    uint32_t parity = 0u;
     const int units = ph.units(), kbs = (ph.K + kTcK - 1) / kTcK, tiles = ph.row_tiles();
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++acc) {
         const int nb = (ph.at(u).count + 15) / 16;
@@ -220,18 +226,24 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<M, UP>& ph, uint32_t smem
         if (!mbar_wait_bounded(a.ctl, &bars.read[acc & 1], (acc / 2 & 1u) ^ 1u, a.timeout_ns)) return false;
         tc_fence_after();
         const uint32_t d = tmem + (acc & 1) * (M * 128);
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-            const uint32_t slot = it % S;
-            if (!mbar_wait_bounded(a.ctl, &bars.full[slot], it / S & 1u, a.timeout_ns)) return false;
+        for (int kb = 0; kb < kbs; ++kb) {
+            if (!mbar_wait_bounded(a.ctl, &full[slot], parity, a.timeout_ns)) return false;
+            // What the copies wrote is read through another path. The fence stands on this side: a copying thread's
+            // would wait for all its copies in flight, 0.7 us a stage.
+            fence_proxy_async_smem();
             tc_fence_after();
-            const uint32_t at = smem + slot * tc_stage_bytes<M>();
-            const uint64_t db = tc_desc(at + M * kTcTileBytes);
+            const uint32_t at = smem + slot * ph.slot_bytes;
+            const uint64_t db = tc_desc(at + ph.weight_bytes);
 #pragma unroll
             for (int kk = 0; kk < kTcK / 16; ++kk)  // 16 k's are 32 bytes further in the swizzled rows
 #pragma unroll
                 for (int m = 0; m < M; ++m)
                     if (m < tiles) tc_mma(d + m * 128, tc_desc(at + m * kTcTileBytes) + kk * 2, db + kk * 2, idesc, uint32_t(kb | kk));
-            tc_commit(&bars.empty[slot]);
+            tc_commit(&empty[slot]);
+            if (++slot == ph.stages) {
+                slot = 0;
+                parity ^= 1u;
+            }
         }
         tc_commit(&bars.done[acc & 1]);
     }
@@ -239,8 +251,9 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<M, UP>& ph, uint32_t smem
 }
 
 // The reading warps' side of a phase.
-template <int M, bool UP>
-__device__ __forceinline__ bool tc_finish(const TcPhase<M, UP>& ph, TcBars<M>& bars, uint32_t tmem, uint32_t& acc) {
+template <bool UP>
+__device__ __forceinline__ bool tc_finish(const TcPhase<UP>& ph, TcBars& bars, uint32_t tmem, uint32_t& acc) {
+    constexpr int M = kTcTiles;
     const MoeLayerArgs& a = ph.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, units = ph.units();
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++acc) {
@@ -280,21 +293,22 @@ __device__ __forceinline__ bool tc_finish(const TcPhase<M, UP>& ph, TcBars<M>& b
     return true;
 }
 
-template <int M> __global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(const __grid_constant__ MoeLayerArgs a) {
+__global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(const __grid_constant__ MoeLayerArgs a) {
     extern __shared__ unsigned char s_raw[];
-    __shared__ TcBars<M> bars;
+    __shared__ TcBars bars;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     const uint32_t smem = (smem_u32(s_raw) + 1023u) & ~1023u;  // the swizzle's period
-    const LayerLists l = layer_lists(a, s_raw + tc_smem<M>());
+    const LayerLists l = layer_lists(a, s_raw + a.tensor_ring + 1024);
     const int warp = threadIdx.x >> 5;
-    constexpr uint32_t kColumns = 2 * M * 128;
+    constexpr uint32_t kColumns = 2 * kTcTiles * 128;
     if (threadIdx.x == 0) {
         s_fail = status_failed(a.ctl);
-        for (int i = 0; i < tc_stages<M>(); ++i) {
-            mbar_init(&bars.full[i], kTcCopy * 32);
-            mbar_init(&bars.empty[i], 1);
-        }
+        for (int ph = 0; ph < 2; ++ph)
+            for (int i = 0; i < kTcStages; ++i) {
+                mbar_init(&bars.full[ph][i], kTcCopy * 32);
+                mbar_init(&bars.empty[ph][i], 1);
+            }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.done[i], 1);
             mbar_init(&bars.read[i], kTcEpilogue);
@@ -310,25 +324,32 @@ template <int M> __global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(c
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    int most = 0;  // assignments of the expert that has most
+    for (int q = threadIdx.x; q < nact; q += kTcThreads) most = max(most, l.act_start[q + 1] - l.act_start[q]);
+    __shared__ int s_most;
+    if (threadIdx.x == 0) s_most = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    atomicMax(&s_most, most);
+    __syncthreads();
+    most = s_most;
     const uint32_t tmem = s_tmem;
-    uint32_t it = 0, acc = 0;
+    uint32_t acc = 0;  // accumulators begun, the same count for the issuing thread and the reading warps
     auto phase = [&](const auto& ph) {
         bool ok = true;
         if (warp < kTcEpilogue) {
             ok = tc_finish(ph, bars, tmem, acc);
         } else if (warp == kTcEpilogue) {
-            if ((threadIdx.x & 31) == 0) ok = tc_issue(ph, smem, bars, tmem, it, acc);
+            if ((threadIdx.x & 31) == 0) ok = tc_issue(ph, smem, bars, tmem, acc);
             __syncwarp();
         } else {
-            ok = tc_copy(ph, smem, bars, it);
+            ok = tc_copy(ph, smem, bars);
         }
         return ok;
     };
-    bool ok = phase(TcPhase<M, true>(a, l, nact));
-    const TcPhase<M, false> down(a, l, nact);
+    bool ok = phase(TcPhase<true>(a, l, nact, most));
+    const TcPhase<false> down(a, l, nact, most);
     if (warp > kTcEpilogue) tc_prefetch(down);
     ok = layer_barrier(a, 1, ok);
     if (ok) ok = layer_barrier(a, 2, phase(down));
@@ -342,26 +363,25 @@ template <int M> __global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(c
     if (threadIdx.x == 0) leave_tasks(&a.st->layer_ctr, &a.st->layer_done);
 }
 
-template <int M> static cudaError_t launch_tensor(MoeLayerArgs& a, int num_sms, cudaStream_t s) {
-    auto* kernel = k_moe_tensor<M>;
-    const size_t smem = tc_smem<M>() + layer_lists_bytes(a.E, a.A);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+// Bytes left for the ring of stages beside the lists: a CTA has 227 KiB, 8 of them for the static part and alignment.
+static int tc_ring_bytes(const MoeLayerArgs& a) {
+    const long long left = 227 * 1024 - 8 * 1024 - (long long)layer_lists_bytes(a.E, a.A);
+    return left < kTcRing ? 0 : int(left / 1024 * 1024);
+}
+
+bool layer_tensor_fits(const MoeLayerArgs& a) { return tc_ring_bytes(a) > 0; }
+
+cudaError_t launch_layer_tensor(MoeLayerArgs a, int num_sms, cudaStream_t s) {
+    a.tensor_ring = tc_ring_bytes(a);
+    const size_t smem = size_t(a.tensor_ring) + 1024 + layer_lists_bytes(a.E, a.A);
+    cudaError_t e = cudaFuncSetAttribute(k_moe_tensor, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     // no more CTAs than there can be units of 16 rows
     const size_t units = (size_t(std::min(a.E, a.A)) + a.A / kTcTokens) * ((size_t(std::max(a.F, a.H)) + 15) / 16);
     dim3 grid(unsigned(std::max<size_t>(1, std::min<size_t>(num_sms, units)))), block(kTcThreads);
     void* args[] = {&a};
-    e = cudaLaunchCooperativeKernel(reinterpret_cast<void*>(kernel), grid, block, args, smem, s);
+    e = cudaLaunchCooperativeKernel(reinterpret_cast<void*>(k_moe_tensor), grid, block, args, smem, s);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-bool layer_tensor_fits(const MoeLayerArgs& a) {
-    constexpr size_t kMost = 227 * 1024 - 8 * 1024;  // of a CTA, without the static part
-    return tc_smem<2>() + layer_lists_bytes(a.E, a.A) <= kMost && tc_smem<1>() + layer_lists_bytes(a.E, a.A) <= kMost;
-}
-
-cudaError_t launch_layer_tensor(MoeLayerArgs a, int num_sms, cudaStream_t s) {
-    return launch_tensor<2>(a, num_sms, s);
 }
 
 }  // namespace simcomm
