@@ -1788,7 +1788,7 @@ void route_shape(sim_comm* c, RouteArgs& a, size_t tokens, int k, int experts, i
     a.E = experts;
     a.normalise = normalise != 0;
     a.T = tokens;
-    a.tokens = tokens * size_t(ranks_of(c));
+    a.ranks = ranks_of(c);
     a.ctl = make_ctl(c);
 }
 

@@ -247,7 +247,8 @@ struct RouteArgs {
     int k, E;
     int normalise;
     int vec;                             // rows of whole 16-byte units at aligned bases, E a multiple of 8
-    size_t T, tokens;                    // tokens per rank, in all
+    int ranks;
+    size_t T;                            // tokens per rank
     Ctl ctl;
 };
 

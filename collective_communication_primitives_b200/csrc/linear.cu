@@ -61,7 +61,7 @@ template <int WK, bool VEC, int MT, int NT> struct LinearJob {
 };
 
 template <int WK, bool VEC, int MT, int NT>
-__global__ void __launch_bounds__(kProdThreads, 2) k_linear_q4(const __grid_constant__ LinearArgs a) {
+__global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_constant__ LinearArgs a) {
     extern __shared__ __align__(128) unsigned char s_raw[];
     __shared__ int s_fail;
     const ProductSmem s = product_layout<MT>(s_raw);
@@ -103,7 +103,7 @@ template <int WK, int MT, int NT> static cudaError_t launch_linear_kind(const Li
     auto go = [&](auto kernel) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem<MT>());
         if (e != cudaSuccess) return e;
-        const unsigned grid = unsigned(std::min(a.units, 2 * num_sms));
+        const unsigned grid = unsigned(std::min(a.units, num_sms));
         kernel<<<grid, kProdThreads, product_smem<MT>(), s>>>(a);
         return cudaGetLastError();
     };
@@ -116,14 +116,14 @@ cudaError_t launch_linear(const LinearArgs& args, int num_sms, cudaStream_t s) {
     a.token_tiles = uint32_t((a.T + 8 * nt - 1) / (8 * nt));
     const size_t shards = a.row || a.view_rank >= 0 ? 1 : size_t(a.p);
     // Row tiles of a warp: more use every staged token more often, and as many as fill the GPU's warps.
-    const size_t units = (a.N + 15) / 16 * a.token_tiles * shards, warps = size_t(num_sms) * 2 * kProdWarps;
+    const size_t units = (a.N + 15) / 16 * a.token_tiles * shards, warps = size_t(num_sms) * kProdWarps;
     const int mt = units * 4 >= warps ? 2 : 1;
     const size_t tiles = (a.N + 16 * mt - 1) / (16 * mt), jobs = tiles * a.token_tiles * shards;
     // warps of a CTA on one row tile: more, the fewer tiles there are
     const int group = 1 << a.group_shift;
     const int stages = int(a.K / 128), panel = kPanelK / nt / 128;
     int splits = 1;
-    while (splits < std::min(kProdWarps, panel) && splits * 2 <= stages && jobs * splits < size_t(num_sms) * 2 * kProdWarps)
+    while (splits < std::min(kProdWarps, panel) && splits * 2 <= stages && jobs * splits < size_t(num_sms) * kProdWarps)
         splits *= 2;
     a.splits = splits;
     const size_t per = kProdWarps / splits;

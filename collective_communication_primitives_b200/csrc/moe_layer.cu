@@ -139,7 +139,7 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
 }
 
 template <int WK, bool VEC>
-__global__ void __launch_bounds__(kProdThreads, 2) k_moe_layer(const __grid_constant__ MoeLayerArgs a) {
+__global__ void __launch_bounds__(kProdThreads, 1) k_moe_layer(const __grid_constant__ MoeLayerArgs a) {
     extern __shared__ __align__(16) unsigned char s_raw[];
     __shared__ int s_fail;
     if (threadIdx.x == 0) s_fail = status_failed(a.ctl);

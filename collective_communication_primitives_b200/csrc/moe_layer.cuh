@@ -5,7 +5,7 @@
 
 namespace simcomm {
 
-constexpr int kMaxLayerWarps = 16;
+constexpr int kMaxLayerWarps = 17;
 
 __device__ __forceinline__ bool layer_barrier(const MoeLayerArgs& a, uint32_t k, bool ok) {
     __shared__ int s_ok;

@@ -99,177 +99,179 @@ template <int LPT, int VPL> __device__ __forceinline__ float softmax_terms(float
     return group_sum<LPT>(sum);
 }
 
-// A warp's tokens and their picks. Picks of consecutive tokens lie together in memory, so a warp's are moved
-// by all its lanes at once, through shared memory: [tokens of the warp][k] of each of up to three words.
+// A warp's tokens (of one rank: blockIdx.y) and their picks. Picks of consecutive tokens lie together in
+// memory, so a warp's are moved by all its lanes at once, through shared memory.
 template <int LPT> struct RouteWarp {
     static constexpr int kTokens = 32 / LPT;
-    int lane, sub, grp;
-    size_t first, token;  // the warp's first token, the group's
-    int count;            // tokens of the warp
+    int lane, sub, grp, rank;
+    uint32_t first, t;  // the warp's first token, the group's
+    int count;          // tokens of the warp
     bool live;
-    int rank;
-    size_t t;
-    uint32_t* picks;      // [3][kTokens * k]
 
-    __device__ __forceinline__ RouteWarp(const RouteArgs& a, uint32_t* smem) {
+    __device__ __forceinline__ RouteWarp(const RouteArgs& a) {
         lane = threadIdx.x & 31;
         sub = lane % LPT;
         grp = lane / LPT;
-        first = ((size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5) * kTokens;
-        token = first + grp;
-        count = first < a.tokens ? int(min(size_t(kTokens), a.tokens - first)) : 0;
-        live = token < a.tokens;
-        rank = a.rank0 + int(live ? token / a.T : 0);
-        t = live ? token % a.T : 0;
-        picks = smem + (threadIdx.x >> 5) * 3 * kTokens * a.k;
+        rank = a.rank0 + int(blockIdx.y);
+        const uint32_t T = uint32_t(a.T);  // tokens * k fits 31 bits
+        first = ((blockIdx.x * kRouteThreads + threadIdx.x) >> 5) * kTokens;
+        t = first + grp;
+        count = first < T ? int(min(uint32_t(kTokens), T - first)) : 0;
+        live = t < T;
     }
-    __device__ __forceinline__ uint32_t* word(const RouteArgs& a, int w) const { return picks + w * kTokens * a.k; }
-    // f(place in the warp's picks, rank, place in the rank's [T][k]) for every pick of the warp, spread over the lanes.
-    template <typename F> __device__ __forceinline__ void each_pick(const RouteArgs& a, F f) const {
-        const int n = count * a.k;
-        const size_t r0 = first / a.T, base = (first - r0 * a.T) * a.k, per = a.T * a.k;
-        for (int i = lane; i < n; i += 32) {  // a warp's tokens may run on into the next ranks
-            size_t at = base + i;
-            int r = a.rank0 + int(r0);
-            while (at >= per) {
-                at -= per;
-                ++r;
-            }
-            f(i, r, at);
-        }
-    }
+    __device__ __forceinline__ size_t pick0(const RouteArgs& a) const { return size_t(first) * a.k; }
 };
+
+// The score that an order key stands for (any NaN for a NaN's).
+__device__ __forceinline__ float key_score(uint32_t o) {
+    return o == 1u ? __int_as_float(0x7fffffff) : __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
 
 template <int DT, int LPT, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) k_route(const __grid_constant__ RouteArgs a) {
-    extern __shared__ uint32_t s_picks[];
+    extern __shared__ uint32_t s_picks[];  // [warps][ids, terms][tokens of a warp][k]
     if (status_failed(a.ctl)) return;
-    const RouteWarp<LPT> w(a, s_picks);
+    const RouteWarp<LPT> w(a);
     const unsigned gmask = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (w.grp * LPT);
-    const char* row = static_cast<const char*>(a.logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
+    const char* row = static_cast<const char*>(a.logits[w.rank]) + size_t(w.live ? w.t : 0) * a.E * Elem<DT>::kBytes;
     const int e0 = w.sub * VPL;
     float v[VPL];
     ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
+    // bf16 scores leave room for the id in the key: the upper half the score's order, the lower the id's complement
+    constexpr bool kPacked = DT == COLL_BF16;
     uint32_t key[VPL];
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = e0 + j < a.E ? order_key(v[j]) : 0u;
+    for (int j = 0; j < VPL; ++j) {
+        key[j] = e0 + j < a.E ? order_key(v[j]) : 0u;
+        if (kPacked && key[j]) key[j] = (max(key[j], 0x10000u) & 0xffff0000u) | uint32_t(0xffff - (e0 + j));
+    }
     float top;
     const float sum = softmax_terms<LPT, VPL>(v, &top);
-    uint32_t* ids = w.word(a, 0) + w.grp * a.k;
-    float* terms = reinterpret_cast<float*>(w.word(a, 1)) + w.grp * a.k;
-    float picked = 0.0f;  // sum of the picked terms, on every lane of the group
-    for (int s = 0; s < a.k; ++s) {
-        uint32_t best = key[0];
+    const float base = top == -INFINITY ? 0.0f : top;
+    const int n = w.kTokens * a.k;
+    uint32_t* all_ids = s_picks + (threadIdx.x >> 5) * 2 * n;
+    uint32_t* all_terms = all_ids + n;
+    uint32_t* ids = all_ids + w.grp * a.k;
+    uint32_t* terms = all_terms + w.grp * a.k;
+    uint32_t best = key[0];
 #pragma unroll
-        for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+    for (int s = 0; s < a.k; ++s) {
         const uint32_t all = group_umax<LPT>(best);
-        const int winner = __ffs(__ballot_sync(0xffffffffu, best == all) & gmask) - 1;
-        float term = 0.0f;
-        if (w.lane == winner) {
+        bool mine = best == all;
+        if constexpr (!kPacked) mine = w.lane == __ffs(__ballot_sync(0xffffffffu, mine) & gmask) - 1;
+        if (mine) {  // one lane of the group: takes the score out and looks for its next best
             int at = 0;
 #pragma unroll
             for (int j = VPL - 1; j >= 0; --j)
-                if (key[j] == all) {
-                    at = j;
-                    term = v[j];
-                }
+                if (key[j] == all) at = j;
+            best = 0u;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
+            for (int j = 0; j < VPL; ++j) {
                 if (j == at) key[j] = 0u;
+                best = max(best, key[j]);
+            }
             ids[s] = uint32_t(e0 + at);
-            terms[s] = term;
+            terms[s] = kPacked ? (all & 0xffff0000u) : all;
         }
-        __syncwarp();
     }
-    for (int s = 0; s < a.k; ++s) picked += terms[s];
-    const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
-    for (int s = w.sub; s < a.k; s += LPT) terms[s] = total == 0.0f ? 0.0f : terms[s] / total;
     __syncwarp();
-    const uint32_t* all_ids = w.word(a, 0);
-    const float* all_terms = reinterpret_cast<const float*>(w.word(a, 1));
-    w.each_pick(a, [&](int i, int r, size_t at) {
-        a.idx_out[r][at] = int32_t(all_ids[i]);
-        a.weight[r][at] = all_terms[i];
-    });
+    // the picks' terms: e^(score - max), from the keys
+    float picked = 0.0f;
+    for (int s = w.sub; s < a.k; s += LPT) {
+        uint32_t o = terms[s];
+        if (kPacked) o = o == 0x10000u ? 1u : o & 0x80000000u ? o : o | 0xffffu;  // a negative one's complement has zeros below
+        const float term = exp2_fast((key_score(o) - base) * kLog2e);
+        terms[s] = __float_as_uint(term);
+        picked += term;
+    }
+    picked = group_sum<LPT>(picked);
+    const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
+    for (int s = w.sub; s < a.k; s += LPT)
+        terms[s] = __float_as_uint(total == 0.0f ? 0.0f : __uint_as_float(terms[s]) / total);
+    __syncwarp();
+    for (int i = w.lane; i < w.count * a.k; i += 32) {
+        a.idx_out[w.rank][w.pick0(a) + i] = int32_t(all_ids[i]);
+        a.weight[w.rank][w.pick0(a) + i] = __uint_as_float(all_terms[i]);
+    }
 }
 
 template <int DT, int LPT, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_constant__ RouteArgs a) {
-    extern __shared__ uint32_t s_picks[];
+    // [warps][32 VPL] a number per score of the warp's tokens, then [warps][ids, g, score][tokens of a warp][k]
+    extern __shared__ __align__(16) uint32_t s_grad[];
     if (status_failed(a.ctl)) return;
-    const RouteWarp<LPT> w(a, s_picks);
-    const char* row = static_cast<const char*>(a.logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
-    const int e0 = w.sub * VPL;
-    float v[VPL], G[VPL];
+    const RouteWarp<LPT> w(a);
+    const char* row = static_cast<const char*>(a.logits[w.rank]) + size_t(w.live ? w.t : 0) * a.E * Elem<DT>::kBytes;
+    const int e0 = w.sub * VPL, warp = threadIdx.x >> 5;
+    float v[VPL];
     if (!a.normalise) ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
+    float* slots = reinterpret_cast<float*>(s_grad) + warp * 32 * VPL;  // scores of the group: [LPT * VPL]
+    const int n = w.kTokens * a.k;
+    uint32_t* ids_all = s_grad + kRouteThreads * VPL + warp * 3 * n;
+    float* g_all = reinterpret_cast<float*>(ids_all + n);
+    float* x_all = g_all + n;
     bool bad = false;
-    uint32_t* ids_all = w.word(a, 0);
-    float* g_all = reinterpret_cast<float*>(w.word(a, 1));
-    float* x_all = reinterpret_cast<float*>(w.word(a, 2));
-    w.each_pick(a, [&](int i, int r, size_t at) {
-        const int e = a.idx_in[r][at];
+    for (int i = w.lane; i < w.count * a.k; i += 32) {
+        const int e = a.idx_in[w.rank][w.pick0(a) + i];
         const bool ok = e >= 0 && e < a.E;
         bad = bad || !ok;
-        ids_all[i] = ok ? uint32_t(e) : 0xffffffffu;  // held by no lane
-        g_all[i] = a.grad_weight[r][at];
+        ids_all[i] = ok ? uint32_t(e) : 0u;
+        g_all[i] = ok ? a.grad_weight[w.rank][w.pick0(a) + i] : 0.0f;
         if (a.normalise)
-            x_all[i] = ok ? ld_score<DT>(static_cast<const char*>(a.logits[r]) + (at / a.k) * a.E * Elem<DT>::kBytes, e) : -INFINITY;
-    });
+            x_all[i] = ld_score<DT>(static_cast<const char*>(a.logits[w.rank]) + size_t(w.first + i / a.k) * a.E * Elem<DT>::kBytes, ok ? e : 0);
+    }
     if (bad) raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+#pragma unroll
+    for (int j = 0; j < VPL; j += 4) *reinterpret_cast<float4*>(slots + w.lane * VPL + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     __syncwarp();
     const uint32_t* ids = ids_all + w.grp * a.k;
     const float* gw = g_all + w.grp * a.k;
-    const float* xs = x_all + w.grp * a.k;
+    float* xs = x_all + w.grp * a.k;
+    float* mine = slots + w.grp * LPT * VPL;
     const int k = w.live ? a.k : 0;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) G[j] = 0.0f;
-    float total, dot = 0.0f;  // the weights' divisor, and sum_q g[q] * term[q]
+    float G[VPL];
     if (a.normalise) {
-        // only the picked scores matter: every lane of the group goes over all k of them
+        // only the picked scores matter: w[s] = term[s] / total, dx = sum of w (g - sum_q g w)
         float top = -INFINITY;
-        for (int s = 0; s < k; ++s) top = xs[s] > top || xs[s] != xs[s] ? xs[s] : top;
+        for (int s = w.sub; s < k; s += LPT) top = fmaxf(top, xs[s]);
+        top = group_max<LPT>(top);  // a NaN comes through by its own term
         const float base = top == -INFINITY ? 0.0f : top;
-        total = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) v[j] = 0.0f;
-        for (int s = 0; s < k; ++s) {
-            const int at = int(ids[s]) - e0;
-            const float term = exp2_fast((xs[s] - base) * kLog2e), g = gw[s];
+        float total = 0.0f, dot = 0.0f;
+        for (int s = w.sub; s < k; s += LPT) {
+            const float term = exp2_fast((xs[s] - base) * kLog2e);
+            xs[s] = term;
             total += term;
-            dot = __fmaf_rn(g, term, dot);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (at == j) {
-                    v[j] += term;
-                    G[j] = __fmaf_rn(g, term, G[j]);
-                }
+            dot = __fmaf_rn(gw[s], term, dot);
         }
-        // dx = sum of term/total (g - dot/total)
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        const float mean = dot * inv;
+        total = group_sum<LPT>(total);
+        dot = group_sum<LPT>(dot);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * inv;
+        __syncwarp();
+        if (w.sub == 0)  // one lane, in order: an id may occur more than once
+            for (int s = 0; s < k; ++s) mine[ids[s]] += xs[s] * inv * (gw[s] - mean);
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < VPL; ++j) G[j] = (G[j] - v[j] * mean) * inv;
+        for (int j = 0; j < VPL; ++j) G[j] = slots[w.lane * VPL + j];
     } else {
         float top;
-        total = softmax_terms<LPT, VPL>(v, &top);
+        const float total = softmax_terms<LPT, VPL>(v, &top);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        for (int s = 0; s < k; ++s) {
-            const int at = int(ids[s]) - e0;
-            if (at < 0 || at >= VPL) continue;
-            const float g = gw[s];
+        if (w.sub == 0)
+            for (int s = 0; s < k; ++s) mine[ids[s]] += gw[s];
+        __syncwarp();
+        float dot = 0.0f;
 #pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                if (at == j) {
-                    G[j] += g;
-                    dot = __fmaf_rn(g, v[j], dot);
-                }
+        for (int j = 0; j < VPL; ++j) {
+            G[j] = slots[w.lane * VPL + j];
+            dot = __fmaf_rn(G[j], v[j], dot);
         }
-        const float mean = group_sum<LPT>(dot) * inv;  // each lane summed the picks it holds
+        const float mean = group_sum<LPT>(dot) * inv;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) G[j] = v[j] * inv * (G[j] - mean);
     }
     if (!w.live) return;
-    char* out = static_cast<char*>(a.grad_logits[w.rank]) + w.t * a.E * Elem<DT>::kBytes;
+    char* out = static_cast<char*>(a.grad_logits[w.rank]) + size_t(w.t) * a.E * Elem<DT>::kBytes;
     if (a.vec) {
         using P = Pack16<DT>;
 #pragma unroll
@@ -291,10 +293,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
 template <int DT> __global__ void __launch_bounds__(kRouteThreads) k_route_wide(const __grid_constant__ RouteArgs a, int backward) {
     if (status_failed(a.ctl)) return;
     const int lane = threadIdx.x & 31;
-    const size_t token = (size_t(blockIdx.x) * kRouteThreads + threadIdx.x) >> 5;
-    if (token >= a.tokens) return;
-    const int rank = a.rank0 + int(token / a.T);
-    const size_t t = token % a.T;
+    const size_t t = (blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    const int rank = a.rank0 + int(blockIdx.y);
     const void* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;
     float m = -INFINITY;
     for (int e = lane; e < a.E; e += 32) m = fmaxf(m, ld_score<DT>(row, e));
@@ -381,14 +382,23 @@ template <int DT> __global__ void __launch_bounds__(kRouteThreads) k_route_wide(
 template <int DT> static cudaError_t launch_route_dt(const RouteArgs& a, bool backward, cudaStream_t s) {
     auto grid = [&](int lanes) {
         const size_t per_cta = size_t(kRouteThreads / lanes);
-        return unsigned((a.tokens + per_cta - 1) / per_cta);
+        return dim3(unsigned((a.T + per_cta - 1) / per_cta), unsigned(a.ranks));
     };
-#define SIMCOMM_ROUTE(LPT, VPL)                                                          \
-    do {                                                                                 \
-        const size_t smem = size_t(kRouteThreads / LPT) * a.k * 12;                         \
-        if (backward) k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a); \
-        else k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a);               \
-        return cudaGetLastError();                                                       \
+#define SIMCOMM_ROUTE(LPT, VPL)                                                                              \
+    do {                                                                                                     \
+        const size_t picks = size_t(kRouteThreads / LPT) * a.k * 4;                                          \
+        if (backward) {                                                                                      \
+            const size_t smem = size_t(kRouteThreads) * VPL * 4 + 3 * picks;                                 \
+            if (smem > 48 * 1024) {                                                                          \
+                cudaError_t e = cudaFuncSetAttribute(k_route_grad<DT, LPT, VPL>,                             \
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); \
+                if (e != cudaSuccess) return e;                                                              \
+            }                                                                                                \
+            k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a);                            \
+        } else {                                                                                             \
+            k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 2 * picks, s>>>(a);                            \
+        }                                                                                                    \
+        return cudaGetLastError();                                                                           \
     } while (0)
     if (a.E <= 8) SIMCOMM_ROUTE(1, 8);
     if (a.E <= 16) SIMCOMM_ROUTE(2, 8);
@@ -404,7 +414,6 @@ template <int DT> static cudaError_t launch_route_dt(const RouteArgs& a, bool ba
 }
 
 cudaError_t launch_route(const RouteArgs& a, int dtype, bool backward, cudaStream_t s) {
-    if ((a.tokens + 7) / 8 > size_t(INT32_MAX)) return cudaErrorInvalidValue;
     return dtype == COLL_BF16 ? launch_route_dt<COLL_BF16>(a, backward, s) : launch_route_dt<COLL_FP32>(a, backward, s);
 }
 
