@@ -8,10 +8,13 @@
 //     otherwise:  dx[e] = P[e] (G[e] - sum_q g[q] w[q]),  G[e] = the sum of g[s] over s with idx[s] = e
 //
 // One pass: a token's row is held in the registers of a group of lanes (8 scores per lane up to 256
-// experts, so that a warp takes 32 / lanes tokens and a lane's row piece is one or two 16-byte loads),
-// and the k rounds of "largest that is left" work on order-preserving integers: the group's maximum by
-// shuffles, then the first lane that holds it, then the first of its scores. Rows of more than 1024
-// experts are read again for every round, a warp per token (from cache; a row is at most 16 KiB).
+// experts, so that a warp takes 32 / lanes tokens and a lane's row piece is one or two 16-byte loads) as
+// order-preserving integers, which each lane sorts (a network: 19 exchanges of 8). A round of "largest that is
+// left" is then the group's maximum over the lanes' first ones, and one lane that moves up. bf16 scores leave
+// room for the id in the integer; for fp32 the ids of all picks are looked up at the end, side by side. The
+// sum over the whole row is formed only where the weights are shares of it. What bounds it is integer
+// instructions, then the launch. Rows of more than 1024 experts are read again for every round, a warp per token
+// (from cache; a row is at most 16 KiB).
 // Scores that are NaN are picked last and make the row's weights NaN; a row of nothing but -inf has
 // weight 0 for every pick.
 #include <algorithm>
@@ -81,6 +84,38 @@ template <int LPT> __device__ __forceinline__ uint32_t group_umax(uint32_t v) {
     }
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+// The row's maximum over the group, NaN if any score is.
+template <int LPT, int VPL> __device__ __forceinline__ float row_max(const float (&v)[VPL]) {
+    float m = v[0];
+#pragma unroll
+    for (int j = 1; j < VPL; ++j) m = max_nan(m, v[j]);
+#pragma unroll
+    for (int d = LPT / 2; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    return m;
+}
+
+// Sorts a lane's integers, largest first: Batcher's odd-even merge network.
+template <int N> __device__ __forceinline__ void sort_down(uint32_t (&x)[N]) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t a = x[i + j], b = x[i + j + k];
+                        x[i + j] = max(a, b);
+                        x[i + j + k] = min(a, b);
+                    }
+}
+
 // Softmax terms of the row in place: v[j] = e^(v[j] - max), the sum over the group returned. Missing
 // scores are -inf. A row of nothing but -inf has terms and sum 0; NaN or +inf makes the sum NaN.
 template <int LPT, int VPL> __device__ __forceinline__ float softmax_terms(float (&v)[VPL], float* top) {
@@ -129,70 +164,133 @@ __device__ __forceinline__ float key_score(uint32_t o) {
 
 template <int DT, int LPT, int VPL>
 __global__ void __launch_bounds__(kRouteThreads) k_route(const __grid_constant__ RouteArgs a) {
-    extern __shared__ uint32_t s_picks[];  // [warps][ids, terms][tokens of a warp][k]
+    // [warps][ids, terms][tokens of a warp][k], then for fp32 [warps][32 VPL] the keys as they came
+    extern __shared__ __align__(16) uint32_t s_picks[];
     if (status_failed(a.ctl)) return;
     const RouteWarp<LPT> w(a);
     const unsigned gmask = LPT == 32 ? 0xffffffffu : ((1u << (LPT & 31)) - 1u) << (w.grp * LPT);
     const char* row = static_cast<const char*>(a.logits[w.rank]) + size_t(w.live ? w.t : 0) * a.E * Elem<DT>::kBytes;
-    const int e0 = w.sub * VPL;
+    const int e0 = w.sub * VPL, warp = threadIdx.x >> 5;
+    constexpr bool kPacked = DT == COLL_BF16;
     float v[VPL];
     ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
-    // bf16 scores leave room for the id in the key: the upper half the score's order, the lower the id's complement
-    constexpr bool kPacked = DT == COLL_BF16;
+    const float top = row_max<LPT, VPL>(v);
+    const bool nan = top != top;
     uint32_t key[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
-        key[j] = e0 + j < a.E ? order_key(v[j]) : 0u;
-        if (kPacked && key[j]) key[j] = (max(key[j], 0x10000u) & 0xffff0000u) | uint32_t(0xffff - (e0 + j));
+        const uint32_t u = __float_as_uint(v[j] + 0.0f);  // -0 and +0 are equal scores
+        key[j] = u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
     }
-    float top;
-    const float sum = softmax_terms<LPT, VPL>(v, &top);
-    const float base = top == -INFINITY ? 0.0f : top;
+    if (__any_sync(0xffffffffu, nan)) {  // a NaN comes behind every number
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (v[j] != v[j]) key[j] = kPacked ? 0x10000u : 1u;
+    }
+    if constexpr (kPacked) {  // the upper half the score's order, the lower the id's complement
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) key[j] = (key[j] & 0xffff0000u) | uint32_t(0xffff - (e0 + j));
+    }
+    if (e0 + VPL > a.E) {  // missing scores: below everything
+#pragma unroll
+        for (int j = 0; j < VPL; ++j)
+            if (e0 + j >= a.E) key[j] = 0u;
+    }
     const int n = w.kTokens * a.k;
-    uint32_t* all_ids = s_picks + (threadIdx.x >> 5) * 2 * n;
+    uint32_t* all_ids = s_picks + warp * 2 * n;
     uint32_t* all_terms = all_ids + n;
     uint32_t* ids = all_ids + w.grp * a.k;
     uint32_t* terms = all_terms + w.grp * a.k;
-    uint32_t best = key[0];
+    uint32_t* kept = s_picks + (kRouteThreads / 32) * 2 * ((n + 1) / 2 * 2) + warp * 32 * VPL;
+    if constexpr (!kPacked) {
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) best = max(best, key[j]);
+        for (int j = 0; j < VPL; j += 2) *reinterpret_cast<uint2*>(kept + w.lane * VPL + j) = make_uint2(key[j], key[j + 1]);
+    }
+    sort_down<VPL>(key);
     for (int s = 0; s < a.k; ++s) {
-        const uint32_t all = group_umax<LPT>(best);
-        bool mine = best == all;
+        const uint32_t all = group_umax<LPT>(key[0]);
+        bool mine = key[0] == all;
         if constexpr (!kPacked) mine = w.lane == __ffs(__ballot_sync(0xffffffffu, mine) & gmask) - 1;
-        if (mine) {  // one lane of the group: takes the score out and looks for its next best
-            int at = 0;
+        if (mine) {  // one lane of the group moves up
 #pragma unroll
-            for (int j = VPL - 1; j >= 0; --j)
-                if (key[j] == all) at = j;
-            best = 0u;
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                if (j == at) key[j] = 0u;
-                best = max(best, key[j]);
-            }
-            ids[s] = uint32_t(e0 + at);
-            terms[s] = kPacked ? (all & 0xffff0000u) : all;
+            for (int j = 0; j + 1 < VPL; ++j) key[j] = key[j + 1];
+            key[VPL - 1] = 0u;
+            ids[s] = uint32_t(w.sub);
+            terms[s] = all;
         }
     }
     __syncwarp();
-    // the picks' terms: e^(score - max), from the keys
+    // side by side: the picks' ids and terms, e^(score - max)
+    const float base = top == -INFINITY ? 0.0f : top;
     float picked = 0.0f;
-    for (int s = w.sub; s < a.k; s += LPT) {
-        uint32_t o = terms[s];
-        if (kPacked) o = o == 0x10000u ? 1u : o & 0x80000000u ? o : o | 0xffffu;  // a negative one's complement has zeros below
-        const float term = exp2_fast((key_score(o) - base) * kLog2e);
-        terms[s] = __float_as_uint(term);
-        picked += term;
+    constexpr int kTurns = (32 + LPT - 1) / LPT;  // of a lane over its group's picks, k <= 32
+    uint32_t id[kTurns];
+    float term[kTurns];
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+        const int s = w.sub + q * LPT;
+        if (s >= a.k) break;
+        const uint32_t o = terms[s];
+        if constexpr (kPacked) {
+            id[q] = 0xffffu - (o & 0xffffu);
+            const uint32_t u = o & 0xffff0000u;  // a negative score's complement has zeros below
+            term[q] = exp2_fast((key_score(u == 0x10000u ? 1u : u & 0x80000000u ? u : u | 0xffffu) - base) * kLog2e);
+        } else {
+            const uint32_t sub = ids[s];
+            int before = 0;  // equal scores of the same lane that were picked earlier
+            for (int r = 0; r < s; ++r) before += terms[r] == o && ids[r] == sub;
+            const uint32_t* from = kept + (w.grp * LPT + sub) * VPL;
+            int at = 0;
+            int seen = 0;
+            for (int j = 0; j < VPL; ++j)
+                if (from[j] == o) {
+                    if (seen == before) at = j;
+                    ++seen;
+                }
+            id[q] = sub * VPL + at;
+            term[q] = exp2_fast((key_score(o) - base) * kLog2e);
+        }
+        picked += term[q];
     }
-    picked = group_sum<LPT>(picked);
-    const float total = a.normalise ? picked + 0.0f * sum : sum;  // NaN anywhere in the row reaches every weight
-    for (int s = w.sub; s < a.k; s += LPT)
-        terms[s] = __float_as_uint(total == 0.0f ? 0.0f : __uint_as_float(terms[s]) / total);
+    float total;
+    if (a.normalise) {
+        total = group_sum<LPT>(picked);
+        if (nan) total = top;  // NaN anywhere in the row reaches every weight; of +inf, inf - inf does
+    } else {
+        float unused;
+        total = softmax_terms<LPT, VPL>(v, &unused);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kTurns; ++q) {
+        const int s = w.sub + q * LPT;
+        if (s >= a.k) break;
+        ids[s] = id[q];
+        terms[s] = __float_as_uint(total == 0.0f ? 0.0f : term[q] / total);
+    }
     __syncwarp();
     for (int i = w.lane; i < w.count * a.k; i += 32) {
         a.idx_out[w.rank][w.pick0(a) + i] = int32_t(all_ids[i]);
         a.weight[w.rank][w.pick0(a) + i] = __uint_as_float(all_terms[i]);
+    }
+}
+
+// row[ids[s]] += value(s) for the group's k picks; a pick that shares its id with another of the same turn goes
+// after it, in order. Warp-collective (every group has the same `most`).
+template <int LPT, typename Value>
+__device__ __forceinline__ void add_picks(const RouteWarp<LPT>& w, float* row, const uint32_t* ids, int k, int most, Value value) {
+    for (int s0 = 0; s0 < most; s0 += LPT) {
+        const int s = s0 + w.sub;
+        const bool in = s < k;
+        const uint32_t id = in ? ids[s] : 0u;
+        const float x = in ? value(s) : 0.0f;
+        // lanes without a pick stand alone
+        const unsigned same = __match_any_sync(0xffffffffu, in ? id << 5 | uint32_t(w.grp) : 0x80000000u | uint32_t(w.lane));
+        const int turn = __popc(same & ((1u << w.lane) - 1u));
+        for (int t = 0; __any_sync(0xffffffffu, in && turn >= t); ++t) {
+            if (in && turn == t) row[id] += x;
+            __syncwarp();
+        }
     }
 }
 
@@ -248,18 +346,14 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
         dot = group_sum<LPT>(dot);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * inv;
         __syncwarp();
-        if (w.sub == 0)  // one lane, in order: an id may occur more than once
-            for (int s = 0; s < k; ++s) mine[ids[s]] += xs[s] * inv * (gw[s] - mean);
-        __syncwarp();
+        add_picks<LPT>(w, mine, ids, k, a.k, [&](int s) { return xs[s] * inv * (gw[s] - mean); });
 #pragma unroll
         for (int j = 0; j < VPL; ++j) G[j] = slots[w.lane * VPL + j];
     } else {
         float top;
         const float total = softmax_terms<LPT, VPL>(v, &top);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        if (w.sub == 0)
-            for (int s = 0; s < k; ++s) mine[ids[s]] += gw[s];
-        __syncwarp();
+        add_picks<LPT>(w, mine, ids, k, a.k, [&](int s) { return gw[s]; });
         float dot = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
@@ -396,7 +490,14 @@ template <int DT> static cudaError_t launch_route_dt(const RouteArgs& a, bool ba
             }                                                                                                \
             k_route_grad<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a);                            \
         } else {                                                                                             \
-            k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, 2 * picks, s>>>(a);                            \
+            const size_t kept = DT == COLL_FP32 ? size_t(kRouteThreads) * VPL * 4 : 0;                       \
+            const size_t smem = 2 * picks + 64 + kept;                                                       \
+            if (smem > 48 * 1024) {                                                                          \
+                cudaError_t e = cudaFuncSetAttribute(k_route<DT, LPT, VPL>,                                  \
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); \
+                if (e != cudaSuccess) return e;                                                              \
+            }                                                                                                \
+            k_route<DT, LPT, VPL><<<grid(LPT), kRouteThreads, smem, s>>>(a);                                 \
         }                                                                                                    \
         return cudaGetLastError();                                                                           \
     } while (0)
