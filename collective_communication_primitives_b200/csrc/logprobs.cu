@@ -14,9 +14,9 @@
 //
 // Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
 // column wins among equals. The scan itself keeps nothing for them but each thread's maximum, which it has
-// anyway: the n-th largest of the CTA's 256 maxima is a bound that n scores reach, so only threads whose maximum
-// reaches it can hold one of the n best. There are n of them, ties aside, and their n / 256 of the columns are
-// read again, the scores that reach the bound gathered in shared memory and sorted out. If more do than it
+// anyway: the n-th largest of the maxima of 32 groups of 8 threads is a bound that n scores reach, so only threads
+// whose maximum reaches it can hold one of the n best. There are little more than n of them, ties aside, and
+// their share of the columns is read again, the scores that reach the bound gathered in shared memory and sorted out. If more do than it
 // holds (many equal scores), all columns are gone through again with a sorted list of the n best per warp.
 //
 // The exponentials are powers of two, 2^(x log2e - B) with B = M log2e rounded to fp32, so that a score
@@ -128,7 +128,7 @@ __device__ __forceinline__ bool top_insert(TopList& l, unsigned long long key, i
 struct TopShared {
     uint32_t bound;   // order of a score that n of the CTA reach
     uint32_t count;   // keys gathered (more than kLpGather: some were dropped)
-    uint32_t max[kLpThreads];       // order of each thread's maximum, 0: none, all ones: it met a NaN
+    uint32_t group[32];             // order of the largest number that 8 threads met, 0: none
     uint32_t threads;               // threads that reach the bound
     uint8_t thread[kLpThreads];
     unsigned long long key[kLpGather];
@@ -139,28 +139,6 @@ __device__ __forceinline__ void top_gather(TopShared& top, float x, uint32_t col
         const uint32_t at = atomicAdd(&top.count, 1u);
         if (at < uint32_t(kLpGather)) top.key[at] = top_key(x, col);
     }
-}
-
-// The n-th largest of the keys that the warp's lanes hold (0: none), by n rounds of "largest that is left".
-template <int N> __device__ __forceinline__ uint32_t warp_nth(uint32_t (&key)[N], int n) {
-    uint32_t m = 0u;
-    for (int i = 0; i < n; ++i) {
-        uint32_t best = key[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) best = max(best, key[j]);
-        m = __reduce_max_sync(0xffffffffu, best);
-        const unsigned who = __ballot_sync(0xffffffffu, best == m);
-        if ((threadIdx.x & 31) == __ffs(who) - 1) {
-            bool gone = false;
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (!gone && key[j] == m) {
-                    key[j] = 0u;
-                    gone = true;
-                }
-        }
-    }
-    return m;
 }
 
 // Two fp32 values in a 64-bit register, for the two-at-a-time arithmetic of sm_100.
@@ -304,47 +282,72 @@ __device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, u
     }
 }
 
-// Gathers the scores that may be among the n best, given every thread's maximum in top.max. CTA-collective.
+// Gathers the scores that may be among the n best, given the thread's maximum (NaN: it met one). CTA-collective.
 template <int DT>
-__device__ __forceinline__ void gather_best(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, TopShared& top) {
+__device__ __forceinline__ void gather_best(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, float raw, TopShared& top) {
     using P = Pack16<DT>;
     constexpr int L = P::L;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 0) {
-        uint32_t key[kLpWarps];
+    const int lane = threadIdx.x & 31;
+    // behind a NaN a thread's maximum is not known: it counts for nothing and is looked at in any case
+    const uint32_t mine = raw > -INFINITY ? score_order(raw) : 0u;
+    uint32_t most = mine;
 #pragma unroll
-        for (int j = 0; j < kLpWarps; ++j) {
-            const uint32_t k = top.max[j * 32 + lane];
-            key[j] = k == 0xffffffffu ? 0u : k;  // behind a NaN a thread's maximum is not known
-        }
-        const uint32_t nth = warp_nth<kLpWarps>(key, a.n_top);  // 0: fewer than n threads have one
-        if (lane == 0) {
-            top.bound = nth;
-            top.count = top.threads = 0u;
-        }
-    }
+    for (int d = 4; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+    if (threadIdx.x % 8 == 0) top.group[threadIdx.x / 8] = most;
+    if (threadIdx.x == 0) top.count = top.threads = 0u;
     __syncthreads();
-    if (top.max[threadIdx.x] >= top.bound) top.thread[atomicAdd(&top.threads, 1u)] = uint8_t(threadIdx.x);
+    // every warp finds the bound for itself: the group whose maximum has n - 1 others before it (the lower group
+    // among equals); 0 where fewer than n groups have a number
+    const uint32_t own = top.group[lane];
+    int before = 0;
+#pragma unroll
+    for (int g = 0; g < 32; ++g) {
+        const uint32_t other = __shfl_sync(0xffffffffu, own, g);
+        before += other > own || (other == own && g < lane);
+    }
+    const uint32_t bound = __shfl_sync(0xffffffffu, own, __ffs(__ballot_sync(0xffffffffu, before == a.n_top - 1)) - 1);
+    if (threadIdx.x == 0) top.bound = bound;
+    if (raw != raw || mine >= bound) top.thread[atomicAdd(&top.threads, 1u)] = uint8_t(threadIdx.x);
     __syncthreads();
     const uint32_t nt = top.threads;
-    for (uint32_t v = v0; v < v1;) {
-        const Piece<DT> pc(a, row, v, v1);
-        if (threadIdx.x < pc.head + pc.tail) {
-            const uint32_t at = pc.end_at(threadIdx.x);
-            top_gather(top, load_elem<DT>(pc.base, at), v + at);
-        }
-        const uint32_t turns = (pc.vecs + kLpThreads - 1) / kLpThreads;
-        const int shift = turns > 1 ? 32 - __clz(turns - 1) : 0;  // turns as a power of two: no division by item
-        for (uint32_t w = threadIdx.x; w < nt << shift; w += kLpThreads) {
-            const uint32_t i = (w & ((1u << shift) - 1u)) * kLpThreads + top.thread[w >> shift];
-            if (i >= pc.vecs) continue;
-            float x[L];
-            P::unpack(ld_stream_v4(pc.vector(i)), x);
-            const uint32_t col = v + pc.head + i * L;
+    auto offer = [&](const uint4& raw_scores, uint32_t col) {
+        float x[L];
+        P::unpack(raw_scores, x);
 #pragma unroll
-            for (int j = 0; j < L; ++j) top_gather(top, x[j], col + j);
+        for (int j = 0; j < L; ++j) top_gather(top, x[j], col + j);
+    };
+    // pieces four at a time, so that their loads are in flight together
+    for (uint32_t v = v0; v < v1;) {
+        uint4 got[4];
+        uint32_t col[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            col[q] = 0xffffffffu;
+            if (v >= v1) continue;
+            const Piece<DT> pc(a, row, v, v1);
+            const uint32_t turns = (pc.vecs + kLpThreads - 1) / kLpThreads;
+            const int shift = turns > 1 ? 32 - __clz(turns - 1) : 0;  // turns as a power of two: no division by item
+            for (uint32_t w = threadIdx.x; w < nt << shift; w += kLpThreads) {
+                const uint32_t i = (w & ((1u << shift) - 1u)) * kLpThreads + top.thread[w >> shift];
+                if (i >= pc.vecs) continue;
+                const uint4 scores = ld_stream_v4(pc.vector(i));
+                const uint32_t c = v + pc.head + i * L;
+                if (w == threadIdx.x) {
+                    got[q] = scores;
+                    col[q] = c;
+                } else {
+                    offer(scores, c);
+                }
+            }
+            if (threadIdx.x < pc.head + pc.tail) {
+                const uint32_t at = pc.end_at(threadIdx.x);
+                top_gather(top, load_elem<DT>(pc.base, at), v + at);
+            }
+            v = pc.end;
         }
-        v = pc.end;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (col[q] != 0xffffffffu) offer(got[q], col[q]);
     }
     __syncthreads();
 }
@@ -426,13 +429,12 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
     Feed f = feed_none();
     scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); });
-    if constexpr (TOP) s_top.max[threadIdx.x] = f.raw != f.raw ? 0xffffffffu : f.raw == -INFINITY ? 0u : score_order(f.raw);
     Stat st = stat_warp(feed_stat(f));
     if (lane == 0) s_stat[warp] = st;
     __syncthreads();
     int nkeys = 0;
     if constexpr (TOP) {
-        gather_best<DT>(a, row, v0, v1, s_top);
+        gather_best<DT>(a, row, v0, v1, f.raw, s_top);
         nkeys = int(s_top.count);
         if (nkeys > kLpGather) {
             top_by_lists<DT>(a, row, v0, v1, s_top.key);
@@ -445,8 +447,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
         for (int q = 0; q < nkeys; ++q) above += s_top.key[q] > k;
         return above;
     };
-    // numbers among the keys; n at most counts
+    // numbers among the keys; n at most counts. Where the bound came from n scores there are as many.
+    bool full = TOP && s_top.bound != 0u && nkeys <= kLpGather;
     auto held = [&]() {
+        if (full) return a.n_top;
         int n = 0;
         for (int i = threadIdx.x; i < nkeys; i += kLpThreads) n += s_top.key[i] != 0ull;
         return __syncthreads_count(n > 0) >= a.n_top ? a.n_top : min(a.n_top, int(cta_sum(float(n), s_w)));
@@ -490,6 +494,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
                 top_insert(l, lane < a.n_top ? __ldcg(a.part_keys + (row * a.parts + q) * a.n_top + lane) : 0ull, a.n_top);
             if (lane < a.n_top) s_top.key[warp * a.n_top + lane] = l.mine;
             nkeys = kLpWarps * a.n_top;
+            full = false;  // of this part only
         }
         __syncthreads();
         st = s_stat[0];
@@ -592,7 +597,7 @@ template <int DT> __device__ __forceinline__ uint4 grad_vector(const RowGrad& g,
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs_grad(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs_grad(const __grid_constant__ LogprobArgs a) {
     using P = Pack16<DT>;
     constexpr int L = P::L, D = Elem<DT>::kBytes;
     __shared__ int s_flag;
