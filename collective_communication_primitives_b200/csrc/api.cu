@@ -1894,6 +1894,7 @@ static coll_status_t coll_linear_w4_impl(sim_comm_t c, const void* const* x, con
     int shift = 0;
     if ((st = check_group(group, K, row ? "k / p" : "k", &shift)) != COLL_OK) return st;
     if ((st = check_rows(N, K, "n")) != COLL_OK) return st;
+    if (tokens > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "tokens must fit in int32");
     if ((st = check_rows(tokens, std::max(N, K), "tokens")) != COLL_OK) return st;
     if (!x || !w || !scale || !out) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
     if (tokens == 0 || N == 0) return COLL_OK;

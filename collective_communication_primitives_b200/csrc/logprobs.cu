@@ -22,7 +22,7 @@
 // The exponentials are powers of two, 2^(x log2e - B) with B = M log2e rounded to fp32, so that a score
 // costs one fused multiply-add and one ex2: S and U refer to B, and the rounding of B is put back at the
 // end (resid below). That holds while |M| is moderate. Masked scores: -inf has probability 0; for the
-// arithmetic a score below -2^100 counts as -2^100, which gives it probability 0 next to any score that is
+// arithmetic a score below -2^40 counts as -2^40, which gives it probability 0 next to any score that is
 // not masked and keeps 0 * inf out of the sums. A row whose maximum is beyond +-1e5, such as one masked
 // throughout by the type's lowest value, is summed again relative to its maximum. A row of nothing but
 // -inf has no distribution: lse and logprob -inf, entropy 0, gradient 0. NaN or +inf in a row makes its
@@ -39,7 +39,7 @@ constexpr int kLpUnroll = 4;            // 16-byte loads in flight per thread
 constexpr int kLpGather = 768;          // keys of scores that passed the bound
 constexpr float kLpLog2e = 1.4426950408889634f;
 constexpr float kLpLn2 = 0.6931471805599453f;
-constexpr float kLpFloor = -0x1p100f;   // scores below count as this in the sums (x log2e is exact at a power of two)
+constexpr float kLpFloor = -0x1p40f;    // scores below count as this in the sums (x log2e rounds alike at a power of two)
 constexpr float kLpFar = 1e5f;          // rows whose maximum is further from 0 are summed again
 
 __device__ __forceinline__ float ex2(float x) {
@@ -188,7 +188,7 @@ template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uin
     if constexpr (DT == COLL_BF16) {  // maximum and clamp on pairs
         const uint32_t p = max_nan_bf16x2(max_nan_bf16x2(w[0], w[1]), max_nan_bf16x2(w[2], w[3]));
         top = max_nan(bf16_bits_to_float(p), __uint_as_float(p & 0xffff0000u));
-        constexpr uint32_t kFloor2 = 0xF180F180u;  // kLpFloor twice
+        constexpr uint32_t kFloor2 = 0xD380D380u;  // kLpFloor twice
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const uint32_t c = max_nan_bf16x2(w[q], kFloor2);
@@ -576,7 +576,7 @@ template <int DT> __device__ __forceinline__ uint4 grad_vector(const RowGrad& g,
     if constexpr (DT == COLL_BF16) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint32_t c = max_nan_bf16x2(w[q], 0xF180F180u);  // kLpFloor: a masked score's 2^d is 0 and d finite
+            const uint32_t c = max_nan_bf16x2(w[q], 0xD380D380u);  // kLpFloor: a masked score's 2^d is 0 and d finite
             x[2 * q] = bf16_bits_to_float(c);
             x[2 * q + 1] = __uint_as_float(c & 0xffff0000u);
         }
@@ -682,7 +682,9 @@ cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s) {
 
 cudaError_t launch_logprobs_grad(const LogprobArgs& args, int dtype, cudaStream_t s) {
     LogprobArgs a = args;
-    constexpr size_t kPiece = 16384;  // columns of one CTA
+    // Columns of one CTA. Measured on B200 with 4096, 16384 and 65536: 109, 79, 79 us for 1023 x 50257 fp32 on 4 ranks,
+    // 371, 202, 202 for 2048 x 131072 bf16 on 8, 6.2, 6.2, 10.4 for 8 x 50257 bf16 on one.
+    constexpr size_t kPiece = 16384;
     a.parts = int(std::max<size_t>(1, (a.m + kPiece - 1) / kPiece));
     const size_t ctas = a.rows * size_t(a.parts) * (a.view_rank >= 0 ? 1 : size_t(a.p));
     if (ctas > size_t(INT32_MAX)) return cudaErrorInvalidValue;

@@ -149,7 +149,7 @@ template <int LPT> struct RouteWarp {
         grp = lane / LPT;
         rank = a.rank0 + int(blockIdx.y);
         const uint32_t T = uint32_t(a.T);  // tokens * k fits 31 bits
-        first = ((blockIdx.x * kRouteThreads + threadIdx.x) >> 5) * kTokens;
+        first = (blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5)) * kTokens;  // below T + a CTA: 32 bits hold it
         t = first + grp;
         count = first < T ? int(min(uint32_t(kTokens), T - first)) : 0;
         live = t < T;
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
 template <int DT> __global__ void __launch_bounds__(kRouteThreads) k_route_wide(const __grid_constant__ RouteArgs a, int backward) {
     if (status_failed(a.ctl)) return;
     const int lane = threadIdx.x & 31;
-    const size_t t = (blockIdx.x * kRouteThreads + threadIdx.x) >> 5;
+    const size_t t = size_t(blockIdx.x) * (kRouteThreads / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const int rank = a.rank0 + int(blockIdx.y);
     const void* row = static_cast<const char*>(a.logits[rank]) + t * a.E * Elem<DT>::kBytes;

@@ -172,6 +172,8 @@ def test_refusals():
         assert args(31, 64, 32, 0) == SC.INVALID_ARG and args(32, 96, 32) == SC.INVALID_ARG
         assert args(1 << 60, 64, 32) == SC.INVALID_ARG and args(32, 64, 32, 2) == SC.INVALID_ARG
         assert args(32, 64, 32) == SC.INVALID_ARG and b"null" in L.sim_comm_last_error()
+        assert L.coll_linear_w4(c._h, None, None, None, 1 << 31, 32, 64, 32, 1, 2, None, None) == SC.INVALID_ARG
+        assert b"int32" in L.sim_comm_last_error()
         n = c.launch_count()
         c.linear_w4([x[:0] for x in xs], w, s, [v[:0] for v in o])
         assert c.launch_count() == n

@@ -181,6 +181,25 @@ def test_masked_and_special_rows(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_masked_columns_get_zero_whatever_comes_in(dtype):
+    """Gradients scaled by a power of two come out scaled by it, bit for bit, and masked columns stay at zero."""
+    x, ids = scores(6, 5000, dtype, 8), tokens(6, 5000, 2)
+    masked = torch.arange(5000, device="cuda") % 3 == 0
+    x[::2, masked] = -inf
+    x[1::2, masked] = torch.finfo(DT[dtype]).min
+    ids = torch.where(ids % 3 == 0, ids - 2, ids).clamp(min=1)
+    a = Call(x, ids, 2)
+    one = torch.ones(6, device="cuda")
+    with SC.SimComm(2) as c:
+        a.run(c)
+        plain, scaled = a.grad(c, one, one), a.grad(c, one * 2.0 ** 70, one * 2.0 ** 70)
+        torch.cuda.synchronize()
+    for u, v in zip(plain, scaled):
+        assert torch.equal(u.double() * 2.0 ** 70, v.double())
+    assert bool((torch.cat(scaled, 1)[:, masked] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_far_scores_keep_their_differences(dtype):
     """Rows whose maximum is far from 0, in either direction, with neighbours one representable step below."""
     V = 3000
