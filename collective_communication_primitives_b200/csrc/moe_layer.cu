@@ -174,11 +174,12 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
     if (per_sm < 1) return cudaErrorNotSupported;
     const size_t resident = size_t(num_sms) * per_sm;
     const size_t picked = size_t(std::min(a.E, a.A)) + size_t(a.A) / kLayTokens;  // at most this many token tiles
-    // warps of a CTA on one row tile: more, the fewer tiles there are to fill the GPU with
+    // Warps of a CTA on one row tile: more, while the tiles do not fill the GPU's warps. Measured on B200 for 16 picked
+    // experts of 4096 x 2048 in 4 bits: 79 us so, 92 with twice as many warps to a tile.
     auto plan = [&](size_t tiles, int K, int* splits, int* blocks) {
         const int stages = K / WTraits<WK>::kStageK;
         int sp = 1;
-        while (sp < max_splits<WK, kLayTokens / 8>() && sp * 2 <= stages && picked * tiles * sp < resident * 4 * kProdWarps)
+        while (sp < max_splits<WK, kLayTokens / 8>() && sp * 2 <= stages && picked * tiles * sp < resident * kProdWarps)
             sp *= 2;
         *splits = sp;
         const size_t per = kProdWarps / sp;

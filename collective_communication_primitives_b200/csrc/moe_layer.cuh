@@ -5,8 +5,6 @@
 
 namespace simcomm {
 
-constexpr int kMaxLayerWarps = 17;
-
 __device__ __forceinline__ bool layer_barrier(const MoeLayerArgs& a, uint32_t k, bool ok) {
     __shared__ int s_ok;
     if (!__syncthreads_and(ok)) return false;  // a wait ran out: the status is set
