@@ -265,9 +265,9 @@ struct LinearArgs {
     int group_shift;                     // log2 of the weights per scale
     int out_bf16;
     int x_vec;                           // x rows are 16-byte aligned
-    int splits, chunk_shift;             // set by the launcher: warps per row tile; log2 of chunks per group
+    int shift, chunk_shift;              // set by the launcher: log2 of the warps per row tile, of the chunks per group
     uint32_t tile_blocks, token_tiles;   // set by the launcher
-    int units;                           // set by the launcher
+    int units, tail_first, tail_shift;   // set by the launcher: units from tail_first on are 2^-tail_shift of one
     uint64_t timeout_ns;
     Ctl ctl;
 };
@@ -294,7 +294,7 @@ struct MoeLayerArgs {
     int vec;                             // every row is whole 16-byte units at an aligned address
     int tensor;                          // option moe_layer_tensor
     int tensor_ring;                     // set by the launcher: bytes of the tensor kernel's ring of stages
-    int splits_up, splits_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
+    int shift_up, shift_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
     size_t T;
     uint16_t* h;                         // scratch: bf16 [A][h_stride]
     size_t h_stride;

@@ -37,12 +37,13 @@ template <int WK, bool VEC, bool UP> struct LayerJob {
     const MoeLayerArgs& a;
     const LayerLists& l;
     int nact;
-    int K, segments, splits, chunk_shift, rows_all, blocks;
+    int K, segments, shift, chunk_shift, rows_all, blocks;
 
     __device__ __forceinline__ LayerJob(const MoeLayerArgs& a_, const LayerLists& l_, int nact_)
-        : a(a_), l(l_), nact(nact_), K(UP ? a_.H : a_.F), segments(1), splits(UP ? a_.splits_up : a_.splits_down),
+        : a(a_), l(l_), nact(nact_), K(UP ? a_.H : a_.F), segments(1), shift(UP ? a_.shift_up : a_.shift_down),
           chunk_shift(a_.chunk_shift), rows_all(UP ? a_.F : a_.H), blocks(UP ? a_.blocks_up : a_.blocks_down) {}
 
+    __device__ __forceinline__ int split_shift(int) const { return shift; }
     __device__ __forceinline__ int units() const { return l.act_tile[nact] * blocks; }
     struct At { int e, row0, first, count; };
     __device__ __forceinline__ At at(int u) const {
@@ -55,7 +56,7 @@ template <int WK, bool VEC, bool UP> struct LayerJob {
         const int tiles = l.act_tile[lo + 1] - l.act_tile[lo], rel = u - l.act_tile[lo] * blocks;
         At x;
         x.e = l.act[lo];
-        x.row0 = rel / tiles * (kProdWarps / splits) * kTile;
+        x.row0 = rel / tiles * (kProdWarps >> shift) * kTile;
         x.first = l.act_start[lo] + rel % tiles * kLayTokens;
         x.count = min(kLayTokens, l.act_start[lo + 1] - x.first);
         return x;
@@ -120,7 +121,7 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
             constexpr int NT = decltype(nt)::value;
             float acc[kLayTiles][NT][4];
             if (!mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc)) return false;
-            finish_unit<UP, kLayTiles, NT>(s, job.splits, acc, [&](int tile, int r, int c, float v, float v2) {
+            finish_unit<UP, kLayTiles, NT>(s, 1 << job.shift, acc, [&](int tile, int r, int c, float v, float v2) {
                 const int row = x.row0 + tile * Job::kTile + (UP ? r / 16 * 8 + r % 8 : r);
                 if (row >= job.rows_all || c >= x.count) return;
                 const int asg = l.list[x.first + c];
@@ -176,17 +177,17 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
     const size_t picked = size_t(std::min(a.E, a.A)) + size_t(a.A) / kLayTokens;  // at most this many token tiles
     // Warps of a CTA on one row tile: more, while the tiles do not fill the GPU's warps. Measured on B200 for 16 picked
     // experts of 4096 x 2048 in 4 bits: 79 us so, 92 with twice as many warps to a tile.
-    auto plan = [&](size_t tiles, int K, int* splits, int* blocks) {
+    auto plan = [&](size_t tiles, int K, int* shift, int* blocks) {
         const int stages = K / WTraits<WK>::kStageK;
-        int sp = 1;
-        while (sp < max_splits<WK, kLayTokens / 8>() && sp * 2 <= stages && picked * tiles * sp < resident * kProdWarps)
-            sp *= 2;
-        *splits = sp;
-        const size_t per = kProdWarps / sp;
+        int sh = 0;
+        while ((1 << sh) < max_splits<WK, kLayTokens / 8>() && (2 << sh) <= stages && (picked * tiles << sh) < resident * kProdWarps)
+            ++sh;
+        *shift = sh;
+        const size_t per = kProdWarps >> sh;
         *blocks = int((tiles + per - 1) / per);
     };
-    plan((size_t(a.F) + 8 * kLayTiles - 1) / (8 * kLayTiles), a.H, &a.splits_up, &a.blocks_up);
-    plan((size_t(a.H) + 16 * kLayTiles - 1) / (16 * kLayTiles), a.F, &a.splits_down, &a.blocks_down);
+    plan((size_t(a.F) + 8 * kLayTiles - 1) / (8 * kLayTiles), a.H, &a.shift_up, &a.blocks_up);
+    plan((size_t(a.H) + 16 * kLayTiles - 1) / (16 * kLayTiles), a.F, &a.shift_down, &a.blocks_down);
     const size_t units = picked * size_t(std::max(a.blocks_up, a.blocks_down));
     dim3 grid(unsigned(std::max<size_t>(1, std::min(resident, units)))), block(kProdThreads);
     void* args[] = {&a};

@@ -257,8 +257,9 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
 //
 // A Job describes a sequence of units; the CTA takes units first, first + step, ... A unit is a block of row
 // tiles against up to 8 NT tokens, summed over `segments` rows of K each (the ranks of a sum over ranks).
-// `splits` warps share each row tile, the stages of a segment dealt to them in turn. A Job has
-//   static kWK, kVecW, kVecX, kMT;   int K, segments, splits, chunk_shift
+// Some warps (1, 2, 4 or 8) share each row tile, the stages of a segment dealt to them in turn. A Job has
+//   static kWK, kVecW, kVecX, kMT;   int K, segments, chunk_shift
+//   int split_shift(unit)                log2 of the warps that share a row tile
 //   void rows(unit, seg, tile, g, w)     the lane's weight rows of the CTA's tile-th row tile group
 //   void scales(unit, seg, tile, g, t, s)
 //   const uint16_t* token(unit, seg, n)  row of the n-th token, null for none
@@ -345,7 +346,7 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
 // Where a multiplying warp's copies have got to: a stage of a segment of a unit.
 template <int MT> struct Ahead {
     const char* w[MT][2];
-    int unit, seg, next, slot;
+    int unit, seg, next, slot, splits;
 };
 
 template <typename Job> struct Multiplier {
@@ -354,7 +355,7 @@ template <typename Job> struct Multiplier {
     const Job& job;
     const ProductSmem& s;
     int units, step;           // of the CTA's sequence: units below `units`, every `step`-th
-    int warp, lane, g, t, tile, split, stages;
+    int warp, lane, g, t, stages;
     uint32_t ring;
     int slot = 0;
     Ahead<MT> ahead;
@@ -366,34 +367,39 @@ template <typename Job> struct Multiplier {
         lane = threadIdx.x & 31;
         g = lane >> 2;
         t = lane & 3;
-        tile = warp / job.splits;
-        split = warp % job.splits;
         stages = (job.K + W::kStageK - 1) / W::kStageK;
         ring = smem_u32(s.base) + s.rings + warp * (kRing * MT * 1024);
         qc = q4_consts();
         ahead.unit = first;
         ahead.seg = 0;
-        ahead.next = split;
         ahead.slot = 0;
-        if (first < units) job.rows(first, 0, tile, g, ahead.w);
+        ahead.next = ahead.splits = 1;
+        if (first < units) start_rows();
         __syncwarp();  // an earlier use of the ring by this warp is over
 #pragma unroll
         for (int i = 0; i < kRing - 1; ++i) fetch();
     }
 
+    // Turns the copies to their segment's rows.
+    __device__ __forceinline__ void start_rows() {
+        const int shift = job.split_shift(ahead.unit);
+        ahead.splits = 1 << shift;
+        ahead.next = warp & (ahead.splits - 1);
+        job.rows(ahead.unit, ahead.seg, warp >> shift, g, ahead.w);
+    }
+
     // Starts the next copy of the sequence; past its end an empty group keeps the count of groups in step.
     __device__ __forceinline__ void fetch() {
         while (ahead.next >= stages && ahead.unit < units) {
-            ahead.next = split;
             if (++ahead.seg == job.segments) {
                 ahead.seg = 0;
                 ahead.unit += step;
             }
-            if (ahead.unit < units) job.rows(ahead.unit, ahead.seg, tile, g, ahead.w);
+            if (ahead.unit < units) start_rows();
         }
         if (ahead.unit < units) {
             fetch_stage<Job::kWK, Job::kVecW, MT>(ring + ahead.slot * (MT * 1024), ahead.w, ahead.next, job.K, g, t);
-            ahead.next += job.splits;
+            ahead.next += ahead.splits;
             ahead.slot = ahead.slot + 1 == kRing ? 0 : ahead.slot + 1;
         }
         cp_async_commit();
@@ -409,6 +415,7 @@ template <typename Job> struct Multiplier {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        const int shift = job.split_shift(u), splits = 1 << shift, tile = warp >> shift, split = warp & (splits - 1);
         const int groups = (((job.K + W::kChunk - 1) / W::kChunk - 1) >> job.chunk_shift) + 1;
         for (int seg = 0; seg < job.segments; ++seg) {
             const uint16_t* sp[(MT + 1) / 2];
@@ -422,9 +429,9 @@ template <typename Job> struct Multiplier {
                 const int buf = pc.buf(), end = min(p0 + kPanelStages, stages);
                 if (!mbar_wait_bounded(ctl, &s.full[buf], pc.parity(), timeout_ns)) return false;
                 const unsigned char* tok = s.base + buf * kPanelBytes + g * kPitch + t * W::kLaneK * 2;
-                for (; st < end; st += job.splits) {
+                for (; st < end; st += splits) {
                     const StageScales<Job::kWK, MT> sc = next;
-                    if constexpr (W::kQ4) load_scales<Job::kWK, MT>(next, sp, st + job.splits, groups, job.chunk_shift);
+                    if constexpr (W::kQ4) load_scales<Job::kWK, MT>(next, sp, st + splits, groups, job.chunk_shift);
                     cp_async_wait<kRing - 2>();
                     __syncwarp();  // the stage is in for every lane, and the slot refilled next has been read
                     fetch();

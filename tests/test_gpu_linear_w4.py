@@ -50,6 +50,8 @@ CASES = [
     (8, 5, 8, 256, 32), (2, 9, 50, 384, 64), (1, 16, 33, 640, 128), (4, 17, 20, 1024, 256), (2, 33, 18, 128, 32),
     (1, 70, 15, 224, 32), (64, 2, 64, 4096, 64), (3, 1, 3, 96, 32), (1, 4, 5000, 128, 128), (2, 2, 40, 1024, 512),
     (1, 1, 24000, 96, 32), (1, 3, 7, 8192, 128),
+    # more blocks than SMs: the last ones in pieces
+    (2, 9, 40100, 1024, 64), (1, 20, 38000, 640, 32), (4, 1, 39000, 2048, 128), (1, 40, 20000, 512, 64),
 ]
 
 
