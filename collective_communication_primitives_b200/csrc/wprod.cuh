@@ -21,7 +21,7 @@
 //
 // 4-bit weights: word bits 4i..4i+3 hold weight i of eight, value q - 8. (w & 0x000F000F) | 0x43004300
 // is the pair (128 + q_0, 128 + q_4) of bf16 values, and subtracting 136 is exact; shifts by 4 give
-// the pairs (1,5), (2,6), (3,7); the tokens' words are paired the same way as they are read. A chunk's sum is taken
+// the pairs (1,5), (2,6), (3,7); the tokens' words are paired the same way. A chunk's sum is taken
 // over the whole numbers q - 8 (bf16 holds them, the products are exact in fp32) and scaled once per
 // chunk in fp32, so the weights are never rounded.
 //
@@ -59,7 +59,7 @@ constexpr int kSumTokens = 16;  // tokens whose sums are exchanged at a time whe
 template <int MT> constexpr int sums_bytes() { return kProdWarps * MT * 16 * kSumTokens * 4; }
 // Shared memory: panels, rings, exchanged sums, mbarriers.
 template <int MT> constexpr int product_smem() {
-    return kPanels * kPanelBytes + kProdWarps * kRing * MT * 1024 + sums_bytes<MT>() + 2 * kPanels * 8;
+    return kPanels * kPanelBytes + kProdWarps * kRing * MT * 1024 + sums_bytes<MT>() + 3 * kPanels * 8;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -102,6 +102,18 @@ template <bool VEC> __device__ __forceinline__ uint4 ld_row8(const uint16_t* row
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
+
+// Eight tokens' values (0..7) as the pairs (0,4) (1,5) (2,6) (3,7), which is how a word's 4-bit weights come apart.
+__device__ __forceinline__ uint4 paired(uint4 v) {
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+// Whether a panel holds its tokens in pairs: the copying warp then makes them once for all, else every warp as it
+// reads. With up to 8 tokens a panel is long and the copying warp has the time: 48 and 45 us at 65536 x 4096 with one
+// token on B200, every warp and once. With more it has not: 117 and 124 at 131072 x 4096 with 16, 49 and 60 at 16384 x
+// 4096 with 64.
+template <int WK, int NT> constexpr bool panel_pairs() { return WTraits<WK>::kQ4 && NT == 1; }
 
 // The constants of the 4-bit form, held in registers: a logic instruction takes one immediate, and the
 // mask and the bias go into one.
@@ -181,11 +193,8 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
     using W = WTraits<WK>;
     constexpr int kPitch = panel_pitch<WK, NT>();
     auto token8 = [&](int n, int u, int j) {  // run j of 8 k's of chunk u
-        return *reinterpret_cast<const uint4*>(tok + n * 8 * kPitch + u * W::kChunk * 2 + j * 16);
-    };
-    auto paired = [](uint4 v) {  // (0,4) (1,5) (2,6) (3,7)
-        return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                          __byte_perm(v.y, v.w, 0x7632));
+        const uint4 v = *reinterpret_cast<const uint4*>(tok + n * 8 * kPitch + u * W::kChunk * 2 + j * 16);
+        return W::kQ4 && !panel_pairs<WK, NT>() ? paired(v) : v;
     };
     if constexpr (!W::kQ4) {
         uint4 x[NT];
@@ -212,7 +221,7 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
 #pragma unroll
                 for (int j = 0; j < W::kWords; ++j)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) x[j][n] = paired(token8(n, u, j));
+                    for (int n = 0; n < NT; ++n) x[j][n] = token8(n, u, j);
             }
             const int byte = (4 * u + t) * W::kLaneBytes;  // of the row's 64
 #pragma unroll
@@ -225,7 +234,7 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
                 for (int j = 0; j < W::kWords; ++j) {
                     if constexpr (!kHold) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) x[0][n] = paired(token8(n, u, j));
+                        for (int n = 0; n < NT; ++n) x[0][n] = token8(n, u, j);
                     }
                     const uint32_t wa = w[0][j], wb = w[1][j];
                     const uint32_t a0 = q4_pair(wa, qc), a1 = q4_pair(wa >> 4, qc), a2 = q4_pair(wa >> 8, qc), a3 = q4_pair(wa >> 12, qc);
@@ -273,6 +282,7 @@ struct ProductSmem {
     unsigned char* base;
     int rings, sums;  // bytes from base
     uint64_t* full;   // [kPanels]: the panel's tokens are in
+    uint64_t* landed; // [kPanels]: they are in, but not yet in pairs (panel_pairs)
     uint64_t* empty;  // [kPanels]: every multiplying warp has used it
 };
 template <int MT> __device__ __forceinline__ ProductSmem product_layout(unsigned char* smem) {
@@ -282,12 +292,14 @@ template <int MT> __device__ __forceinline__ ProductSmem product_layout(unsigned
     s.sums = s.rings + kProdWarps * kRing * MT * 1024;
     s.full = reinterpret_cast<uint64_t*>(smem + s.sums + sums_bytes<MT>());
     s.empty = s.full + kPanels;
+    s.landed = s.empty + kPanels;
     return s;
 }
 // By one thread, before a __syncthreads.
 __device__ __forceinline__ void init_panels(const ProductSmem& s) {
     for (int i = 0; i < kPanels; ++i) {
         mbar_init(&s.full[i], 1);
+        mbar_init(&s.landed[i], 1);
         mbar_init(&s.empty[i], kProdWarps);
     }
     fence_barrier_init();
@@ -310,6 +322,7 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
                                             PanelCount& pc, int unit) {
     using W = WTraits<Job::kWK>;
     constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kSpan = kPanelK / NT;
+    constexpr bool kPairs = panel_pairs<Job::kWK, NT>();
     const int lane = threadIdx.x & 31;
     for (int seg = 0; seg < job.segments; ++seg) {
         const uint16_t* row = lane < 8 * NT ? job.token(unit, seg, lane) : nullptr;
@@ -318,22 +331,58 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
             const int buf = pc.buf(), n = min(kSpan, job.K - k0);
             const int padded = (n + W::kStageK - 1) / W::kStageK * W::kStageK;  // a stage is read whole
             if (!mbar_wait_bounded(ctl, &s.empty[buf], pc.parity() ^ 1u, timeout_ns)) return false;
-            unsigned char* to = s.base + buf * kPanelBytes + lane * kPitch;
+            unsigned char* panel = s.base + buf * kPanelBytes;
             if constexpr (Job::kVecX) {
+                unsigned char* to = panel + lane * kPitch;
                 if (padded > n) {  // zeros past the row's end, before the copies that follow
                     if (row)
                         for (int k = n; k < padded; k += 8) *reinterpret_cast<uint4*>(to + k * 2) = make_uint4(0u, 0u, 0u, 0u);
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&s.full[buf], rows * uint32_t(n) * 2u);
+                uint64_t* in = kPairs ? &s.landed[buf] : &s.full[buf];
+                if constexpr (kPairs) fence_proxy_async_smem();  // the panel's last pairs
+                if (lane == 0) mbar_arrive_expect_tx(in, rows * uint32_t(n) * 2u);
                 __syncwarp();
-                if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, &s.full[buf]);
-            } else {  // rows at odd addresses: a warp-wide copy, row after row
-                for (uint32_t i = 0; i < rows; ++i) {
-                    const uint16_t* from = job.token(unit, seg, int(i));
-                    unsigned char* dst = s.base + buf * kPanelBytes + i * kPitch;
-                    for (int k = lane * 8; k < padded; k += 256) *reinterpret_cast<uint4*>(dst + k * 2) = ld_row8<false>(from, k0 + k, job.K);
+                if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, in);
+                if constexpr (kPairs) {  // put into pairs where they lie
+                    if (!mbar_wait_bounded(ctl, in, pc.parity(), timeout_ns)) return false;
+                    constexpr int kPieces = kSpan / 256, kRows = 8 / kPieces;  // of a lane and row; rows at a time
+                    for (uint32_t i = 0; i < rows; i += kRows) {
+                        uint4 v[kRows][kPieces];
+#pragma unroll
+                        for (int h = 0; h < kRows; ++h)
+#pragma unroll
+                            for (int q = 0; q < kPieces; ++q)
+                                if (i + h < rows) v[h][q] = *reinterpret_cast<const uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16);
+#pragma unroll
+                        for (int h = 0; h < kRows; ++h)
+#pragma unroll
+                            for (int q = 0; q < kPieces; ++q)
+                                if (i + h < rows) *reinterpret_cast<uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16) = paired(v[h][q]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.full[buf]);
+                }
+            } else {  // by loads and stores, the pieces of two rows in flight
+                constexpr int kPieces = kSpan / 256;  // of a lane and row
+                const uint64_t at = reinterpret_cast<uint64_t>(row);
+                for (uint32_t i = 0; i < rows; i += 2) {
+                    uint4 v[2][kPieces];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const auto* from = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, at, int(i) + h));
+#pragma unroll
+                        for (int q = 0; q < kPieces; ++q)
+                            v[h][q] = ld_row8<Job::kVecX>(i + h < rows ? from : nullptr, k0 + (q * 32 + lane) * 8, job.K);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int q = 0; q < kPieces; ++q)
+                            if (i + h < rows && (q * 32 + lane) * 8 < padded)
+                                *reinterpret_cast<uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16) =
+                                    kPairs ? paired(v[h][q]) : v[h][q];
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.full[buf]);
