@@ -15,7 +15,9 @@
 //   2  per (picked expert, 16 rows of D, up to 32 assignments): y = D h, fp32;
 //   3  per (token, columns): the weighted sum over slots in slot order and the residual, each product and
 //      sum rounded to fp32 as in the combine, rounded once.
-// Bound by the bytes of the picked experts' weights; the warp-level product is in wprod.cuh.
+// The warp-level product and what bounds it are in wprod.cuh. Measured on B200, 4-bit weights of 4096 x 2048: 16 picked
+// experts 76 us, 64 of them with 256 assignments 258 us, 3.1 TB/s (the bytes take 127 at the copy rate); bf16 in
+// moe_tensor.cu and at the rule below.
 #include <algorithm>
 #include <type_traits>
 
@@ -196,14 +198,17 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
 }
 
 // The kernel on the fifth-generation tensor cores needs bf16 weights and rows of 16-byte units. By itself it is
-// taken where its units of 128 rows give every third SM one. Its stages of 64 k's go by at 0.4 us at best, so that
-// it wants the work spread; measured on B200, streamed against tensor: 35 and 62 us with 2 picked experts of 4096 x
-// 2048 (32 units), 22 and 31 with 8 of 1024 x 512 (32), 40 and 37 with 8 of 1024 x 1024 (64), 82 and 45 with 16 of
-// 1000 x 712 and 33 assignments each (96), 153 and 144 with 16 of 4096 x 2048 (256), 1837 and 594 with 64 of
-// them and 64 assignments each.
+// taken where an expert gets 24 assignments or more, which the streamed products read the weights again for (32 to a
+// unit) and multiply at the older instructions' rate, and where units of 128 rows fill one and a half rounds of the SMs
+// in both products: its stages of 64 k's go by at 0.4 us at best, so that few units are slow. Measured on B200, us
+// streamed and tensor, by picked experts of H x F and assignments each: 8 of 1024 x 1024 with 16 29 and 37, with 32 45
+// and 39; 16 of 1000 x 712 with 33 62 and 43; 8 of 4096 x 2048 with 16 93 and 94, with 32 155 and 104; with one
+// assignment each, 2 of 4096 x 2048 31 and 62, 16 of them 150 and 145, 8 of 4096 x 14336 480 and 447, 4 of them
+// 222 and 254; 64 of 1024 x 1024 with 2 84 and 88.
 static bool layer_takes_tensor(const MoeLayerArgs& a, int num_sms) {
     if (a.tensor == 0 || a.weight_kind != COLL_WEIGHT_BF16 || !a.vec || !layer_tensor_fits(a)) return false;
-    return a.tensor == 1 || std::min(a.E, a.A) * ((a.F + 127) / 128) >= num_sms / 3;
+    const int experts = std::min(a.E, a.A);
+    return a.tensor == 1 || a.A >= 24 * experts || experts * ((std::min(a.H, a.F) + 127) / 128) * 2 >= num_sms * 3;
 }
 
 cudaError_t launch_moe_layer(const MoeLayerArgs& args, int num_sms, cudaStream_t s) {

@@ -14,7 +14,9 @@
 // room for the id in the integer; for fp32 the ids of all picks are looked up at the end, side by side. The
 // sum over the whole row is formed only where the weights are shares of it. What bounds it is integer
 // instructions, then the launch. Rows of more than 1024 experts are read again for every round, a warp per token
-// (from cache; a row is at most 16 KiB).
+// (from cache; a row is at most 16 KiB). Measured on B200, kernels alone: 8 ranks x 8192 tokens x 64 experts bf16,
+// k = 2, 10.4 us (the bytes take 1.5 at the copy rate); 4 x 4099 x 256 fp32, k = 8, with the gradient 26.7 us (8.1);
+// one token 4.3 us.
 // Scores that are NaN are picked last and make the row's weights NaN; a row of nothing but -inf has
 // weight 0 for every pick.
 #include <algorithm>

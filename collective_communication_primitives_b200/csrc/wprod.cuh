@@ -3,8 +3,10 @@
 //
 //   D[r][n] = sum_k W[r][k] X[n][k],   16 MT weight rows x 8 NT tokens per warp
 //
-// With few tokens the weights' bytes bound the time: every weight is used once per token, so the job
-// is to keep enough loads in flight and to spend few instructions per byte. Weights are the 16-row
+// Every weight is used once per token, so the job is to keep enough loads in flight and to spend few instructions
+// per byte. bf16 weights run at 3 to 5 TB/s on B200. 4-bit weights are bound by instructions, at 2.5 to 3.2 TB/s: 21 (to
+// 8 tokens) or 27 (16) for 256 weights, 11 of them to take them apart, with the integer pipe 43 to 48% busy whether 8
+// or 16 warps share it. Weights are the 16-row
 // operand of the matrix instruction (mma.sync m16n8k16) and tokens its 8 columns, so that one token
 // wastes no more than 7 columns. A sum over k may be taken in any order as long as both operands use
 // the same one, so no weight is ever moved between lanes for the instruction's sake: lane (g, t)

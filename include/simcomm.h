@@ -53,7 +53,7 @@
  *     bounded device wait ran out: a ring, tree or butterfly step for its predecessor, an LL word,
  *     a bulk copy), COLL_ERR_ABORTED (sim_comm_abort was called while such a wait was running),
  *     COLL_ERR_OVERFLOW (an All-to-Allv count or an MoE dispatch exceeds a capacity; nothing is
- *     copied), COLL_ERR_INVALID_ARG (an MoE expert id or routing-map entry out of range),
+ *     copied), COLL_ERR_INVALID_ARG (an MoE expert id, routing-map entry or given token out of range),
  *     COLL_ERR_INTERNAL (an invariant check failed). Collectives are not transactions: after an
  *     asynchronous error the outputs of the failed call are unspecified, and later calls do no
  *     work until sim_comm_reset ([Primer] "Collective 的故障语义不是事务").
@@ -229,7 +229,7 @@ const char* coll_status_string(coll_status_t status);
  *                  16-byte units at 16-byte aligned bases; otherwise the load/store kernel runs)
  *   "moe_layer_tensor"  products of coll_moe_layer with bf16 weights in rows of 16-byte units: 1 = on the
  *                  tcgen05 tensor cores, 0 = streamed through the warps' matrix instructions, -1 = by the
- *                  number of assignments per expert (default)
+ *                  assignments per expert and the number and size of experts (default)
  *   "trace"        1 = keep a record of every call (sim_comm_trace_read), 0 = off (default).
  *                  Every entry point also opens an NVTX range named after its collective, whatever
  *                  this option says (a no-op unless a profiler collects NVTX).
@@ -260,15 +260,16 @@ coll_status_t sim_comm_launch_count(sim_comm_t comm, unsigned long long* out);
  * call's first kernel and one just after its last. */
 typedef struct {
     unsigned long long seq;   /* number of the call among the traced calls of this communicator */
-    const char* coll;         /* "allreduce", "reduce", ..., "moe_combine" (a static string) */
+    const char* coll;         /* "allreduce", "reduce", ..., "logprobs_backward" (a static string) */
     int p;                    /* ranks */
     int dtype;                /* coll_dtype_t */
     int op;                   /* coll_op_t, or -1 where the call takes none */
     int root;                 /* root rank, or -1 where the call takes none */
-    int algo;                 /* coll_algo_t, or -1 for the MoE calls */
+    int algo;                 /* coll_algo_t, or -1 where the call takes none */
     int status;               /* coll_status_t the call returned (asynchronous errors are not here) */
-    unsigned long long n;     /* element count as passed; tokens for the MoE calls; 0 for All-to-Allv,
-                                 whose counts stay on the device */
+    unsigned long long n;     /* element count as passed; tokens for the MoE calls and the 4-bit
+                                 linear, rows for the log probabilities; 0 for All-to-Allv, whose
+                                 counts stay on the device */
     unsigned int launches;    /* kernels the call enqueued */
     float device_ms;          /* time between the two events; -1 when the call launched nothing or its
                                  stream was being captured into a graph */
