@@ -2092,21 +2092,20 @@ static coll_status_t coll_logprobs_impl(sim_comm_t c, const void* const* logits,
     }
     if ((st = sp.check()) != COLL_OK) return st;
     a.n_top = top_n;
-    // CTAs per row. Four run on an SM at a time; a CTA costs its columns and, in columns, 4096 for its start and
-    // end, 12288 with alternatives, and 512 for every part that the last one joins. Full waves cost that each, a last
-    // one that is not full as many quarters as an SM gets CTAs, but two at least (a CTA alone takes half as long as
-    // one of four).
-    // Measured on B200 with V = 131072, us with 1, 2, 4, 8 and 16 parts: 8 rows fp32, 8 alternatives 31, 23, 17, 14,
-    // 14; 64 rows bf16, 4 alternatives 27, 21, 17, 17, 21; 700 rows without 53, 52, 55, 62, 80; 2048 rows with 4 157,
-    // 180, 201, 252, 387.
+    // CTAs per row. Five run on an SM at a time; a CTA costs its columns and, in columns, 4096 for its start and
+    // end, 12288 with alternatives, and 512 for every part that the last one joins. The SM with the most CTAs takes a
+    // fifth of that sum for each, but a CTA alone at the end as long as two (it has less to overlap with).
+    // Measured on B200 with V = 131072, us with 1, 2, 4, 8 and 16 parts: 8 rows fp32, 8 alternatives 31, 23, 18, 14,
+    // 14; 64 rows bf16, 4 alternatives 27, 21, 17, 17, 21; 300 rows 41, 37, 39, 43, 60; 700 rows without 45, 48, 50, 56,
+    // 70; 2048 rows with 4 145, 171, 183, 225, 344.
     a.parts = 1;
     if (rows <= size_t(kLogprobMaxSplitRows)) {
         const size_t sms = size_t(c->num_sms), most = std::min(size_t(kLogprobMaxParts), std::max<size_t>(1, vocab / 1024));
         const size_t fixed = top_n > 0 ? 12288 : 4096;
         size_t best = SIZE_MAX;
         for (size_t q = 1; q <= most; ++q) {
-            const size_t per_sm = (rows * q + sms - 1) / sms, quarters = per_sm % 4 == 1 ? per_sm + 1 : per_sm;
-            const size_t cost = quarters * (vocab / q + fixed + (q > 1 ? 512 * q : 0));
+            const size_t per_sm = (rows * q + sms - 1) / sms, time = per_sm % 5 == 1 ? per_sm + 1 : per_sm;
+            const size_t cost = time * (vocab / q + fixed + (q > 1 ? 512 * q : 0));
             if (cost < best) {
                 best = cost;
                 a.parts = int(q);

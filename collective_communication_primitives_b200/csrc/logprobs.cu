@@ -10,8 +10,8 @@
 // vector of scores brings a larger one; threads, then parts of a row, are joined in a fixed order. Both
 // terms of the entropy's form above are non-negative, so nothing cancels. Few rows are cut into parts, one
 // CTA each; the last part to finish joins them all. Bound by the scores' bytes, then, for 2-byte scores,
-// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 49 us, 4.2 TB/s; 2048 x 131072 bf16 126 us,
-// 4.3 TB/s, with 4 alternatives 157 us; 8 x 131072 fp32 with 8 alternatives 14.4 us.
+// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 49 us, 4.2 TB/s; 2048 x 131072 bf16 112 us,
+// 4.8 TB/s, with 4 alternatives 145 us (120 and 157 with four CTAs on an SM instead of five); 8 x 131072 fp32 with 8 alternatives 14.4 us.
 //
 // Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
 // column wins among equals. The scan itself keeps nothing for them but each thread's maximum, which it has
@@ -416,7 +416,7 @@ __device__ __noinline__ void top_by_lists(const LogprobArgs& a, size_t row, uint
 }
 
 template <int DT, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 5) k_logprobs(const __grid_constant__ LogprobArgs a) {
     __shared__ Stat s_stat[kLpWarps];
     __shared__ TopShared s_top;
     __shared__ float s_w[kLpWarps];
