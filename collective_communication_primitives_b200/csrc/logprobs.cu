@@ -10,8 +10,8 @@
 // vector of scores brings a larger one; threads, then parts of a row, are joined in a fixed order. Both
 // terms of the entropy's form above are non-negative, so nothing cancels. Few rows are cut into parts, one
 // CTA each; the last part to finish joins them all. Bound by the scores' bytes, then, for 2-byte scores,
-// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 49 us, 4.2 TB/s; 2048 x 131072 bf16 112 us,
-// 4.8 TB/s, with 4 alternatives 145 us (120 and 157 with four CTAs on an SM instead of five); 8 x 131072 fp32 with 8 alternatives 14.4 us.
+// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 47 us, 4.3 TB/s; 2048 x 131072 bf16 109 us,
+// 4.9 TB/s, with 4 alternatives 142 us (120 and 157 with four CTAs on an SM instead of five); 8 x 131072 fp32 with 8 alternatives 14.4 us.
 //
 // Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
 // column wins among equals. The scan itself keeps nothing for them but each thread's maximum, which it has
@@ -181,14 +181,35 @@ __device__ __forceinline__ Stat feed_stat(const Feed& f) {
     return Stat{f.m, s0 + s1, u0 + u1, f.raw};
 }
 
+// The largest of a 16-byte vector of scores, NaN if any is.
+template <int DT> __device__ __forceinline__ float vector_top(const uint4& v) {
+    if constexpr (DT == COLL_BF16) {
+        const uint32_t p = max_nan_bf16x2(max_nan_bf16x2(v.x, v.y), max_nan_bf16x2(v.z, v.w));
+        return max_nan(bf16_bits_to_float(p), __uint_as_float(p & 0xffff0000u));
+    } else {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+}
+
+// Makes the sums refer to a maximum of at least `top`.
+__device__ __forceinline__ void feed_raise(Feed& f, float top) {
+    if (!(top <= f.m)) {  // larger, or NaN
+        const float m = top == INFINITY ? __int_as_float(0x7fffffff) : top;
+        const float d = log2_base(f.m) - log2_base(m), scale = ex2(d);
+        const unsigned long long dd = pack2(d, d), ss = pack2(scale, scale), zero = 0ull;
+        f.s = fma2(f.s, ss, zero);
+        f.u = fma2(f.s, dd, fma2(f.u, ss, zero));
+        f.m = m;
+    }
+}
+
 // Adds one 16-byte vector of scores to a thread's sums.
 template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uint4& v) {
     constexpr int L = 16 / Elem<DT>::kBytes;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[L], top;
-    if constexpr (DT == COLL_BF16) {  // maximum and clamp on pairs
-        const uint32_t p = max_nan_bf16x2(max_nan_bf16x2(w[0], w[1]), max_nan_bf16x2(w[2], w[3]));
-        top = max_nan(bf16_bits_to_float(p), __uint_as_float(p & 0xffff0000u));
+    float x[L];
+    const float top = vector_top<DT>(v);
+    if constexpr (DT == COLL_BF16) {  // clamp on pairs
         constexpr uint32_t kFloor2 = 0xD380D380u;  // kLpFloor twice
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -198,20 +219,10 @@ template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uin
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = __uint_as_float(w[q]);
-        top = max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = fmaxf(x[q], kLpFloor);
+        for (int q = 0; q < 4; ++q) x[q] = fmaxf(__uint_as_float(w[q]), kLpFloor);
     }
     f.raw = max_nan(f.raw, top);
-    if (!(top <= f.m)) {  // larger, or NaN
-        const float m = top == INFINITY ? __int_as_float(0x7fffffff) : top;
-        const float d = log2_base(f.m) - log2_base(m), scale = ex2(d);
-        const unsigned long long dd = pack2(d, d), ss = pack2(scale, scale), zero = 0ull;
-        f.s = fma2(f.s, ss, zero);
-        f.u = fma2(f.s, dd, fma2(f.u, ss, zero));
-        f.m = m;
-    }
+    feed_raise(f, top);
     const float base = -log2_base(f.m);
     const unsigned long long bb = pack2(base, base), ll = pack2(kLpLog2e, kLpLog2e);
 #pragma unroll
@@ -247,9 +258,9 @@ template <int DT> struct Piece {
 
 // Calls take(raw vector, scores in it, column of the first) for all columns [v0, v1) of a row; vector i of a
 // piece falls to thread i modulo kLpThreads. Scores at the ends of pieces come as vectors of one score, one per
-// lane of the first warp; missing scores are -inf.
-template <int DT, typename Take>
-__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, Take take) {
+// lane of the first warp; missing scores are -inf. first(raw vectors) sees a warp's first ones before they are taken.
+template <int DT, typename Take, typename First>
+__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, Take take, First first) {
     constexpr int L = Pack16<DT>::L;
     constexpr uint32_t kNone = DT == COLL_BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     const uint32_t warp0 = threadIdx.x & ~31u;
@@ -272,6 +283,7 @@ __device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, u
                 const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
                 raw[q] = i < pc.vecs ? ld_stream_v4(pc.vector(i)) : make_uint4(kNone, kNone, kNone, kNone);
             }
+            if (i0 == 0 && v == v0) first(raw);
 #pragma unroll
             for (int q = 0; q < kLpUnroll; ++q) {
                 const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
@@ -409,7 +421,7 @@ __device__ __noinline__ void top_by_lists(const LogprobArgs& a, size_t row, uint
         Pack16<DT>::unpack(raw, x);
 #pragma unroll
         for (int j = 0; j < L; ++j) top_insert(l, j < cnt && x[j] == x[j] ? top_key(x[j], col + j) : 0ull, a.n_top);
-    });
+    }, [](const uint4 (&)[kLpUnroll]) {});
     __syncthreads();
     if (lane < a.n_top) key[warp * a.n_top + lane] = l.mine;
     __syncthreads();
@@ -429,7 +441,18 @@ __global__ void __launch_bounds__(kLpThreads, 5) k_logprobs(const __grid_constan
     if (s_flag) return;
     const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
     Feed f = feed_none();
-    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); });
+    // A thread's sums refer to the largest of its warp's first vectors from the start: a warp rescales where any of its
+    // threads meets a larger score, and without this it did in two vectors of three (112 us instead of 109 for 2048 x
+    // 131072 bf16).
+    auto begin = [&](const uint4 (&raw)[kLpUnroll]) {
+        float top = vector_top<DT>(raw[0]);
+#pragma unroll
+        for (int q = 1; q < kLpUnroll; ++q) top = max_nan(top, vector_top<DT>(raw[q]));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+        feed_raise(f, top);
+    };
+    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); }, begin);
     Stat st = stat_warp(feed_stat(f));
     if (lane == 0) s_stat[warp] = st;
     __syncthreads();
@@ -554,7 +577,8 @@ __global__ void __launch_bounds__(kLpThreads, 5) k_logprobs(const __grid_constan
 
 // With d = x log2e - B, B = (m + ln_s) log2e rounded: P = 2^d c, c = 2^-(what the rounding of B left out), and
 // ln P = d ln 2 + ln c. So dx = -P (gl + ge (ln P + H)) = 2^d (a0 + a1 d), two constants of the row. Bound by memory:
-// 1023 x 50257 fp32 79 us, 5.2 TB/s, 2048 x 131072 bf16 202 us, 5.3 TB/s on B200.
+// 1023 x 50257 fp32 79 us, 5.2 TB/s, 2048 x 131072 bf16 202 us, 5.3 TB/s on B200 (with three CTAs on an SM instead of
+// four 78 and 221, with five, which spill, 84 and 214).
 struct RowGrad {
     float base, a0, a1;
 };
