@@ -95,6 +95,7 @@ CASES = [
     (1, 1, 2, 1, 32, 32, 32, True), (2, 3, 8, 2, 64, 96, 32, False), (4, 17, 8, 3, 128, 64, 64, True),
     (2, 1, 8, 2, 256, 128, 128, True), (1, 70, 4, 2, 384, 128, 128, False), (2, 9, 4, 2, 512, 256, 256, True),
     (1, 33, 4, 4, 160, 224, 32, True),
+    (1, 512, 4096, 8, 16, 8, 0, True), (2, 256, 4096, 8, 32, 32, 32, False),  # as many assignments as there may be
 ]
 
 
@@ -240,6 +241,24 @@ def test_nan_and_inf_stay_in_their_token():
     assert bool(out[2].isnan().all()) and not bool(out[4].isfinite().all())
     for t in (0, 1, 3, 5):
         assert bool(out[t].isfinite().all())
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_two_communicators_at_once(group):
+    """Each kernel holds every SM it asks for until its grid barriers are passed; two of them take turns."""
+    a, b = Layer(2, 12, 16, 4, 512, 1024, group, seed=31), Layer(4, 5, 8, 2, 1024, 640, group, seed=32)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    with SC.SimComm(2) as ca, SC.SimComm(4) as cb:
+        a.run(ca)
+        b.run(cb)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a.run(ca, stream=sa)
+            b.run(cb, stream=sb)
+        torch.cuda.synchronize()
+        assert ca.async_error() == SC.OK and cb.async_error() == SC.OK
+    a.check()
+    b.check()
 
 
 def test_graph_replays_with_new_tokens_and_calls_between():
