@@ -10,8 +10,8 @@
 // vector of scores brings a larger one; threads, then parts of a row, are joined in a fixed order. Both
 // terms of the entropy's form above are non-negative, so nothing cancels. Few rows are cut into parts, one
 // CTA each; the last part to finish joins them all. Bound by the scores' bytes, then, for 2-byte scores,
-// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 47 us, 4.3 TB/s; 2048 x 131072 bf16 109 us,
-// 4.9 TB/s, with 4 alternatives 142 us (120 and 157 with four CTAs on an SM instead of five); 8 x 131072 fp32 with 8 alternatives 14.4 us.
+// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 47 us, 4.3 TB/s; 2048 x 131072 bf16 106 us,
+// 5.1 TB/s, with 4 alternatives 137 us (five CTAs on an SM; with four 8% and 9% more); 8 x 131072 fp32 with 8 alternatives 14.4 us.
 //
 // Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
 // column wins among equals. The scan itself keeps nothing for them but each thread's maximum, which it has
@@ -203,12 +203,21 @@ __device__ __forceinline__ void feed_raise(Feed& f, float top) {
     }
 }
 
+// Whether the maximum is raised for a batch of kLpUnroll vectors at once or for each as it arrives: 2-byte scores are
+// bound by instructions, 4-byte ones by waiting for the loads. Measured on B200, batch and each: 106 and 109 us for 2048
+// x 131072 bf16, 137 and 142 with 4 alternatives, 54 and 47 for 1023 x 50257 fp32.
+template <int DT> constexpr bool by_batch() { return DT == COLL_BF16; }
+
 // Adds one 16-byte vector of scores to a thread's sums.
 template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uint4& v) {
     constexpr int L = 16 / Elem<DT>::kBytes;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float x[L];
-    const float top = vector_top<DT>(v);
+    if constexpr (!by_batch<DT>()) {
+        const float top = vector_top<DT>(v);
+        f.raw = max_nan(f.raw, top);
+        feed_raise(f, top);
+    }
     if constexpr (DT == COLL_BF16) {  // clamp on pairs
         constexpr uint32_t kFloor2 = 0xD380D380u;  // kLpFloor twice
 #pragma unroll
@@ -221,8 +230,6 @@ template <int DT> __device__ __forceinline__ void feed_vector(Feed& f, const uin
 #pragma unroll
         for (int q = 0; q < 4; ++q) x[q] = fmaxf(__uint_as_float(w[q]), kLpFloor);
     }
-    f.raw = max_nan(f.raw, top);
-    feed_raise(f, top);
     const float base = -log2_base(f.m);
     const unsigned long long bb = pack2(base, base), ll = pack2(kLpLog2e, kLpLog2e);
 #pragma unroll
@@ -258,9 +265,10 @@ template <int DT> struct Piece {
 
 // Calls take(raw vector, scores in it, column of the first) for all columns [v0, v1) of a row; vector i of a
 // piece falls to thread i modulo kLpThreads. Scores at the ends of pieces come as vectors of one score, one per
-// lane of the first warp; missing scores are -inf. first(raw vectors) sees a warp's first ones before they are taken.
-template <int DT, typename Take, typename First>
-__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, Take take, First first) {
+// lane of the first warp; missing scores are -inf. batch(raw vectors, whether they are the warp's
+// first) comes before the vectors are taken.
+template <int DT, typename Take, typename Batch>
+__device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, uint32_t v0, uint32_t v1, Take take, Batch batch) {
     constexpr int L = Pack16<DT>::L;
     constexpr uint32_t kNone = DT == COLL_BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
     const uint32_t warp0 = threadIdx.x & ~31u;
@@ -274,6 +282,8 @@ __device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, u
                 if constexpr (DT == COLL_BF16) raw.x = (kNone & 0xffff0000u) | reinterpret_cast<const uint16_t*>(pc.base)[at];
                 else raw.x = reinterpret_cast<const uint32_t*>(pc.base)[at];
             }
+            const uint4 none = make_uint4(kNone, kNone, kNone, kNone), ends[kLpUnroll] = {raw, none, none, none};
+            batch(ends, false);
             take(raw, cnt, v + at);
         }
         for (uint32_t i0 = 0; i0 < pc.vecs; i0 += kLpThreads * kLpUnroll) {
@@ -283,7 +293,7 @@ __device__ __forceinline__ void scan_columns(const LogprobArgs& a, size_t row, u
                 const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
                 raw[q] = i < pc.vecs ? ld_stream_v4(pc.vector(i)) : make_uint4(kNone, kNone, kNone, kNone);
             }
-            if (i0 == 0 && v == v0) first(raw);
+            batch(raw, i0 == 0 && v == v0);
 #pragma unroll
             for (int q = 0; q < kLpUnroll; ++q) {
                 const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
@@ -421,7 +431,7 @@ __device__ __noinline__ void top_by_lists(const LogprobArgs& a, size_t row, uint
         Pack16<DT>::unpack(raw, x);
 #pragma unroll
         for (int j = 0; j < L; ++j) top_insert(l, j < cnt && x[j] == x[j] ? top_key(x[j], col + j) : 0ull, a.n_top);
-    }, [](const uint4 (&)[kLpUnroll]) {});
+    }, [](const uint4 (&)[kLpUnroll], bool) {});
     __syncthreads();
     if (lane < a.n_top) key[warp * a.n_top + lane] = l.mine;
     __syncthreads();
@@ -442,17 +452,19 @@ __global__ void __launch_bounds__(kLpThreads, 5) k_logprobs(const __grid_constan
     const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
     Feed f = feed_none();
     // A thread's sums refer to the largest of its warp's first vectors from the start: a warp rescales where any of its
-    // threads meets a larger score, and without this it did in two vectors of three (112 us instead of 109 for 2048 x
-    // 131072 bf16).
-    auto begin = [&](const uint4 (&raw)[kLpUnroll]) {
+    // threads meets a larger score, and without this it did in two vectors of three (3% more for 2048 x 131072 bf16).
+    auto batch = [&](const uint4 (&raw)[kLpUnroll], bool start) {
+        if (!by_batch<DT>() && !start) return;
         float top = vector_top<DT>(raw[0]);
 #pragma unroll
         for (int q = 1; q < kLpUnroll; ++q) top = max_nan(top, vector_top<DT>(raw[q]));
+        if constexpr (by_batch<DT>()) f.raw = max_nan(f.raw, top);
+        if (start)
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = 16; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
         feed_raise(f, top);
     };
-    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); }, begin);
+    scan_columns<DT>(a, row, v0, v1, [&](const uint4& raw, int, uint32_t) { feed_vector<DT>(f, raw); }, batch);
     Stat st = stat_warp(feed_stat(f));
     if (lane == 0) s_stat[warp] = st;
     __syncthreads();
