@@ -32,6 +32,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "panels.h"
 
 namespace simcomm {
 
@@ -51,8 +52,6 @@ template <int WK> struct WTraits {
 constexpr int kProdWarps = 8;                       // warps that multiply
 constexpr int kProdThreads = (kProdWarps + 1) * 32;  // and one that copies tokens
 constexpr int kRing = 4;                            // stages of a warp's weight ring
-constexpr int kPanelK = 1024;                       // a panel: 8 NT tokens x kPanelK / NT k's
-constexpr int kPanels = 2;
 constexpr int kMaxNT = 4;
 template <int WK> constexpr int panel_pad() { return WK == W_Q4X4 ? 32 : WK == W_Q4X2 ? 16 : 64; }  // bytes per row
 template <int WK, int NT> constexpr int panel_pitch() { return kPanelK / NT * 2 + panel_pad<WK>(); }
@@ -311,13 +310,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// How many panels have gone by, the same for both sides.
-struct PanelCount {
-    uint32_t n = 0;
-    __device__ int buf() const { return int(n % kPanels); }
-    __device__ uint32_t parity() const { return n / kPanels & 1u; }
-};
-
 // The copying warp's side of a unit. False after a wait that ran out.
 template <int NT, typename Job>
 __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint64_t timeout_ns, const ProductSmem& s,
@@ -348,7 +340,8 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
                 __syncwarp();
                 if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, in);
                 if constexpr (kPairs) {  // put into pairs where they lie
-                    if (!mbar_wait_bounded(ctl, in, pc.parity(), timeout_ns)) return false;
+                    if (!mbar_wait_bounded(ctl, in, pc.landed_parity(), timeout_ns)) return false;
+                    pc.used_landed();
                     constexpr int kPieces = kSpan / 256, kRows = 8 / kPieces;  // of a lane and row; rows at a time
                     for (uint32_t i = 0; i < rows; i += kRows) {
                         uint4 v[kRows][kPieces];
