@@ -328,14 +328,14 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
             unsigned char* panel = s.base + buf * kPanelBytes;
             if constexpr (Job::kVecX) {
                 unsigned char* to = panel + lane * kPitch;
-                if (padded > n) {  // zeros past the row's end, before the copies that follow
-                    if (row)
-                        for (int k = n; k < padded; k += 8) *reinterpret_cast<uint4*>(to + k * 2) = make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                }
+                if (padded > n && row)  // zeros past the row's end
+                    for (int k = n; k < padded; k += 8) *reinterpret_cast<uint4*>(to + k * 2) = make_uint4(0u, 0u, 0u, 0u);
+                // This warp's ordinary writes to the buffer come before the copies that follow: zeros, those of the
+                // panel that it held before (of any length), and that panel's pairs (of a unit that makes them, which
+                // this one need not be).
+                fence_proxy_async_smem();
                 __syncwarp();
                 uint64_t* in = kPairs ? &s.landed[buf] : &s.full[buf];
-                if constexpr (kPairs) fence_proxy_async_smem();  // the panel's last pairs
                 if (lane == 0) mbar_arrive_expect_tx(in, rows * uint32_t(n) * 2u);
                 __syncwarp();
                 if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, in);
