@@ -1927,6 +1927,7 @@ static coll_status_t coll_linear_w4_impl(sim_comm_t c, const void* const* x, con
     a.out_bf16 = dt == COLL_BF16;
     a.x_vec = vec ? 1 : 0;
     a.timeout_ns = uint64_t(c->timeout_ns);
+    a.fault_cta = int(c->fault_skip_rank);
     a.ctl = make_ctl(c);
     cudaError_t e = launch_linear(a, c->num_sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "4-bit linear launch");
@@ -2020,6 +2021,7 @@ static coll_status_t coll_moe_layer_impl(sim_comm_t c, const void* const* x, con
     a.h = reinterpret_cast<uint16_t*>(c->moe);
     a.y = reinterpret_cast<float*>(c->moe + b_h);
     a.timeout_ns = uint64_t(c->timeout_ns);
+    a.fault_cta = int(c->fault_skip_rank);
     a.st = c->dstate;
     a.ctl = make_ctl(c);
     cudaError_t e = launch_moe_layer(a, c->num_sms, static_cast<cudaStream_t>(stream));

@@ -473,5 +473,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(const Ctl& ctl, uint64_t* bar,
     raise_status(ctl, COLL_ERR_INTERNAL);
     return false;
 }
+// The same by a whole warp, whose lanes agree: false if the wait of any lane ran out.
+__device__ __forceinline__ bool mbar_wait_warp(const Ctl& ctl, uint64_t* bar, uint32_t parity, uint64_t timeout_ns) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(ctl, bar, parity, timeout_ns));
+}
 
 }  // namespace simcomm

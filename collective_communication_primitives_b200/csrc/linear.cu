@@ -86,20 +86,22 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
     PanelCount pc;
     if (threadIdx.x >= kProdWarps * 32) {
         for (int u = blockIdx.x; u < a.units; u += gridDim.x)
-            if (!copy_tokens<NT>(job, a.ctl, a.timeout_ns, s, pc, u)) return;
+            if (!copy_tokens<NT>(job, a.ctl, a.timeout_ns, s, pc, u)) break;
+        land_panels(a.ctl, s, pc);
         return;
     }
     Multiplier<Job> mul(job, s, blockIdx.x, a.units, gridDim.x);
+    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up(a.ctl);
     for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
         float acc[MT][NT][4];
-        if (!mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc)) break;
+        mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc);
         const typename Job::At x = job.at(u);
         // stored to the ranks that get it
         const int first = a.row ? (a.view_rank >= 0 ? a.view_rank : 0) : x.rank;
         const int last = a.row ? (a.view_rank >= 0 ? a.view_rank + 1 : a.p) : x.rank + 1;
         finish_unit<false, MT, NT>(s, 1 << job.split_shift(u), acc, [&](int tile, int r, int c, float v, float) {
             const size_t row = x.row0 + tile * (16 * MT) + r, token = x.token0 + c;
-            if (row >= a.N || token >= a.T) return;
+            if (row >= a.N || token >= a.T || !mul.live) return;
             for (int d = first; d < last; ++d) {
                 if (a.out_bf16) st_out<true>(a.out[d], token * a.N + row, v);
                 else st_out<false>(a.out[d], token * a.N + row, v);

@@ -109,36 +109,34 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
     const Job job(a, l, nact);
     const int units = job.units();
     if (threadIdx.x >= kProdWarps * 32) {
-        for (int u = blockIdx.x; u < units; u += gridDim.x)
-            if (!with_tiles(job.at(u).count, [&](auto nt) {
-                    return copy_tokens<decltype(nt)::value>(job, a.ctl, a.timeout_ns, s, pc, u);
-                }))
-                return false;
-        return true;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x)
+            ok = with_tiles(job.at(u).count, [&](auto nt) {
+                return copy_tokens<decltype(nt)::value>(job, a.ctl, a.timeout_ns, s, pc, u);
+            });
+        land_panels(a.ctl, s, pc);
+        return ok;
     }
     Multiplier<Job> mul(job, s, blockIdx.x, units, gridDim.x);
+    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up(a.ctl);
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const typename Job::At x = job.at(u);
-        const bool ok = with_tiles(x.count, [&](auto nt) {
+        with_tiles(x.count, [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             float acc[kLayTiles][NT][4];
-            if (!mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc)) return false;
+            mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc);
             finish_unit<UP, kLayTiles, NT>(s, 1 << job.shift, acc, [&](int tile, int r, int c, float v, float v2) {
                 const int row = x.row0 + tile * Job::kTile + (UP ? r / 16 * 8 + r % 8 : r);
-                if (row >= job.rows_all || c >= x.count) return;
+                if (row >= job.rows_all || c >= x.count || !mul.live) return;
                 const int asg = l.list[x.first + c];
                 if constexpr (UP) a.h[size_t(asg) * a.h_stride + row] = float_to_bf16_bits(silu_mul(v, v2));
                 else a.y[size_t(asg) * a.H + row] = v;
             });
             return true;
         });
-        if (!ok) {
-            mul.drain();
-            return false;
-        }
     }
     mul.drain();
-    return true;
+    return mul.live;
 }
 
 template <int WK, bool VEC>

@@ -31,6 +31,7 @@ constexpr int kTcTileBytes = 128 * kTcK * 2;                      // 128 rows of
 constexpr int kTcTiles = 2;                                       // row tiles of a unit, at most
 constexpr int kTcStages = 16;                                     // stages, at most
 constexpr int kTcRing = 192 * 1024;                               // bytes of the ring of stages, at least
+constexpr uint64_t kTcIdleNs = 1000000000ull;                     // longest wait for instructions in flight before leaving
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -66,9 +67,10 @@ __device__ __forceinline__ void tc_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
-// Barriers of a CTA: stages copied and free, one set for each phase, accumulators finished and read.
+// Barriers of a CTA: stages copied and free, one set for each phase, accumulators finished and read, and no instruction
+// left in flight (after a wait that ran out).
 struct TcBars {
-    uint64_t full[2][kTcStages], empty[2][kTcStages], done[2], read[2];
+    uint64_t full[2][kTcStages], empty[2][kTcStages], done[2], read[2], idle;
 };
 
 // A unit: `span` rows from row0 of an expert's output, assignments [first, first + count). The span is a
@@ -212,6 +214,14 @@ template <bool UP> __device__ __forceinline__ void tc_prefetch(const TcPhase<UP>
     }
 }
 
+// What the issuing thread does after a wait that ran out: the matrix instructions that it has issued read shared memory
+// and write the accumulators, so the CTA stays until they are through.
+__device__ __forceinline__ bool tc_quit(const Ctl& ctl, TcBars& bars) {
+    tc_commit(&bars.idle);
+    mbar_wait_bounded(ctl, &bars.idle, 0u, kTcIdleNs);
+    return false;
+}
+
 // The issuing thread's side of a phase. acc: accumulators begun.
 template <bool UP>
 __device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, TcBars& bars, uint32_t tmem, uint32_t& acc) {
@@ -225,11 +235,15 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, T
         const int nb = (ph.at(u).count + 15) / 16;
         // fp32 accumulator, bf16 operands, both K-major, N = 16 nb, M = 128
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(nb * 2) << 17) | (8u << 24);
-        if (!mbar_wait_bounded(a.ctl, &bars.read[acc & 1], (acc / 2 & 1u) ^ 1u, a.timeout_ns)) return false;
+        if (!mbar_wait_bounded(a.ctl, &bars.read[acc & 1], (acc / 2 & 1u) ^ 1u, a.timeout_ns)) return tc_quit(a.ctl, bars);
         tc_fence_after();
         const uint32_t d = tmem + (acc & 1) * (M * 128);
         for (int kb = 0; kb < kbs; ++kb) {
-            if (!mbar_wait_bounded(a.ctl, &full[slot], parity, a.timeout_ns)) return false;
+            if (!mbar_wait_bounded(a.ctl, &full[slot], parity, a.timeout_ns)) return tc_quit(a.ctl, bars);
+            if (int(blockIdx.x) == a.fault_cta && kb == 1) {  // fault injection: as if the wait had run out
+                raise_status(a.ctl, COLL_ERR_TIMEOUT);
+                return tc_quit(a.ctl, bars);
+            }
             // What the copies wrote is read through another path. The fence stands on this side: a copying thread's
             // would wait for all its copies in flight, 0.7 us a stage.
             fence_proxy_async_smem();
@@ -260,8 +274,7 @@ __device__ __forceinline__ bool tc_finish(const TcPhase<UP>& ph, TcBars& bars, u
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, units = ph.units();
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++acc) {
         const auto x = ph.at(u);
-        if (!mbar_wait_bounded(a.ctl, &bars.done[acc & 1], acc / 2 & 1u, a.timeout_ns)) return false;
-        __syncwarp();
+        if (!mbar_wait_warp(a.ctl, &bars.done[acc & 1], acc / 2 & 1u, a.timeout_ns)) return false;
         tc_fence_after();
         const uint32_t d = tmem + (acc & 1) * (M * 128) + (uint32_t(warp * 32) << 16);
 #pragma unroll
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(const __grid_const
             mbar_init(&bars.done[i], 1);
             mbar_init(&bars.read[i], kTcEpilogue);
         }
+        mbar_init(&bars.idle, 1);
         fence_barrier_init();
     }
     __syncthreads();

@@ -310,6 +310,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
+constexpr uint64_t kLandNs = 1000000000ull;  // longest wait for copies in flight before a CTA may leave
+
 // The copying warp's side of a unit. False after a wait that ran out.
 template <int NT, typename Job>
 __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint64_t timeout_ns, const ProductSmem& s,
@@ -324,7 +326,7 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
         for (int k0 = 0; k0 < job.K; k0 += kSpan, ++pc.n) {
             const int buf = pc.buf(), n = min(kSpan, job.K - k0);
             const int padded = (n + W::kStageK - 1) / W::kStageK * W::kStageK;  // a stage is read whole
-            if (!mbar_wait_bounded(ctl, &s.empty[buf], pc.parity() ^ 1u, timeout_ns)) return false;
+            if (!mbar_wait_warp(ctl, &s.empty[buf], pc.parity() ^ 1u, timeout_ns)) return false;
             unsigned char* panel = s.base + buf * kPanelBytes;
             if constexpr (Job::kVecX) {
                 unsigned char* to = panel + lane * kPitch;
@@ -340,7 +342,10 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
                 __syncwarp();
                 if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, in);
                 if constexpr (kPairs) {  // put into pairs where they lie
-                    if (!mbar_wait_bounded(ctl, in, pc.landed_parity(), timeout_ns)) return false;
+                    if (!mbar_wait_warp(ctl, in, pc.landed_parity(), timeout_ns)) {
+                        mbar_wait_warp(ctl, in, pc.landed_parity(), kLandNs);
+                        return false;
+                    }
                     pc.used_landed();
                     constexpr int kPieces = kSpan / 256, kRows = 8 / kPieces;  // of a lane and row; rows at a time
                     for (uint32_t i = 0; i < rows; i += kRows) {
@@ -387,6 +392,15 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
     return true;
 }
 
+// The copying warp's last step, after its units or a wait that ran out: its copies are in before the CTA can leave, for
+// they write the CTA's shared memory. (The multiplying warps wait for them too, unless their waits run out.)
+__device__ __forceinline__ void land_panels(const Ctl& ctl, const ProductSmem& s, PanelCount pc) {
+    for (int i = 0; i < kPanels && pc.n > 0; ++i) {
+        --pc.n;
+        mbar_wait_warp(ctl, &s.full[pc.buf()], pc.parity(), kLandNs);
+    }
+}
+
 // Where a multiplying warp's copies have got to: a stage of a segment of a unit.
 template <int MT> struct Ahead {
     const char* w[MT][2];
@@ -402,6 +416,7 @@ template <typename Job> struct Multiplier {
     int warp, lane, g, t, stages;
     uint32_t ring;
     int slot = 0;
+    bool live = true;          // false after a wait that ran out: the warp's sums are 0, and it only meets the others
     Ahead<MT> ahead;
     Q4Consts qc;
 
@@ -449,9 +464,10 @@ template <typename Job> struct Multiplier {
         cp_async_commit();
     }
 
-    // The warp's sums of a unit over its share of the stages. False after a wait that ran out.
+    // The warp's sums of a unit over its share of the stages (0 where the warp is not live). Every warp of the CTA goes
+    // through all units, since warps that share a row tile meet at a barrier.
     template <int NT>
-    __device__ __forceinline__ bool unit(const Ctl& ctl, uint64_t timeout_ns, PanelCount& pc, int u, float (&acc)[MT][NT][4]) {
+    __device__ __forceinline__ void unit(const Ctl& ctl, uint64_t timeout_ns, PanelCount& pc, int u, float (&acc)[MT][NT][4]) {
         constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kPanelStages = kPanelK / NT / W::kStageK;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -459,6 +475,7 @@ template <typename Job> struct Multiplier {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+        if (!live) return;
         const int shift = job.split_shift(u), splits = 1 << shift, tile = warp >> shift, split = warp & (splits - 1);
         const int groups = (((job.K + W::kChunk - 1) / W::kChunk - 1) >> job.chunk_shift) + 1;
         for (int seg = 0; seg < job.segments; ++seg) {
@@ -471,7 +488,10 @@ template <typename Job> struct Multiplier {
             int st = split;
             for (int p0 = 0; p0 < stages; p0 += kPanelStages, ++pc.n) {
                 const int buf = pc.buf(), end = min(p0 + kPanelStages, stages);
-                if (!mbar_wait_bounded(ctl, &s.full[buf], pc.parity(), timeout_ns)) return false;
+                if (!mbar_wait_warp(ctl, &s.full[buf], pc.parity(), timeout_ns)) {
+                    live = false;
+                    return;
+                }
                 const unsigned char* tok = s.base + buf * kPanelBytes + g * kPitch + t * W::kLaneK * 2;
                 for (; st < end; st += splits) {
                     const StageScales<Job::kWK, MT> sc = next;
@@ -487,7 +507,12 @@ template <typename Job> struct Multiplier {
                 if (lane == 0) mbar_arrive(&s.empty[buf]);
             }
         }
-        return true;
+    }
+
+    // Host-side fault injection: what a wait of the warp that runs out does.
+    __device__ __forceinline__ void give_up(const Ctl& ctl) {
+        if (lane == 0) raise_status(ctl, COLL_ERR_TIMEOUT);
+        live = false;
     }
 
     // Waits for the warp's copies in flight (none after a whole sequence but empty groups).
