@@ -470,7 +470,7 @@ __device__ __forceinline__ bool mbar_wait_bounded(const Ctl& ctl, uint64_t* bar,
         if (mbar_try_wait(bar, parity)) return true;
         if ((it & 255u) == 0u && globaltimer_ns() - t0 > timeout_ns) break;
     }
-    raise_status(ctl, COLL_ERR_INTERNAL);
+    raise_status(ctl, COLL_ERR_TIMEOUT);
     return false;
 }
 // The same by a whole warp, whose lanes agree: false if the wait of any lane ran out.

@@ -269,7 +269,7 @@ struct LinearArgs {
     uint32_t tile_blocks, token_tiles;   // set by the launcher
     int units, tail_first, tail_shift;   // set by the launcher: units from tail_first on are 2^-tail_shift of one
     uint64_t timeout_ns;
-    int fault_cta;                       // fault injection: a warp of this CTA gives up (-1: none)
+    int fault_cta;                       // fault injection: a warp of this CTA falls silent (-1: none)
     Ctl ctl;
 };
 
@@ -301,7 +301,7 @@ struct MoeLayerArgs {
     size_t h_stride;
     float* y;                            // scratch: [A][H]
     uint64_t timeout_ns;
-    int fault_cta;                       // fault injection: a warp of this CTA gives up (-1: none)
+    int fault_cta;                       // fault injection: a warp of this CTA falls silent (-1: none)
     DevState* st;
     Ctl ctl;
 };

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
         return;
     }
     Multiplier<Job> mul(job, s, blockIdx.x, a.units, gridDim.x);
-    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up(a.ctl);
+    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up();
     for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
         float acc[MT][NT][4];
         mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
             }
         });
     }
-    mul.drain();
+    mul.drain(a.ctl);
 }
 
 template <int WK, int MT, int NT> static cudaError_t launch_linear_kind(const LinearArgs& a, int num_sms, cudaStream_t s) {

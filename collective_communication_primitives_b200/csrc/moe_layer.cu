@@ -118,7 +118,7 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
         return ok;
     }
     Multiplier<Job> mul(job, s, blockIdx.x, units, gridDim.x);
-    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up(a.ctl);
+    if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up();
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const typename Job::At x = job.at(u);
         with_tiles(x.count, [&](auto nt) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
             return true;
         });
     }
-    mul.drain();
+    mul.drain(a.ctl);
     return mul.live;
 }
 

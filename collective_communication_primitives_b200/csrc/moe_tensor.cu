@@ -240,10 +240,7 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, T
         const uint32_t d = tmem + (acc & 1) * (M * 128);
         for (int kb = 0; kb < kbs; ++kb) {
             if (!mbar_wait_bounded(a.ctl, &full[slot], parity, a.timeout_ns)) return tc_quit(a.ctl, bars);
-            if (int(blockIdx.x) == a.fault_cta && kb == 1) {  // fault injection: as if the wait had run out
-                raise_status(a.ctl, COLL_ERR_TIMEOUT);
-                return tc_quit(a.ctl, bars);
-            }
+            if (int(blockIdx.x) == a.fault_cta && kb == 1) return tc_quit(a.ctl, bars);  // fault injection
             // What the copies wrote is read through another path. The fence stands on this side: a copying thread's
             // would wait for all its copies in flight, 0.7 us a stage.
             fence_proxy_async_smem();

@@ -509,14 +509,15 @@ template <typename Job> struct Multiplier {
         }
     }
 
-    // Host-side fault injection: what a wait of the warp that runs out does.
-    __device__ __forceinline__ void give_up(const Ctl& ctl) {
-        if (lane == 0) raise_status(ctl, COLL_ERR_TIMEOUT);
-        live = false;
-    }
+    // Host-side fault injection: the warp falls silent, as after a wait that ran out.
+    __device__ __forceinline__ void give_up() { live = false; }
 
-    // Waits for the warp's copies in flight (none after a whole sequence but empty groups).
-    __device__ __forceinline__ void drain() { cp_async_wait<0>(); }
+    // After the last unit: waits for the warp's copies in flight (none after a whole sequence but empty groups), and
+    // reports sums that are missing, in case nobody had to wait for this warp.
+    __device__ __forceinline__ void drain(const Ctl& ctl) {
+        cp_async_wait<0>();
+        if (!live && lane == 0) raise_status(ctl, COLL_ERR_TIMEOUT);
+    }
 };
 
 __device__ __forceinline__ void sync_multipliers() { asm volatile("bar.sync 1, %0;" :: "n"(kProdWarps * 32) : "memory"); }

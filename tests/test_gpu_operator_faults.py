@@ -1,7 +1,7 @@
 """Failure detection of the 4-bit linear and the expert layer, tested without a GPU fault: host-side fault injection
-(option fault_skip_rank: one warp of a CTA gives up, as after a wait that ran out) leaves the CTA's other warps without
-tokens, free buffers or finished sums. Each of their waits runs out, the kernel returns, the call reports an error, and
-sim_comm_reset makes the communicator usable again."""
+(option fault_skip_rank: one warp of a CTA falls silent) leaves the CTA's other warps without tokens, free buffers or
+finished sums. Each of their waits runs out, the kernel returns, the call reports COLL_ERR_TIMEOUT, and sim_comm_reset
+makes the communicator usable again."""
 import time
 
 import pytest
@@ -21,10 +21,10 @@ def _fails_and_recovers(c, run, cta):
     run()
     torch.cuda.synchronize()
     assert time.time() - t0 < 5.0
-    failed = c.async_error()
-    assert failed != SC.OK
-    with pytest.raises(SC.SimCommError):  # refused until reset
+    assert c.async_error() == SC.TIMEOUT
+    with pytest.raises(SC.SimCommError) as e:  # refused until reset
         run()
+    assert e.value.status == SC.TIMEOUT
     c.set_option("fault_skip_rank", -1)
     c.reset()
     run()
