@@ -2016,7 +2016,8 @@ static coll_status_t coll_moe_layer_impl(sim_comm_t c, const void* const* x, con
     a.tensor = int(c->moe_layer_tensor);
     a.T = tokens;
     a.h_stride = round_up(ffn, 8);
-    const size_t b_h = align_up(A * a.h_stride * 2, 256);
+    a.h_part = A * a.h_stride;
+    const size_t b_h = align_up(2 * a.h_part * 2, 256);
     if ((st = ensure_moe(c, b_h + A * hidden * 4)) != COLL_OK) return st;
     a.h = reinterpret_cast<uint16_t*>(c->moe);
     a.y = reinterpret_cast<float*>(c->moe + b_h);

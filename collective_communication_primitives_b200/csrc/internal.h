@@ -297,8 +297,8 @@ struct MoeLayerArgs {
     int tensor_ring;                     // set by the launcher: bytes of the tensor kernel's ring of stages
     int shift_up, shift_down, blocks_up, blocks_down, chunk_shift;  // set by the launcher
     size_t T;
-    uint16_t* h;                         // scratch: bf16 [A][h_stride]
-    size_t h_stride;
+    uint16_t* h;                         // scratch: bf16 [2][A][h_stride], what rounding left out behind the rounded values
+    size_t h_stride, h_part;             // h_part = A * h_stride
     float* y;                            // scratch: [A][H]
     uint64_t timeout_ns;
     int fault_cta;                       // fault injection: a warp of this CTA falls silent (-1: none)

@@ -28,6 +28,7 @@ template <bool BF16> __device__ __forceinline__ void st_out(void* p, size_t i, f
 template <int WK, bool VEC, int MT, int NT> struct LinearJob {
     static constexpr int kWK = WK, kMT = MT;
     static constexpr bool kVecW = true, kVecX = VEC;
+    static constexpr ptrdiff_t part = 0;
     const LinearArgs& a;
     int K, segments, chunk_shift;
 
@@ -74,7 +75,7 @@ template <int WK, bool VEC, int MT, int NT>
 __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_constant__ LinearArgs a) {
     extern __shared__ __align__(128) unsigned char s_raw[];
     __shared__ int s_fail;
-    const ProductSmem s = product_layout<MT>(s_raw);
+    const ProductSmem s = product_layout<MT, 1>(s_raw);
     if (threadIdx.x == 0) {
         s_fail = status_failed(a.ctl);
         init_panels(s);
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
     PanelCount pc;
     if (threadIdx.x >= kProdWarps * 32) {
         for (int u = blockIdx.x; u < a.units; u += gridDim.x)
-            if (!copy_tokens<NT>(job, a.ctl, a.timeout_ns, s, pc, u)) break;
+            if (!copy_tokens<NT, 1>(job, a.ctl, a.timeout_ns, s, pc, u)) break;
         land_panels(a.ctl, s, pc);
         return;
     }
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
     if (int(blockIdx.x) == a.fault_cta && threadIdx.x < 32) mul.give_up();
     for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
         float acc[MT][NT][4];
-        mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc);
+        mul.template unit<NT, 1>(a.ctl, a.timeout_ns, pc, u, acc);
         const typename Job::At x = job.at(u);
         // stored to the ranks that get it
         const int first = a.row ? (a.view_rank >= 0 ? a.view_rank : 0) : x.rank;
@@ -113,10 +114,10 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_linear_q4(const __grid_cons
 
 template <int WK, int MT, int NT> static cudaError_t launch_linear_kind(const LinearArgs& a, int num_sms, cudaStream_t s) {
     auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem<MT>());
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, product_smem<MT, 1>());
         if (e != cudaSuccess) return e;
         const unsigned grid = unsigned(std::min(a.units, num_sms));
-        kernel<<<grid, kProdThreads, product_smem<MT>(), s>>>(a);
+        kernel<<<grid, kProdThreads, product_smem<MT, 1>(), s>>>(a);
         return cudaGetLastError();
     };
     return a.x_vec ? go(k_linear_q4<WK, true, MT, NT>) : go(k_linear_q4<WK, false, MT, NT>);

@@ -9,9 +9,9 @@
 //      another (redundant, but shorter than a barrier);
 //   1  per (picked expert, 8 rows of G and of U, up to 32 of its assignments): both products, then
 //      h = silu(g) u. A warp's 16-row tile holds G's rows in its upper half and U's in its lower half,
-//      so that one lane's accumulators hold g and u of the same element. h is rounded to bf16, the type
-//      that the second product's instruction takes (its relative error of 2^-9 a term averages out in a
-//      sum of F terms to less than the rounding of the output);
+//      so that one lane's accumulators hold g and u of the same element. The second product's instruction
+//      takes bf16; h goes into it in two parts, 16 bits of it. In one part its rounding would show: the error of
+//      a layer without a residual grew from the output's rounding alone, 1.66e-3, to 2.37e-3;
 //   2  per (picked expert, 16 rows of D, up to 32 assignments): y = D h, fp32;
 //   3  per (token, columns): the weighted sum over slots in slot order and the residual, each product and
 //      sum rounded to fp32 as in the combine, rounded once.
@@ -35,15 +35,17 @@ constexpr int kLayTiles = 2;
 template <int WK, bool VEC, bool UP> struct LayerJob {
     static constexpr int kWK = WK, kMT = kLayTiles;
     static constexpr bool kVecW = WTraits<WK>::kQ4 || VEC, kVecX = VEC;
+    static constexpr int kParts = UP ? 1 : kLayParts;
     static constexpr int kTile = (UP ? 8 : 16) * kMT;  // rows of the output in a group of row tiles
     const MoeLayerArgs& a;
     const LayerLists& l;
     int nact;
     int K, segments, shift, chunk_shift, rows_all, blocks;
+    ptrdiff_t part;
 
     __device__ __forceinline__ LayerJob(const MoeLayerArgs& a_, const LayerLists& l_, int nact_)
         : a(a_), l(l_), nact(nact_), K(UP ? a_.H : a_.F), segments(1), shift(UP ? a_.shift_up : a_.shift_down),
-          chunk_shift(a_.chunk_shift), rows_all(UP ? a_.F : a_.H), blocks(UP ? a_.blocks_up : a_.blocks_down) {}
+          chunk_shift(a_.chunk_shift), rows_all(UP ? a_.F : a_.H), blocks(UP ? a_.blocks_up : a_.blocks_down), part(a_.h_part) {}
 
     __device__ __forceinline__ int split_shift(int) const { return shift; }
     __device__ __forceinline__ int units() const { return l.act_tile[nact] * blocks; }
@@ -85,12 +87,11 @@ template <int WK, bool VEC, bool UP> struct LayerJob {
     __device__ __forceinline__ const uint16_t* token(int u, int, int n) const {
         const At x = at(u);
         if (n >= x.count) return nullptr;
-        const int asg = l.list[x.first + n];
         if constexpr (UP) {
-            const int tok = asg / a.k;
+            const int tok = l.list[x.first + n] / a.k;
             return a.x[a.rank0 + tok / int(a.T)] + size_t(tok % int(a.T)) * a.H;
         } else {
-            return a.h + size_t(asg) * a.h_stride;
+            return a.h + size_t(l.list[x.first + n]) * a.h_stride;
         }
     }
 };
@@ -112,7 +113,7 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x)
             ok = with_tiles(job.at(u).count, [&](auto nt) {
-                return copy_tokens<decltype(nt)::value>(job, a.ctl, a.timeout_ns, s, pc, u);
+                return copy_tokens<decltype(nt)::value, Job::kParts>(job, a.ctl, a.timeout_ns, s, pc, u);
             });
         land_panels(a.ctl, s, pc);
         return ok;
@@ -124,12 +125,12 @@ __device__ __forceinline__ bool layer_phase(const MoeLayerArgs& a, const LayerLi
         with_tiles(x.count, [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             float acc[kLayTiles][NT][4];
-            mul.template unit<NT>(a.ctl, a.timeout_ns, pc, u, acc);
+            mul.template unit<NT, Job::kParts>(a.ctl, a.timeout_ns, pc, u, acc);
             finish_unit<UP, kLayTiles, NT>(s, 1 << job.shift, acc, [&](int tile, int r, int c, float v, float v2) {
                 const int row = x.row0 + tile * Job::kTile + (UP ? r / 16 * 8 + r % 8 : r);
                 if (row >= job.rows_all || c >= x.count || !mul.live) return;
                 const int asg = l.list[x.first + c];
-                if constexpr (UP) a.h[size_t(asg) * a.h_stride + row] = float_to_bf16_bits(silu_mul(v, v2));
+                if constexpr (UP) store_h(a, asg, row, silu_mul(v, v2));
                 else a.y[size_t(asg) * a.H + row] = v;
             });
             return true;
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_moe_layer(const __grid_cons
     if (threadIdx.x == 0) s_fail = status_failed(a.ctl);
     __syncthreads();
     if (s_fail) return;
-    const LayerLists l = layer_lists(a, s_raw + product_smem<kLayTiles>());
-    const ProductSmem s = product_layout<kLayTiles>(s_raw);
+    const LayerLists l = layer_lists(a, s_raw + product_smem<kLayTiles, kLayParts>());
+    const ProductSmem s = product_layout<kLayTiles, kLayParts>(s_raw);
     if (threadIdx.x == 0) init_panels(s);
     const int nact = sort_assignments<kProdThreads>(a, l, kLayTokens);
     if (nact < 0) return;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) k_moe_layer(const __grid_cons
 
 template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int num_sms, cudaStream_t s) {
     auto* kernel = k_moe_layer<WK, VEC>;
-    const size_t smem = product_smem<kLayTiles>() + layer_lists_bytes(a.E, a.A);
+    const size_t smem = product_smem<kLayTiles, kLayParts>() + layer_lists_bytes(a.E, a.A);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;
     int per_sm = 0;

@@ -149,6 +149,16 @@ __device__ __forceinline__ int sort_assignments(const MoeLayerArgs& a, const Lay
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
+// h of an assignment in two bf16 parts: its rounding, and what that left out (none of an infinity or NaN).
+constexpr int kLayParts = 2;
+__device__ __forceinline__ void store_h(const MoeLayerArgs& a, int asg, int row, float h) {
+    uint16_t* to = a.h + size_t(asg) * a.h_stride + row;
+    const uint16_t high = float_to_bf16_bits(h);
+    const float rest = h - bf16_bits_to_float(high);
+    to[0] = high;
+    to[a.h_part] = fabsf(rest) < INFINITY ? float_to_bf16_bits(rest) : uint16_t(0);
+}
+
 // Phase 3: the weighted sum, a thread per token and N columns. y was written by other CTAs before the barrier.
 template <int THREADS, int N> __device__ __forceinline__ void weighted_sum_of(const MoeLayerArgs& a) {
     const int tokens = a.A / a.k, pieces = a.H / N;

@@ -12,6 +12,7 @@
 //              token rows through the list of assignments, so nothing is gathered beforehand;
 //   warp 4     one thread issues the matrix instructions of a stage, whose completion frees the stage;
 //   warps 0-3  read a finished accumulator (two alternate) and write the results.
+// In phase 2 a stage holds both parts of the tokens' values, operands of two instructions into the same accumulator.
 // In phase 1 a group of 32 accumulator lanes holds 16 rows of G and the same 16 of U, so that silu(g) u needs one
 // exchange between lanes of a warp. A unit is M row tiles of 128: with two, the tokens' rows are staged
 // half as often. Bound by the weights' bytes while an expert has fewer than about 100 assignments. Measured on B200
@@ -37,6 +38,13 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+// One lane of the warp, in a form that tells the compiler so: the instructions' operands stay in uniform registers.
+// (By a test of the lane's number a stage took 0.1 us longer to issue.)
+__device__ __forceinline__ bool elected() {
+    uint32_t mine;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(mine));
+    return mine != 0u;
 }
 // Shared-memory descriptor of a K-major tile in the 128-byte swizzle: groups of 8 rows 1024 bytes apart.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t smem) {
@@ -97,9 +105,13 @@ template <bool UP> struct TcPhase {
         while (span > 16 && (rows + span - 17) / (span - 16) * tiles <= grid) span -= 16;
         blocks = (rows + span - 1) / span;
         weight_bytes = span * (UP ? 256 : 128);
-        slot_bytes = weight_bytes + min(kTcTokens / 16, (most + 15) / 16) * 2048;
+        slot_bytes = weight_bytes + token_rows(min(kTcTokens, most)) * 128;
         stages = min(kTcStages, (a.tensor_ring - (weight_bytes % kTcTileBytes ? kTcTileBytes : 0)) / slot_bytes);
     }
+    // Rows of a stage for so many assignments: those of one part (an instruction's columns: a multiple of 16), and all.
+    static constexpr int kParts = UP ? 1 : kLayParts;
+    __device__ __forceinline__ static int part_rows(int count) { return (count + 15) / 16 * 16; }
+    __device__ __forceinline__ static int token_rows(int count) { return kParts * part_rows(count); }
     __device__ __forceinline__ int units() const { return l.act_tile[nact] * blocks; }
     __device__ __forceinline__ int row_tiles() const { return (span + kTile - 1) / kTile; }
     struct At { int e, row0, first, count; };
@@ -134,7 +146,7 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<UP>& ph, uint32_t smem, Tc
     bool ok = true;
     for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
         const auto x = ph.at(u);
-        const int el = x.e % a.E_loc, rank = x.e / a.E_loc, nb = (x.count + 15) / 16;
+        const int el = x.e % a.E_loc, rank = x.e / a.E_loc, nb = ph.token_rows(x.count) / 16, part = ph.part_rows(x.count) / 16;
         const char* w[M][8];
 #pragma unroll
         for (int m = 0; m < M; ++m)
@@ -149,18 +161,19 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<UP>& ph, uint32_t smem, Tc
                 }
                 w[m][j] = (UP ? a.up[rank] : a.down[rank]) + (row * ph.K + c * 8) * 2;
             }
-        const char* b[8];
+        constexpr int kB = TcPhase<UP>::kParts * kTcTokens / 16;
+        const char* b[kB];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kB; ++j) {
             b[j] = nullptr;
-            const int n = min(j * 16 + r0, x.count - 1);
             if (j >= nb) continue;
-            const int asg = ph.l.list[x.first + n];
+            const bool low = j >= part;  // the second part; rows past the count: the last one
+            const int asg = ph.l.list[x.first + min((low ? j - part : j) * 16 + r0, x.count - 1)];
             if constexpr (UP) {
                 const int tok = asg / a.k;
                 b[j] = reinterpret_cast<const char*>(a.x[a.rank0 + tok / int(a.T)] + size_t(tok % int(a.T)) * a.H + c * 8);
             } else {
-                b[j] = reinterpret_cast<const char*>(a.h + size_t(asg) * a.h_stride + c * 8);
+                b[j] = reinterpret_cast<const char*>(a.h + size_t(asg) * a.h_stride + (low ? a.h_part : 0) + c * 8);
             }
         }
         // Every CTA begins at another k: rows are often a power of two apart, and CTAs that read the same columns of
@@ -183,8 +196,10 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<UP>& ph, uint32_t smem, Tc
                     if (m * ph.kTile + (UP ? j / 2 : j) * 16 < ph.span)
                         tc_copy16(to + m * kTcTileBytes + j * 2048, w[m][j] + at + back, bytes);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < nb) tc_copy16(to + ph.weight_bytes + j * 2048, b[j] + at + back, bytes);
+            for (int j = 0; j < kB; ++j) {
+                if (j >= nb) break;
+                tc_copy16(to + ph.weight_bytes + j * 2048, b[j] + at + back, bytes);
+            }
             // the barrier hears from this thread when its copies are in; many stages are in flight at a time
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full[slot])) : "memory");
             if (++slot == ph.stages) {
@@ -232,9 +247,9 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, T
     uint32_t parity = 0u;
     const int units = ph.units(), kbs = (ph.K + kTcK - 1) / kTcK, tiles = ph.row_tiles();
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++acc) {
-        const int nb = (ph.at(u).count + 15) / 16;
-        // fp32 accumulator, bf16 operands, both K-major, N = 16 nb, M = 128
-        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(nb * 2) << 17) | (8u << 24);
+        const int part = ph.part_rows(ph.at(u).count);
+        // fp32 accumulator, bf16 operands, both K-major, N = part, M = 128
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(part / 8) << 17) | (8u << 24);
         if (!mbar_wait_bounded(a.ctl, &bars.read[acc & 1], (acc / 2 & 1u) ^ 1u, a.timeout_ns)) return tc_quit(a.ctl, bars);
         tc_fence_after();
         const uint32_t d = tmem + (acc & 1) * (M * 128);
@@ -251,7 +266,11 @@ __device__ __forceinline__ bool tc_issue(const TcPhase<UP>& ph, uint32_t smem, T
             for (int kk = 0; kk < kTcK / 16; ++kk)  // 16 k's are 32 bytes further in the swizzled rows
 #pragma unroll
                 for (int m = 0; m < M; ++m)
-                    if (m < tiles) tc_mma(d + m * 128, tc_desc(at + m * kTcTileBytes) + kk * 2, db + kk * 2, idesc, uint32_t(kb | kk));
+                    if (m < tiles)
+#pragma unroll
+                        for (int q = 0; q < ph.kParts; ++q)  // the parts' rows are part * 128 bytes apart
+                            tc_mma(d + m * 128, tc_desc(at + m * kTcTileBytes) + kk * 2, db + q * part * 8 + kk * 2, idesc,
+                                   uint32_t(kb | kk | q));
             tc_commit(&empty[slot]);
             if (++slot == ph.stages) {
                 slot = 0;
@@ -289,8 +308,7 @@ __device__ __forceinline__ bool tc_finish(const TcPhase<UP>& ph, TcBars& bars, u
                         const float other = __shfl_xor_sync(0xffffffffu, v[i], 16);
                         const bool mine = (i & 1) == (lane >> 4);
                         if (mine && use && c0 + i < x.count)
-                            a.h[size_t(ph.l.list[x.first + c0 + i]) * a.h_stride + row] =
-                                float_to_bf16_bits(lane < 16 ? silu_mul(v[i], other) : silu_mul(other, v[i]));
+                            store_h(a, ph.l.list[x.first + c0 + i], row, lane < 16 ? silu_mul(v[i], other) : silu_mul(other, v[i]));
                     } else {
                         if (use && c0 + i < x.count)
                             a.y[size_t(ph.l.list[x.first + c0 + i]) * a.H + row] = v[i];
@@ -354,7 +372,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_moe_tensor(const __grid_const
         if (warp < kTcEpilogue) {
             ok = tc_finish(ph, bars, tmem, acc);
         } else if (warp == kTcEpilogue) {
-            if ((threadIdx.x & 31) == 0) ok = tc_issue(ph, smem, bars, tmem, acc);
+            if (elected()) ok = tc_issue(ph, smem, bars, tmem, acc);
             __syncwarp();
         } else {
             ok = tc_copy(ph, smem, bars);

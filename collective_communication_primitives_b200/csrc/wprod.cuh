@@ -19,7 +19,9 @@
 // copies a panel of k's of their rows ahead (one bulk copy per token, completing on an mbarrier), and the
 // eight others hand a panel back when they have used it. Rows of a panel are padded so that the lanes'
 // 16-byte reads spread over the banks (2-way for 32 consecutive k's per lane, free otherwise). Columns
-// without a token hold whatever the panel held before: a column's sums depend on that column alone.
+// without a token hold whatever the panel held before: a column's sums depend on that column alone. A token's values
+// may come in two bf16 parts (16 bits of them): the second ones have rows of their own behind the first ones', and
+// both go into the same sums.
 //
 // 4-bit weights: word bits 4i..4i+3 hold weight i of eight, value q - 8. (w & 0x000F000F) | 0x43004300
 // is the pair (128 + q_0, 128 + q_4) of bf16 values, and subtracting 136 is exact; shifts by 4 give
@@ -55,12 +57,12 @@ constexpr int kRing = 4;                            // stages of a warp's weight
 constexpr int kMaxNT = 4;
 template <int WK> constexpr int panel_pad() { return WK == W_Q4X4 ? 32 : WK == W_Q4X2 ? 16 : 64; }  // bytes per row
 template <int WK, int NT> constexpr int panel_pitch() { return kPanelK / NT * 2 + panel_pad<WK>(); }
-constexpr int kPanelBytes = 8 * kPanelK * 2 + 8 * kMaxNT * 64;
+template <int PARTS> constexpr int panel_bytes() { return PARTS * (8 * kPanelK * 2 + 8 * kMaxNT * 64); }
 constexpr int kSumTokens = 16;  // tokens whose sums are exchanged at a time where warps share a row tile
 template <int MT> constexpr int sums_bytes() { return kProdWarps * MT * 16 * kSumTokens * 4; }
-// Shared memory: panels, rings, exchanged sums, mbarriers.
-template <int MT> constexpr int product_smem() {
-    return kPanels * kPanelBytes + kProdWarps * kRing * MT * 1024 + sums_bytes<MT>() + 3 * kPanels * 8;
+// Shared memory: panels, rings, exchanged sums, mbarriers. PARTS: the most bf16 parts of a token value.
+template <int MT, int PARTS> constexpr int product_smem() {
+    return kPanels * panel_bytes<PARTS>() + kProdWarps * kRing * MT * 1024 + sums_bytes<MT>() + 3 * kPanels * 8;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -188,41 +190,47 @@ template <int BYTES> __device__ __forceinline__ void lds(uint32_t (&v)[4], const
 }
 
 // acc += one stage, whose tokens' k's start at `tok` of the panel (at this lane's token and first k).
-template <int WK, int MT, int NT>
+template <int WK, int MT, int NT, int PARTS>
 __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigned char* ring, const StageScales<WK, MT>& sc,
                                           const unsigned char* tok, int g, int t, const Q4Consts& qc) {
     using W = WTraits<WK>;
     constexpr int kPitch = panel_pitch<WK, NT>();
-    auto token8 = [&](int n, int u, int j) {  // run j of 8 k's of chunk u
-        const uint4 v = *reinterpret_cast<const uint4*>(tok + n * 8 * kPitch + u * W::kChunk * 2 + j * 16);
+    auto token8 = [&](int part, int n, int u, int j) {  // run j of 8 k's of chunk u
+        const uint4 v = *reinterpret_cast<const uint4*>(tok + (part * NT + n) * 8 * kPitch + u * W::kChunk * 2 + j * 16);
         return W::kQ4 && !panel_pairs<WK, NT>() ? paired(v) : v;
     };
     if constexpr (!W::kQ4) {
-        uint4 x[NT];
+        uint4 x[PARTS][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n] = token8(n, 0, 0);
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[q][n] = token8(q, n, 0, 0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             uint32_t a[2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) lds<16>(a[i], ring + ring_at(m, i, g, t));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma_bf16(acc[m][n], a[0][0], a[1][0], a[0][1], a[1][1], x[n].x, x[n].y);
-                mma_bf16(acc[m][n], a[0][2], a[1][2], a[0][3], a[1][3], x[n].z, x[n].w);
-            }
+            for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_bf16(acc[m][n], a[0][0], a[1][0], a[0][1], a[1][1], x[q][n].x, x[q][n].y);
+                    mma_bf16(acc[m][n], a[0][2], a[1][2], a[0][3], a[1][3], x[q][n].z, x[q][n].w);
+                }
         }
     } else {
         // a chunk's tokens are held for all row tiles, unless they are too many registers
-        constexpr bool kHold = W::kWords * NT <= 8;
+        constexpr bool kHold = W::kWords * NT * PARTS <= 8;
 #pragma unroll
         for (int u = 0; u < W::kChunks; ++u) {
-            uint4 x[kHold ? W::kWords : 1][NT];
+            uint4 x[kHold ? W::kWords : 1][PARTS][NT];
             if constexpr (kHold) {
 #pragma unroll
                 for (int j = 0; j < W::kWords; ++j)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) x[j][n] = token8(n, u, j);
+                    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) x[j][q][n] = token8(q, n, u, j);
             }
             const int byte = (4 * u + t) * W::kLaneBytes;  // of the row's 64
 #pragma unroll
@@ -235,18 +243,22 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
                 for (int j = 0; j < W::kWords; ++j) {
                     if constexpr (!kHold) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) x[0][n] = token8(n, u, j);
+                        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) x[0][q][n] = token8(q, n, u, j);
                     }
                     const uint32_t wa = w[0][j], wb = w[1][j];
                     const uint32_t a0 = q4_pair(wa, qc), a1 = q4_pair(wa >> 4, qc), a2 = q4_pair(wa >> 8, qc), a3 = q4_pair(wa >> 12, qc);
                     const uint32_t b0 = q4_pair(wb, qc), b1 = q4_pair(wb >> 4, qc), b2 = q4_pair(wb >> 8, qc), b3 = q4_pair(wb >> 12, qc);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint4 v = x[kHold ? j : 0][n];
-                        if (j == 0) mma_bf16_from0(d[n], a0, b0, a1, b1, v.x, v.y);
-                        else mma_bf16(d[n], a0, b0, a1, b1, v.x, v.y);
-                        mma_bf16(d[n], a2, b2, a3, b3, v.z, v.w);
-                    }
+                    for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint4 v = x[kHold ? j : 0][q][n];
+                            if (j == 0 && q == 0) mma_bf16_from0(d[n], a0, b0, a1, b1, v.x, v.y);
+                            else mma_bf16(d[n], a0, b0, a1, b1, v.x, v.y);
+                            mma_bf16(d[n], a2, b2, a3, b3, v.z, v.w);
+                        }
                 }
                 const int from = (threadIdx.x & 28) + 2 * (m % 2);  // the quad's lane that holds row (m, 0)
                 const float sa = bf16_bits_to_float(__shfl_sync(0xffffffffu, uint32_t(sc.v[m / 2][u]), from));
@@ -273,6 +285,7 @@ __device__ __forceinline__ void use_stage(float (&acc)[MT][NT][4], const unsigne
 //   void rows(unit, seg, tile, g, w)     the lane's weight rows of the CTA's tile-th row tile group
 //   void scales(unit, seg, tile, g, t, s)
 //   const uint16_t* token(unit, seg, n)  row of the n-th token, null for none
+//   ptrdiff_t part                       elements from a row to that of its values' second parts
 
 // Most warps that can share a row tile: every panel has a stage for each.
 template <int WK, int NT> constexpr int max_splits() {
@@ -281,15 +294,17 @@ template <int WK, int NT> constexpr int max_splits() {
 
 struct ProductSmem {
     unsigned char* base;
+    int panel;        // bytes of a buffer
     int rings, sums;  // bytes from base
     uint64_t* full;   // [kPanels]: the panel's tokens are in
     uint64_t* landed; // [kPanels]: they are in, but not yet in pairs (panel_pairs)
     uint64_t* empty;  // [kPanels]: every multiplying warp has used it
 };
-template <int MT> __device__ __forceinline__ ProductSmem product_layout(unsigned char* smem) {
+template <int MT, int PARTS> __device__ __forceinline__ ProductSmem product_layout(unsigned char* smem) {
     ProductSmem s;
     s.base = smem;
-    s.rings = kPanels * kPanelBytes;
+    s.panel = panel_bytes<PARTS>();
+    s.rings = kPanels * s.panel;
     s.sums = s.rings + kProdWarps * kRing * MT * 1024;
     s.full = reinterpret_cast<uint64_t*>(smem + s.sums + sums_bytes<MT>());
     s.empty = s.full + kPanels;
@@ -313,11 +328,11 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 constexpr uint64_t kLandNs = 1000000000ull;  // longest wait for copies in flight before a CTA may leave
 
 // The copying warp's side of a unit. False after a wait that ran out.
-template <int NT, typename Job>
+template <int NT, int PARTS, typename Job>
 __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint64_t timeout_ns, const ProductSmem& s,
                                             PanelCount& pc, int unit) {
     using W = WTraits<Job::kWK>;
-    constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kSpan = kPanelK / NT;
+    constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kSpan = kPanelK / NT, kPart = 8 * NT * kPitch;
     constexpr bool kPairs = panel_pairs<Job::kWK, NT>();
     const int lane = threadIdx.x & 31;
     for (int seg = 0; seg < job.segments; ++seg) {
@@ -327,20 +342,25 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
             const int buf = pc.buf(), n = min(kSpan, job.K - k0);
             const int padded = (n + W::kStageK - 1) / W::kStageK * W::kStageK;  // a stage is read whole
             if (!mbar_wait_warp(ctl, &s.empty[buf], pc.parity() ^ 1u, timeout_ns)) return false;
-            unsigned char* panel = s.base + buf * kPanelBytes;
+            unsigned char* panel = s.base + buf * s.panel;
             if constexpr (Job::kVecX) {
                 unsigned char* to = panel + lane * kPitch;
                 if (padded > n && row)  // zeros past the row's end
-                    for (int k = n; k < padded; k += 8) *reinterpret_cast<uint4*>(to + k * 2) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int q = 0; q < PARTS; ++q)
+                        for (int k = n; k < padded; k += 8)
+                            *reinterpret_cast<uint4*>(to + q * kPart + k * 2) = make_uint4(0u, 0u, 0u, 0u);
                 // This warp's ordinary writes to the buffer come before the copies that follow: zeros, those of the
                 // panel that it held before (of any length), and that panel's pairs (of a unit that makes them, which
                 // this one need not be).
                 fence_proxy_async_smem();
                 __syncwarp();
                 uint64_t* in = kPairs ? &s.landed[buf] : &s.full[buf];
-                if (lane == 0) mbar_arrive_expect_tx(in, rows * uint32_t(n) * 2u);
+                if (lane == 0) mbar_arrive_expect_tx(in, rows * uint32_t(n) * (2u * PARTS));
                 __syncwarp();
-                if (row) bulk_g2s(to, row + k0, uint32_t(n) * 2u, in);
+                if (row)
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q)
+                        bulk_g2s(to + q * kPart, row + q * job.part + k0, uint32_t(n) * 2u, in);
                 if constexpr (kPairs) {  // put into pairs where they lie
                     if (!mbar_wait_warp(ctl, in, pc.landed_parity(), timeout_ns)) {
                         mbar_wait_warp(ctl, in, pc.landed_parity(), kLandNs);
@@ -348,18 +368,21 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
                     }
                     pc.used_landed();
                     constexpr int kPieces = kSpan / 256, kRows = 8 / kPieces;  // of a lane and row; rows at a time
-                    for (uint32_t i = 0; i < rows; i += kRows) {
-                        uint4 v[kRows][kPieces];
+                    for (int part = 0; part < PARTS; ++part) {
+                        unsigned char* rows_of = panel + part * kPart;
+                        for (uint32_t i = 0; i < rows; i += kRows) {
+                            uint4 v[kRows][kPieces];
 #pragma unroll
-                        for (int h = 0; h < kRows; ++h)
+                            for (int h = 0; h < kRows; ++h)
 #pragma unroll
-                            for (int q = 0; q < kPieces; ++q)
-                                if (i + h < rows) v[h][q] = *reinterpret_cast<const uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16);
+                                for (int q = 0; q < kPieces; ++q)
+                                    if (i + h < rows) v[h][q] = *reinterpret_cast<const uint4*>(rows_of + (i + h) * kPitch + (q * 32 + lane) * 16);
 #pragma unroll
-                        for (int h = 0; h < kRows; ++h)
+                            for (int h = 0; h < kRows; ++h)
 #pragma unroll
-                            for (int q = 0; q < kPieces; ++q)
-                                if (i + h < rows) *reinterpret_cast<uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16) = paired(v[h][q]);
+                                for (int q = 0; q < kPieces; ++q)
+                                    if (i + h < rows) *reinterpret_cast<uint4*>(rows_of + (i + h) * kPitch + (q * 32 + lane) * 16) = paired(v[h][q]);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.full[buf]);
@@ -367,23 +390,24 @@ __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint
             } else {  // by loads and stores, the pieces of two rows in flight
                 constexpr int kPieces = kSpan / 256;  // of a lane and row
                 const uint64_t at = reinterpret_cast<uint64_t>(row);
-                for (uint32_t i = 0; i < rows; i += 2) {
-                    uint4 v[2][kPieces];
+                for (int part = 0; part < PARTS; ++part)
+                    for (uint32_t i = 0; i < rows; i += 2) {
+                        uint4 v[2][kPieces];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const auto* from = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, at, int(i) + h));
+                        for (int h = 0; h < 2; ++h) {
+                            const auto* from = reinterpret_cast<const uint16_t*>(__shfl_sync(0xffffffffu, at, int(i) + h));
 #pragma unroll
-                        for (int q = 0; q < kPieces; ++q)
-                            v[h][q] = ld_row8<Job::kVecX>(i + h < rows ? from : nullptr, k0 + (q * 32 + lane) * 8, job.K);
+                            for (int q = 0; q < kPieces; ++q)
+                                v[h][q] = ld_row8<Job::kVecX>(i + h < rows ? from + part * job.part : nullptr, k0 + (q * 32 + lane) * 8, job.K);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int q = 0; q < kPieces; ++q)
+                                if (i + h < rows && (q * 32 + lane) * 8 < padded)
+                                    *reinterpret_cast<uint4*>(panel + part * kPart + (i + h) * kPitch + (q * 32 + lane) * 16) =
+                                        kPairs ? paired(v[h][q]) : v[h][q];
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int q = 0; q < kPieces; ++q)
-                            if (i + h < rows && (q * 32 + lane) * 8 < padded)
-                                *reinterpret_cast<uint4*>(panel + (i + h) * kPitch + (q * 32 + lane) * 16) =
-                                    kPairs ? paired(v[h][q]) : v[h][q];
-                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.full[buf]);
             }
@@ -466,7 +490,7 @@ template <typename Job> struct Multiplier {
 
     // The warp's sums of a unit over its share of the stages (0 where the warp is not live). Every warp of the CTA goes
     // through all units, since warps that share a row tile meet at a barrier.
-    template <int NT>
+    template <int NT, int PARTS>
     __device__ __forceinline__ void unit(const Ctl& ctl, uint64_t timeout_ns, PanelCount& pc, int u, float (&acc)[MT][NT][4]) {
         constexpr int kPitch = panel_pitch<Job::kWK, NT>(), kPanelStages = kPanelK / NT / W::kStageK;
 #pragma unroll
@@ -492,14 +516,14 @@ template <typename Job> struct Multiplier {
                     live = false;
                     return;
                 }
-                const unsigned char* tok = s.base + buf * kPanelBytes + g * kPitch + t * W::kLaneK * 2;
+                const unsigned char* tok = s.base + buf * s.panel + g * kPitch + t * W::kLaneK * 2;
                 for (; st < end; st += splits) {
                     const StageScales<Job::kWK, MT> sc = next;
                     if constexpr (W::kQ4) load_scales<Job::kWK, MT>(next, sp, st + splits, groups, job.chunk_shift);
                     cp_async_wait<kRing - 2>();
                     __syncwarp();  // the stage is in for every lane, and the slot refilled next has been read
                     fetch();
-                    use_stage<Job::kWK, MT, NT>(acc, s.base + s.rings + (warp * kRing + slot) * (MT * 1024), sc,
+                    use_stage<Job::kWK, MT, NT, PARTS>(acc, s.base + s.rings + (warp * kRing + slot) * (MT * 1024), sc,
                                                 tok + (st - p0) * (W::kStageK * 2), g, t, qc);
                     slot = slot + 1 == kRing ? 0 : slot + 1;
                 }
