@@ -104,12 +104,14 @@ class RankComm(SC.SimComm):
         mapped here. Collective: every rank calls it with its own buffer."""
         return open_handles(exchange(buf.handle, self.group), self.rank, buf.ptr, self._open)
 
-    def sync(self):
-        """Stream synchronised, then a barrier of all ranks; a rank that does not arrive within the
-        process group's timeout raises COLL_ERR_TIMEOUT."""
+    def sync(self, stream=None):
+        """Stream (default: the current one) synchronised, then a barrier of all ranks; a rank that does
+        not arrive within the process group's timeout raises COLL_ERR_TIMEOUT."""
         import torch
         import torch.distributed as dist
-        torch.cuda.current_stream().synchronize()
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        (torch.cuda.current_stream() if stream is None else stream).synchronize()
         try:
             dist.barrier(group=self.group)
         except Exception as e:  # the group's timeout or a peer that left
@@ -189,6 +191,37 @@ class RankComm(SC.SimComm):
                 self._parr(self._outs(residual)) if residual is not None else None, tokens, topk, hidden,
                 int(experts), SC.DTYPES[dtype], self._parr(self._outs(out)), SC._stream(None)))
         self._call(go)
+
+    # The operators of a model's step take SimComm's arguments: tensors, lists in rank order. Of an array that the call
+    # reads from every rank this rank's entry is a tensor (over its registered buffer) and the others registered
+    # pointers; of an array that is this rank's own the other entries are None. The router and its gradient and the
+    # column-parallel linear read no peer's memory and meet no barrier.
+    def linear_w4(self, x, w, scale, out, parallel="row", stream=None):
+        """parallel "row": x, w and scale are every rank's (registered), out this rank's own."""
+        if parallel == "column":
+            super().linear_w4(x, w, scale, out, parallel=parallel, stream=stream)
+        else:
+            self._operator(super().linear_w4, x, w, scale, out, parallel=parallel, stream=stream)
+
+    def moe_layer(self, *args, stream=None, **kw):
+        """w_up, w_down and their scales are every rank's (registered), the other arrays this rank's own."""
+        self._operator(super().moe_layer, *args, stream=stream, **kw)
+
+    def logprobs(self, *args, stream=None, **kw):
+        """logits are every rank's (registered), the outputs this rank's own."""
+        self._operator(super().logprobs, *args, stream=stream, **kw)
+
+    def logprobs_backward(self, *args, stream=None, **kw):
+        """logits are every rank's (registered), the other arrays this rank's own."""
+        self._operator(super().logprobs_backward, *args, stream=stream, **kw)
+
+    def _operator(self, fn, *args, stream, **kw):
+        """_call on the caller's stream: complete on every rank before the call and after it."""
+        self.sync(stream)
+        try:
+            fn(*args, stream=stream, **kw)
+        finally:
+            self.sync(stream)
 
     def close(self):
         for ptr in getattr(self, "_opened", []):

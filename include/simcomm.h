@@ -144,7 +144,9 @@ sim_comm_t sim_comm_create(int p);
  * (counts_dev: this process's device copy of the whole count matrix, identical on every rank;
  * send_cap and recv_cap: every rank's capacities; only this rank's blocks are copied), Scatter,
  * Gather, COLL_ALGO_DIRECT only (the other schedules wait on other ranks inside their kernels:
- * COLL_ERR_UNSUPPORTED), and the MoE dispatch (fused kernel only) and combine (see there).
+ * COLL_ERR_UNSUPPORTED), the MoE dispatch (fused kernel only) and combine, the router, the 4-bit linear,
+ * the expert layer, the log probabilities and the gradients (see there; the expert layer's sums may be
+ * split otherwise than the whole communicator's, by the view's number of assignments).
  * Reduce and Gather enqueue nothing
  * on a non-root rank. No output may overlap any rank's input (a peer may still be reading it), except
  * the root's own in-place Broadcast and Scatter forms. The ranks' calls are not synchronised by the
