@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
     const char* row = static_cast<const char*>(a.logits[w.rank]) + size_t(w.live ? w.t : 0) * a.E * Elem<DT>::kBytes;
     const int e0 = w.sub * VPL, warp = threadIdx.x >> 5;
     float v[VPL];
-    if (!a.normalise) ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
+    ld_scores<DT, VPL>(v, row, e0, w.live ? a.E : 0, a.vec, -INFINITY);
     float* slots = reinterpret_cast<float*>(s_grad) + warp * 32 * VPL;  // scores of the group: [LPT * VPL]
     const int n = w.kTokens * a.k;
     uint32_t* ids_all = s_grad + kRouteThreads * VPL + warp * 3 * n;
@@ -332,7 +332,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
     const int k = w.live ? a.k : 0;
     float G[VPL];
     if (a.normalise) {
-        // only the picked scores matter: w[s] = term[s] / total, dx = sum of w (g - sum_q g w)
+        // only the picked scores matter: w[s] = term[s] / total, dx = sum of w (g - sum_q g w); but the forward pass's
+        // weights are NaN where any score of the row is
+        const float all = row_max<LPT, VPL>(v);
         float top = -INFINITY;
         for (int s = w.sub; s < k; s += LPT) top = fmaxf(top, xs[s]);
         top = group_max<LPT>(top);  // a NaN comes through by its own term
@@ -344,8 +346,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(const __grid_const
             total += term;
             dot = __fmaf_rn(gw[s], term, dot);
         }
-        total = group_sum<LPT>(total);
+        total = group_sum<LPT>(total);  // by all lanes, before rows part company
         dot = group_sum<LPT>(dot);
+        if (all != all) total = all;
         const float inv = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * inv;
         __syncwarp();
         add_picks<LPT>(w, mine, ids, k, a.k, [&](int s) { return xs[s] * inv * (gw[s] - mean); });
@@ -458,7 +461,7 @@ template <int DT> __global__ void __launch_bounds__(kRouteThreads) k_route_wide(
         total += term;
         dot = __fmaf_rn(gw[s], term, dot);
     }
-    if (!a.normalise) total = sum;
+    total = a.normalise ? total + 0.0f * sum : sum;  // a NaN anywhere in the row reaches every pick
     const float inv = total == 0.0f ? 0.0f : 1.0f / total, mean = dot * inv;
     for (int e = lane; e < a.E; e += 32) {
         float g = 0.0f;

@@ -427,7 +427,8 @@ coll_status_t coll_moe_route(sim_comm_t comm, const void* const* logits, size_t 
  *   normalise:  grad_logits[e] = sum over s with idx[s] = e of w[s] (g[s] - sum_q g[q] w[q])
  *   otherwise:  grad_logits[e] = P[e] (sum over s with idx[s] = e of g[s] - sum_q g[q] w[q])
  * for every e (0 where the sum is empty). P and w are computed again from logits (unchanged since the
- * forward call); an id that occurs twice in a row counts twice.
+ * forward call); an id that occurs twice in a row counts twice. A score that is NaN makes its row's gradient
+ * NaN as it makes the weights, at the picked experts when `normalise` is not 0 (the others' is 0), else everywhere.
  *   grad_weight  HOST array of p DEVICE pointers, [T][k] fp32.
  *   grad_logits  HOST array of p DEVICE pointers, output [T][E] of the scores' type.
  * Other arguments and refusals as for coll_moe_route. An id outside [0, E) is reported asynchronously as
