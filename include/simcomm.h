@@ -526,8 +526,9 @@ coll_status_t coll_logprobs(sim_comm_t comm, const void* const* logits, size_t l
  *   grad_logprob DEVICE fp32 [rows]; grad_entropy DEVICE fp32 [rows] or NULL.
  *   grad_logits  HOST array of p DEVICE pointers, output [rows][ld_grad] of the scores' type, ld_grad >= m;
  *                columns past m are left untouched. Never in place: no output may overlap another buffer.
- * On a rank view every rank's logits are given (a row whose lse passes 1e5 in magnitude is summed again,
- * over all of them), the rest is this rank's. */
+ * P's relative error is 2^-24 |lse| from the rounding of lse, at most 2^-18 (fp32 scores) or 2^-14 (bf16): a row
+ * whose lse passes 128 or 2048 in magnitude is summed again. On a rank view every rank's logits are given, for
+ * such rows, the rest is this rank's. */
 coll_status_t coll_logprobs_backward(sim_comm_t comm, const void* const* logits, size_t ld, const int32_t* tokens,
                                      size_t rows, size_t vocab, coll_dtype_t dtype, const float* const* lse,
                                      const float* const* entropy, const float* grad_logprob, const float* grad_entropy,
