@@ -99,7 +99,9 @@ template <bool UP> struct TcPhase {
         // With more units than CTAs whole tiles are best, ragged rounds and all: the CTAs of a last, partial round
         // have the memory to themselves. (Measured on 14 picked experts of 4096 x 2048: 142 us with whole tiles in
         // 1.5 rounds, 147 with spans that make two even rounds, 162 and 169 with three and four.)
-        // Results do not depend on the span.
+        // Results do not depend on the span: every unit sums over k from its beginning. (Units that began at different
+        // k's, so as not to read the same columns of their rows at the same time, were 1 to 3% faster, but the order of
+        // a row's sum then went by which other experts were picked.)
         const int tiles = l.act_tile[nact], grid = int(gridDim.x);
         span = kTile * M;
         while (span > 16 && (rows + span - 17) / (span - 16) * tiles <= grid) span -= 16;
@@ -176,17 +178,13 @@ __device__ __forceinline__ bool tc_copy(const TcPhase<UP>& ph, uint32_t smem, Tc
                 b[j] = reinterpret_cast<const char*>(a.h + size_t(asg) * a.h_stride + (low ? a.h_part : 0) + c * 8);
             }
         }
-        // Every CTA begins at another k: rows are often a power of two apart, and CTAs that read the same columns of
-        // their rows at the same time would keep asking the same part of the memory.
-        const int turn = u * 5 % kbs;
         for (int kb = 0; kb < kbs; ++kb) {
             if (!mbar_wait_bounded(a.ctl, &empty[slot], parity, a.timeout_ns)) {
                 ok = false;
                 break;
             }
-            const int k = turn + kb < kbs ? turn + kb : turn + kb - kbs;
-            const bool in = k * kTcK + c * 8 < ph.K;
-            const size_t at = in ? size_t(k) * (kTcK * 2) : 0;
+            const bool in = kb * kTcK + c * 8 < ph.K;
+            const size_t at = in ? size_t(kb) * (kTcK * 2) : 0;
             const ptrdiff_t back = in ? 0 : -ptrdiff_t(c) * 16;  // past the end nothing is read; stay in the row
             const uint32_t to = smem + slot * ph.slot_bytes + off, bytes = in ? 16u : 0u;
 #pragma unroll
@@ -221,10 +219,9 @@ template <bool UP> __device__ __forceinline__ void tc_prefetch(const TcPhase<UP>
     const char* w = (UP ? a.up[x.e / a.E_loc] : a.down[x.e / a.E_loc]) +
                     (size_t(x.e % a.E_loc) * (UP ? 2 * a.F : a.H) + x.row0) * ph.K * 2;
     const size_t row_bytes = size_t(ph.K) * 2;
-    const int turn = blockIdx.x * 5 % ((ph.K + kTcK - 1) / kTcK);
     const int n = min(ph.span, ph.rows - x.row0);
     for (int i = threadIdx.x - (kTcEpilogue + 1) * 32; i < n * kLines; i += kTcCopy * 32) {
-        const size_t at = size_t(turn + i % kLines) * 128;
+        const size_t at = size_t(i % kLines) * 128;
         if (at < row_bytes) asm volatile("prefetch.global.L2 [%0];" :: "l"(w + i / kLines * row_bytes + at));
     }
 }

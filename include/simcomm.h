@@ -481,7 +481,8 @@ coll_status_t coll_linear_w4(sim_comm_t comm, const void* const* x, const void* 
  *   weight, group  COLL_WEIGHT_BF16 (group ignored) or COLL_WEIGHT_INT4 (group divides H and F).
  *   dtype    of x, residual and out: COLL_BF16 (others: COLL_ERR_UNSUPPORTED).
  * Products are summed in fp32; silu(g) u goes into the second product in two bf16 parts (2^-16 of it is
- * lost); the weighted sum runs in slot order in fp32 like the combine's, rounded once. p * T * k (a rank view:
+ * lost); the weighted sum runs in slot order in fp32 like the combine's, rounded once. In calls of one shape a
+ * token's result does not depend on the other tokens. p * T * k (a rank view:
  * T * k) may be at most 4096, else COLL_ERR_UNSUPPORTED: larger batches go through the dispatch. An expert
  * id outside [0, E) is reported asynchronously as COLL_ERR_INVALID_ARG and nothing is written. Rows of
  * whole 16-byte units at 16-byte aligned addresses take 16-byte loads, others element-wise ones. Needs a
