@@ -6,6 +6,7 @@ fallback: without the built library (``python -m collective_communication_primit
 creating a communicator raises.
 """
 import ctypes
+import math
 import os
 import struct
 
@@ -134,12 +135,16 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_NAMES = {}  # torch's types, once torch is there
+
+
 def _dtype_of(t):
-    import torch
-    m = {torch.int32: "int32", torch.float32: "fp32", torch.bfloat16: "bf16"}
-    if t.dtype not in m:
+    if not _NAMES:
+        import torch
+        _NAMES.update({torch.int32: "int32", torch.float32: "fp32", torch.bfloat16: "bf16"})
+    if t.dtype not in _NAMES:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return _NAMES[t.dtype]
 
 
 def _stream(stream):
@@ -336,23 +341,29 @@ class SimComm:
 
 
     # -- router, products with sharded weights, log probabilities ------------------------------------
-    def _tensors(self, what, tensors, dtype, numel, row=None, one=False):
+    def _tensors(self, what, tensors, dtype, shape, row=None, one=False):
         """HOST array of the ranks' device pointers (its bytes), after checking that every tensor is where and what
-        the kernels take it for: on the communicator's device, of `dtype` (a torch dtype), `numel`
-        elements, contiguous (or, with `row` = (ld, columns), rows at that distance). A rank view's
-        entries of other ranks may be None or addresses. `one`: a single tensor, its address."""
+        the kernels take it for: on the communicator's device, of `dtype` (a torch dtype) and `shape`, or flat
+        with as many elements (a whole number: so many of any shape), contiguous (or, with `row` = (ld,
+        columns), rows at that distance). A rank view's entries of other ranks may be None or addresses.
+        `one`: a single tensor, its address."""
         if tensors is None:
             return None
         dev = self._device
+        vector = isinstance(shape, int)
         if not one:
             try:  # the usual call in one sweep; anything else takes the slow way, which says what is wrong
-                out = [t.data_ptr() for t in tensors
-                       if t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous()]
+                if vector:
+                    out = [t.data_ptr() for t in tensors
+                           if t.dtype is dtype and t.get_device() == dev and t.numel() == shape and t.is_contiguous()]
+                else:
+                    out = [t.data_ptr() for t in tensors
+                           if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()]
             except AttributeError:
                 out = ()
             if len(out) == self.p == len(tensors) and (row is None or row[0] == row[1]):
                 return self._pack(*out)
-        out = []
+        out, numel = [], shape if vector else math.prod(shape)
         for t in ((tensors,) if one else tensors):
             if t is None or isinstance(t, int):
                 if self.rank is None:
@@ -363,11 +374,13 @@ class SimComm:
                 raise TypeError(f"{what}: {t.dtype}, not {dtype}")
             if t.get_device() != dev:
                 raise ValueError(f"{what}: on {t.device}, not on the communicator's device")
+            if t.numel() != numel or not (vector or t.shape == shape or t.dim() == 1 and row is None):
+                raise ValueError(f"{what}: shape {tuple(t.shape)}, {shape} is wanted")
             if row is not None and t.shape[0] > 1:
-                if t.numel() != numel or t.stride(1) != 1 or t.stride(0) != row[0]:
-                    raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()} do not fit the call")
-            elif t.numel() != numel or not t.is_contiguous():
-                raise ValueError(f"{what}: {t.numel()} elements ({numel} are wanted), or not contiguous")
+                if t.stride(1) != 1 or t.stride(0) != row[0]:
+                    raise ValueError(f"{what}: strides {t.stride()} do not fit the call")
+            elif not t.is_contiguous():
+                raise ValueError(f"{what}: not contiguous")
             out.append(t.data_ptr())
         if one:
             return out[0]
@@ -394,9 +407,9 @@ class SimComm:
         T, E = x.shape
         k = self._own(topk_idx).shape[1]
         self._check(self._L.coll_moe_route(
-            self._h, self._tensors("logits", logits, x.dtype, T * E), T, k, E, DTYPES[_dtype_of(x)], 1 if normalise else 0,
-            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
-            self._tensors("topk_weight", topk_weight, torch.float32, T * k), self._launch_stream(stream)))
+            self._h, self._tensors("logits", logits, x.dtype, (T, E)), T, k, E, DTYPES[_dtype_of(x)], 1 if normalise else 0,
+            self._tensors("topk_idx", topk_idx, torch.int32, (T, k)),
+            self._tensors("topk_weight", topk_weight, torch.float32, (T, k)), self._launch_stream(stream)))
 
     def moe_route_backward(self, logits, topk_idx, grad_weight, grad_logits, normalise=True, stream=None):
         """Gradient of moe_route's scores into grad_logits[i] [T][E] (of the scores' type), from grad_weight[i]
@@ -406,10 +419,10 @@ class SimComm:
         T, E = x.shape
         k = self._own(topk_idx).shape[1]
         self._check(self._L.coll_moe_route_backward(
-            self._h, self._tensors("logits", logits, x.dtype, T * E),
-            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
-            self._tensors("grad_weight", grad_weight, torch.float32, T * k), T, k, E, DTYPES[_dtype_of(x)],
-            1 if normalise else 0, self._tensors("grad_logits", grad_logits, x.dtype, T * E), self._launch_stream(stream)))
+            self._h, self._tensors("logits", logits, x.dtype, (T, E)),
+            self._tensors("topk_idx", topk_idx, torch.int32, (T, k)),
+            self._tensors("grad_weight", grad_weight, torch.float32, (T, k)), T, k, E, DTYPES[_dtype_of(x)],
+            1 if normalise else 0, self._tensors("grad_logits", grad_logits, x.dtype, (T, E)), self._launch_stream(stream)))
 
     def linear_w4(self, x, w, scale, out, parallel="row", stream=None):
         """out = x W^T for few tokens, W of 4-bit weights (q - 8) * scale: w[r] uint8 [N_r][K_r/2] (element 2i in
@@ -427,10 +440,10 @@ class SimComm:
             raise ValueError(f"scale: {groups} groups do not divide rows of {K}")
         row = parallel == "row"
         self._check(self._L.coll_linear_w4(
-            self._h, self._tensors("x", x, torch.bfloat16, T * K), self._tensors("w", w, torch.uint8, N * (K // 2)),
-            self._tensors("scale", scale, torch.bfloat16, N * groups), T, N if row else N * self.p,
+            self._h, self._tensors("x", x, torch.bfloat16, (T, K)), self._tensors("w", w, torch.uint8, (N, K // 2)),
+            self._tensors("scale", scale, torch.bfloat16, (N, groups)), T, N if row else N * self.p,
             K * self.p if row else K, K // groups, PARALLEL[parallel], DTYPES[_dtype_of(o)],
-            self._tensors("out", out, o.dtype, T * N), self._launch_stream(stream)))
+            self._tensors("out", out, o.dtype, (T, N)), self._launch_stream(stream)))
 
     def moe_layer(self, x, topk_idx, topk_weight, experts, w_up, w_down, out, up_scale=None, down_scale=None,
                   residual=None, stream=None):
@@ -446,21 +459,21 @@ class SimComm:
         q4 = up_scale is not None
         if q4 != (down_scale is not None) or rows != 2 * F or el * self.p != experts:
             raise ValueError("w_up must be [experts / p][2 F][...], and both scales or none be given")
-        group, wt, n, su, sd = 0, torch.bfloat16, el * F * H, None, None
+        group, wt, per, su, sd = 0, torch.bfloat16, 1, None, None
         if q4:
             groups = self._own(up_scale).shape[2]
             if groups < 1 or H % groups or F % (H // groups):
                 raise ValueError(f"up_scale: {groups} groups do not fit rows of {H} and {F}")
-            group, wt, n = H // groups, torch.uint8, el * F * (H // 2)
-            su = self._tensors("up_scale", up_scale, torch.bfloat16, el * rows * groups)
-            sd = self._tensors("down_scale", down_scale, torch.bfloat16, el * H * (F // group))
+            group, wt, per = H // groups, torch.uint8, 2  # weights to an element
+            su = self._tensors("up_scale", up_scale, torch.bfloat16, (el, rows, groups))
+            sd = self._tensors("down_scale", down_scale, torch.bfloat16, (el, H, F // group))
         self._check(self._L.coll_moe_layer(
-            self._h, self._tensors("x", x, torch.bfloat16, T * H),
-            self._tensors("topk_idx", topk_idx, torch.int32, T * k),
-            self._tensors("topk_weight", topk_weight, torch.float32, T * k),
-            self._tensors("residual", residual, torch.bfloat16, T * H), T, k, H, F, int(experts), 1 if q4 else 0, group,
-            self._tensors("w_up", w_up, wt, 2 * n), su, self._tensors("w_down", w_down, wt, n), sd, DTYPES["bf16"],
-            self._tensors("out", out, torch.bfloat16, T * H), self._launch_stream(stream)))
+            self._h, self._tensors("x", x, torch.bfloat16, (T, H)),
+            self._tensors("topk_idx", topk_idx, torch.int32, (T, k)),
+            self._tensors("topk_weight", topk_weight, torch.float32, (T, k)),
+            self._tensors("residual", residual, torch.bfloat16, (T, H)), T, k, H, F, int(experts), 1 if q4 else 0, group,
+            self._tensors("w_up", w_up, wt, (el, rows, H // per)), su, self._tensors("w_down", w_down, wt, (el, H, F // per)), sd, DTYPES["bf16"],
+            self._tensors("out", out, torch.bfloat16, (T, H)), self._launch_stream(stream)))
 
     def logprobs(self, logits, tokens, vocab, logprob, entropy=None, lse=None, top_idx=None, top_logprob=None,
                  stream=None):
@@ -479,11 +492,11 @@ class SimComm:
         if (top_idx is None) != (top_logprob is None):
             raise ValueError("top_idx and top_logprob go together")
         self._check(self._L.coll_logprobs(
-            self._h, self._tensors("logits", logits, x.dtype, R * m, row=(ld, m)), ld,
+            self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld,
             self._tensors("tokens", tokens, torch.int32, R, one=True), R, int(vocab), DTYPES[_dtype_of(x)],
             self._tensors("logprob", logprob, f, R), self._tensors("entropy", entropy, f, R),
-            self._tensors("lse", lse, f, R), n, self._tensors("top_idx", top_idx, torch.int32, R * n),
-            self._tensors("top_logprob", top_logprob, f, R * n), self._launch_stream(stream)))
+            self._tensors("lse", lse, f, R), n, self._tensors("top_idx", top_idx, torch.int32, (R, n)),
+            self._tensors("top_logprob", top_logprob, f, (R, n)), self._launch_stream(stream)))
 
     def logprobs_backward(self, logits, tokens, vocab, lse, grad_logprob, grad_logits, entropy=None,
                           grad_entropy=None, stream=None):
@@ -500,12 +513,12 @@ class SimComm:
         if grad_entropy is not None and entropy is None:
             raise ValueError("grad_entropy needs entropy")
         self._check(self._L.coll_logprobs_backward(
-            self._h, self._tensors("logits", logits, x.dtype, R * m, row=(ld, m)), ld,
+            self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld,
             self._tensors("tokens", tokens, torch.int32, R, one=True), R, int(vocab), DTYPES[_dtype_of(x)],
             self._tensors("lse", lse, f, R), self._tensors("entropy", entropy, f, R),
             self._tensors("grad_logprob", grad_logprob, f, R, one=True),
             None if grad_entropy is None else self._tensors("grad_entropy", grad_entropy, f, R, one=True),
-            self._tensors("grad_logits", grad_logits, x.dtype, R * m, row=(ldg, m)), ldg, self._launch_stream(stream)))
+            self._tensors("grad_logits", grad_logits, x.dtype, (R, m), row=(ldg, m)), ldg, self._launch_stream(stream)))
 
 
 def allreduce_ring_noalloc(sends, recvs, op="sum", n=None, dtype=None, status=None, stream=None):
