@@ -198,16 +198,17 @@ template <int WK, bool VEC> static cudaError_t launch_layer(MoeLayerArgs& a, int
 
 // The kernel on the fifth-generation tensor cores needs bf16 weights and rows of 16-byte units. By itself it is
 // taken where an expert gets 24 assignments or more, which the streamed products read the weights again for (32 to a
-// unit) and multiply at the older instructions' rate, and where units of 128 rows fill one and a half rounds of the SMs
-// in both products: its stages of 64 k's go by at 0.4 us at best, so that few units are slow. Measured on B200, us
-// streamed and tensor, by picked experts of H x F and assignments each: 8 of 1024 x 1024 with 16 29 and 37, with 32 45
-// and 39; 16 of 1000 x 712 with 33 62 and 43; 8 of 4096 x 2048 with 16 93 and 94, with 32 155 and 104; with one
-// assignment each, 2 of 4096 x 2048 31 and 62, 16 of them 150 and 145, 8 of 4096 x 14336 480 and 447, 4 of them
-// 222 and 254; 64 of 1024 x 1024 with 2 84 and 88.
+// unit) and multiply at the older instructions' rate; from 12 on where units of 128 rows fill half a round of the SMs in
+// both products; and with fewer where they fill one and a half: few units are slow, for their stages of 64 k's wait for
+// one another. Measured on B200, us streamed and tensor, by picked experts of H x F and assignments each: 8 of 1024 x
+// 1024 with 16 34 and 35, with 24 38 and 39, with 32 56 and 39; 16 of 1000 x 712 with 8 37 and 35, with 12 45 and 38,
+// with 32 62 and 47; 8 of 4096 x 2048 with 8 92 and 90, with 12 116 and 98, with 32 191 and 110; 8 of 1024 x 512 with 16
+// 27 and 31, 4 of 2048 x 4096 with 16 77 and 80; with one assignment each, 2 of 4096 x 2048 21 and 54, 14 of them 152
+// and 144, 8 of 4096 x 14336 492 and 446, 4 of them 222 and 233; 64 of 1024 x 1024 with 2 87 and 87.
 static bool layer_takes_tensor(const MoeLayerArgs& a, int num_sms) {
     if (a.tensor == 0 || a.weight_kind != COLL_WEIGHT_BF16 || !a.vec || !layer_tensor_fits(a)) return false;
-    const int experts = std::min(a.E, a.A);
-    return a.tensor == 1 || a.A >= 24 * experts || experts * ((std::min(a.H, a.F) + 127) / 128) * 2 >= num_sms * 3;
+    const int experts = std::min(a.E, a.A), units = experts * ((std::min(a.H, a.F) + 127) / 128);
+    return a.tensor == 1 || a.A >= 24 * experts || (a.A >= 12 * experts && units * 2 >= num_sms) || units * 2 >= num_sms * 3;
 }
 
 cudaError_t launch_moe_layer(const MoeLayerArgs& args, int num_sms, cudaStream_t s) {
