@@ -8,8 +8,9 @@
 // In the row-parallel form the exchange costs nothing of its own: the sum over ranks is part of the sum
 // over k, whose range one CTA's warps split between them, and the epilogue stores the finished value to
 // every rank's output. The warp-level product and what bounds it are in wprod.cuh. Measured on B200: 4096 x 4096, one
-// token, row parallel over 8 ranks 12.5 us (the bytes take 1.4 at the copy rate: a latency); 65536 x 4096, one token
-// 45 us (21.5); 131072 x 4096, 16 tokens 117 us, 2.5 TB/s (46).
+// token, row parallel over 8 ranks 13.5 us (the bytes take 1.4 at the copy rate: every rank's tokens are a panel of their
+// own, half empty, and go through two buffers one after the other); 65536 x 4096, one token 47 us (21.6); 131072 x 4096,
+// 16 tokens 117 us, 2.5 TB/s (45); 16384 x 4096, 512 tokens 316 us (13.2: the weights are taken apart for every 32).
 #include <algorithm>
 #include <type_traits>
 

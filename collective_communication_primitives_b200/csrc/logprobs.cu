@@ -10,7 +10,7 @@
 // vector of scores brings a larger one; threads, then parts of a row, are joined in a fixed order. Both
 // terms of the entropy's form above are non-negative, so nothing cancels. Few rows are cut into parts, one
 // CTA each; the last part to finish joins them all. Bound by the scores' bytes, then, for 2-byte scores,
-// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 47 us, 4.3 TB/s; 2048 x 131072 bf16 106 us,
+// by the one exponential per score. Measured on B200: 1023 x 50257 fp32 48 us, 4.3 TB/s; 2048 x 131072 bf16 105 us,
 // 5.1 TB/s, with 4 alternatives 137 us (five CTAs on an SM; with four 8% and 9% more); 8 x 131072 fp32 with 8 alternatives 14.4 us.
 //
 // Alternatives are 64-bit keys: the score's order, then the complement of the column, so that the lower
@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kLpThreads, 5) k_logprobs(const __grid_constan
 
 // With d = x log2e - B, B = (m + ln_s) log2e rounded: P = 2^d c, c = 2^-(what the rounding of B left out), and
 // ln P = d ln 2 + ln c. So dx = -P (gl + ge (ln P + H)) = 2^d (a0 + a1 d), two constants of the row. Bound by memory:
-// 1023 x 50257 fp32 79 us, 5.2 TB/s, 2048 x 131072 bf16 202 us, 5.3 TB/s on B200 (with three CTAs on an SM instead of
-// four 78 and 221, with five, which spill, 84 and 214).
+// 1023 x 50257 fp32 80 us, 5.1 TB/s, 2048 x 131072 bf16 207 us, 5.2 TB/s on B200 (when it was
+// 79 and 202 with four CTAs on an SM, it was 78 and 221 with three, 84 and 214 with five, which spill).
 struct RowGrad {
     float base, a0, a1;
 };

@@ -15,9 +15,10 @@
 //   2  per (picked expert, 16 rows of D, up to 32 assignments): y = D h, fp32;
 //   3  per (token, columns): the weighted sum over slots in slot order and the residual, each product and
 //      sum rounded to fp32 as in the combine, rounded once.
-// The warp-level product and what bounds it are in wprod.cuh. Measured on B200, 4-bit weights of 4096 x 2048: 16 picked
-// experts 76 us, 64 of them with 256 assignments 258 us, 3.1 TB/s (the bytes take 127 at the copy rate); bf16 in
-// moe_tensor.cu and at the rule below.
+// The warp-level product and what bounds it are in wprod.cuh. Measured on B200, 4-bit weights of 4096 x 2048: 14 picked
+// experts with one assignment each 82 us (the bytes take 29 at the copy rate), 64 of them with 256 assignments 275 us,
+// 3.0 TB/s (127); with h in one part 76 and 262. bf16 in moe_tensor.cu and at the rule below; rows that are not whole
+// 16-byte units are loaded by element: 16 experts of 1001 x 713 with 33 each 256 us, 45 for 1000 x 712.
 #include <algorithm>
 #include <type_traits>
 

@@ -16,8 +16,10 @@
 // In phase 1 a group of 32 accumulator lanes holds 16 rows of G and the same 16 of U, so that silu(g) u needs one
 // exchange between lanes of a warp. A unit is M row tiles of 128: with two, the tokens' rows are staged
 // half as often. Bound by the weights' bytes while an expert has fewer than about 100 assignments. Measured on B200
-// with experts of 4096 x 2048: 64 of them with 64 assignments each 572 us, 5.7 TB/s, 0.88 of the copy rate; 16 with
-// one each 145 us, 5.0 TB/s (the two products' ends weigh more).
+// with experts of 4096 x 2048: 64 of them with 64 assignments each 607 us, 5.3 TB/s, 0.83 of the copy rate (with h in
+// one part 572); 14 with one each 143 us, 5.0 TB/s (the two products' ends weigh more). Of 50 us for 16 of 1000 x 712 with
+// 33 each, caches cold, the order takes 3.5, the first product 24, the first barrier 4 to 6, the second product with
+// its barrier 16, the sum 2.6.
 #include <algorithm>
 
 #include "moe_layer.cuh"

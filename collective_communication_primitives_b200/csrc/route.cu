@@ -12,11 +12,12 @@
 // order-preserving integers, which each lane sorts (a network: 19 exchanges of 8). A round of "largest that is
 // left" is then the group's maximum over the lanes' first ones, and one lane that moves up. bf16 scores leave
 // room for the id in the integer; for fp32 the ids of all picks are looked up at the end, side by side. The
-// sum over the whole row is formed only where the weights are shares of it. What bounds it is integer
-// instructions, then the launch. Rows of more than 1024 experts are read again for every round, a warp per token
+// sum over the whole row is formed only where the weights are shares of it. What bounds it with many tokens is
+// instructions, integer ones before all (issue slots 85 to 93% busy, the integer pipe 62 to 75%, 6 to 7 warps ready on
+// a scheduler); with few the launch; the gradient waits for its loads (61% and 48%). Rows of more than 1024 experts are read again for every round, a warp per token
 // (from cache; a row is at most 16 KiB). Measured on B200, kernels alone: 8 ranks x 8192 tokens x 64 experts bf16,
-// k = 2, 10.4 us (the bytes take 1.5 at the copy rate); 4 x 4099 x 256 fp32, k = 8, with the gradient 26.7 us (8.1);
-// one token 4.3 us.
+// k = 2, 10.3 us (the bytes take 1.5 at the copy rate), the gradient 14.4; 4 x 4099 x 256 fp32, k = 8, 15.7 us and
+// 14.3 (8.1 in all); one token 4.1 us; 4096 x 2048 fp32, k = 8, 69 us, the gradient 35 to 37.
 // Scores that are NaN are picked last and make the row's weights NaN; a row of nothing but -inf has
 // weight 0 for every pick.
 #include <algorithm>

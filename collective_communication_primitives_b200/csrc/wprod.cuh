@@ -4,9 +4,11 @@
 //   D[r][n] = sum_k W[r][k] X[n][k],   16 MT weight rows x 8 NT tokens per warp
 //
 // Every weight is used once per token, so the job is to keep enough loads in flight and to spend few instructions
-// per byte. bf16 weights run at 3 to 5 TB/s on B200. 4-bit weights are bound by instructions, at 2.5 to 3.2 TB/s: 21 (to
-// 8 tokens) or 27 (16) for 256 weights, 11 of them to take them apart, with the integer pipe 43 to 48% busy whether 8
-// or 16 warps share it. Weights are the 16-row
+// per byte. bf16 weights run at 3 to 5 TB/s on B200, 4-bit weights at 2.5 to 3.1. Those spend 21 (to 8 tokens) or 27 (16)
+// instructions on 256 weights, 11 of them to take them apart, but no pipe is full: issue slots are 38 to 49% busy, the
+// integer pipe 35 to 48%, the tensor pipe 17 to 29%, with 0.5 to 0.7 warps ready on a scheduler. The warps wait, for
+// the results in the chain from a loaded word over its weights and their product to the scaled sum more than for
+// memory; twice as many warps wait for each other instead (all measured). Weights are the 16-row
 // operand of the matrix instruction (mma.sync m16n8k16) and tokens its 8 columns, so that one token
 // wastes no more than 7 columns. A sum over k may be taken in any order as long as both operands use
 // the same one, so no weight is ever moved between lanes for the instruction's sake: lane (g, t)
@@ -23,7 +25,8 @@
 // may come in two bf16 parts (16 bits of them): the second ones have rows of their own behind the first ones', and
 // both go into the same sums.
 //
-// 4-bit weights: word bits 4i..4i+3 hold weight i of eight, value q - 8. (w & 0x000F000F) | 0x43004300
+// 4-bit weights (whole numbers set into a float's last bits, as published by Kim, Henry, Fahim and Awadalla, "Who says
+// elephants can't run", 2022): word bits 4i..4i+3 hold weight i of eight, value q - 8. (w & 0x000F000F) | 0x43004300
 // is the pair (128 + q_0, 128 + q_4) of bf16 values, and subtracting 136 is exact; shifts by 4 give
 // the pairs (1,5), (2,6), (3,7); the tokens' words are paired the same way. A chunk's sum is taken
 // over the whole numbers q - 8 (bf16 holds them, the products are exact in fp32) and scaled once per
