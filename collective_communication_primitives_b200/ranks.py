@@ -203,17 +203,23 @@ class RankComm(SC.SimComm):
         else:
             self._operator(super().linear_w4, x, w, scale, out, parallel=parallel, stream=stream)
 
-    def moe_layer(self, *args, stream=None, **kw):
+    def moe_layer(self, x, topk_idx, topk_weight, experts, w_up, w_down, out, up_scale=None, down_scale=None,
+                  residual=None, stream=None):
         """w_up, w_down and their scales are every rank's (registered), the other arrays this rank's own."""
-        self._operator(super().moe_layer, *args, stream=stream, **kw)
+        self._operator(super().moe_layer, x, topk_idx, topk_weight, experts, w_up, w_down, out, up_scale=up_scale,
+                       down_scale=down_scale, residual=residual, stream=stream)
 
-    def logprobs(self, *args, stream=None, **kw):
+    def logprobs(self, logits, tokens, vocab, logprob, entropy=None, lse=None, top_idx=None, top_logprob=None,
+                 stream=None):
         """logits are every rank's (registered), the outputs this rank's own."""
-        self._operator(super().logprobs, *args, stream=stream, **kw)
+        self._operator(super().logprobs, logits, tokens, vocab, logprob, entropy=entropy, lse=lse, top_idx=top_idx,
+                       top_logprob=top_logprob, stream=stream)
 
-    def logprobs_backward(self, *args, stream=None, **kw):
+    def logprobs_backward(self, logits, tokens, vocab, lse, grad_logprob, grad_logits, entropy=None,
+                          grad_entropy=None, stream=None):
         """logits are every rank's (registered), the other arrays this rank's own."""
-        self._operator(super().logprobs_backward, *args, stream=stream, **kw)
+        self._operator(super().logprobs_backward, logits, tokens, vocab, lse, grad_logprob, grad_logits,
+                       entropy=entropy, grad_entropy=grad_entropy, stream=stream)
 
     def _operator(self, fn, *args, stream, **kw):
         """_call on the caller's stream: complete on every rank before the call and after it."""

@@ -1,7 +1,7 @@
 """Host side of the operators of a model's step on rank views, without a GPU: a call that reads the peers' memory
 stands between two meetings of all ranks, also when the library refuses it; the others meet nobody."""
+import inspect
 import struct
-import types
 
 import pytest
 import torch
@@ -78,6 +78,11 @@ def test_arguments_that_the_binding_refuses_still_meet_both():
         c.linear_w4(own(torch.zeros(4, 64, dtype=BF)), own(torch.zeros(8, 32, dtype=torch.uint8)),
                     own(torch.zeros(8, 3, dtype=BF)), own(torch.zeros(4, 8)), parallel="row")
     assert c.log == [("sync", None)] * 2
+
+
+@pytest.mark.parametrize("name", ["linear_w4", "moe_layer", "logprobs", "logprobs_backward"])
+def test_arguments_are_those_of_the_whole_communicator(name):
+    assert inspect.signature(getattr(ranks.RankComm, name)) == inspect.signature(getattr(SC.SimComm, name))
 
 
 def test_calls_on_own_memory_meet_nobody():
