@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <cctype>
+#include <cfloat>
 #include <climits>
 #include <cstdio>
 #include <cstdlib>
@@ -1812,6 +1813,28 @@ coll_status_t check_row(size_t len, const char* what) {
     return COLL_OK;
 }
 
+// CTAs per row of scores. Five run on an SM at a time; a CTA costs its columns and, in columns, `fixed` for its start and
+// end (log probabilities 4096, with alternatives 12288), and 512 for every part that the last one joins. The SM with the most
+// CTAs takes a fifth of that sum for each, but a CTA alone at the end as long as two (it has less to overlap with).
+// Measured on B200 with V = 131072, log probabilities, us with 1, 2, 4, 8 and 16 parts: 8 rows fp32, 8 alternatives 31, 23, 18,
+// 14, 14; 64 rows bf16, 4 alternatives 27, 21, 17, 17, 21; 300 rows 41, 37, 39, 43, 60; 700 rows without 45, 48, 50, 56,
+// 70; 2048 rows with 4 145, 171, 183, 225, 344.
+int row_parts(const sim_comm* c, size_t rows, size_t vocab, size_t fixed) {
+    int parts = 1;
+    if (rows > size_t(kLogprobMaxSplitRows)) return parts;
+    const size_t sms = size_t(c->num_sms), most = std::min(size_t(kLogprobMaxParts), std::max<size_t>(1, vocab / 1024));
+    size_t best = SIZE_MAX;
+    for (size_t q = 1; q <= most; ++q) {
+        const size_t per_sm = (rows * q + sms - 1) / sms, time = per_sm % 5 == 1 ? per_sm + 1 : per_sm;
+        const size_t cost = time * (vocab / q + fixed + (q > 1 ? 512 * q : 0));
+        if (cost < best) {
+            best = cost;
+            parts = int(q);
+        }
+    }
+    return parts;
+}
+
 }  // namespace
 
 extern "C" {
@@ -2095,26 +2118,7 @@ static coll_status_t coll_logprobs_impl(sim_comm_t c, const void* const* logits,
     }
     if ((st = sp.check()) != COLL_OK) return st;
     a.n_top = top_n;
-    // CTAs per row. Five run on an SM at a time; a CTA costs its columns and, in columns, 4096 for its start and
-    // end, 12288 with alternatives, and 512 for every part that the last one joins. The SM with the most CTAs takes a
-    // fifth of that sum for each, but a CTA alone at the end as long as two (it has less to overlap with).
-    // Measured on B200 with V = 131072, us with 1, 2, 4, 8 and 16 parts: 8 rows fp32, 8 alternatives 31, 23, 18, 14,
-    // 14; 64 rows bf16, 4 alternatives 27, 21, 17, 17, 21; 300 rows 41, 37, 39, 43, 60; 700 rows without 45, 48, 50, 56,
-    // 70; 2048 rows with 4 145, 171, 183, 225, 344.
-    a.parts = 1;
-    if (rows <= size_t(kLogprobMaxSplitRows)) {
-        const size_t sms = size_t(c->num_sms), most = std::min(size_t(kLogprobMaxParts), std::max<size_t>(1, vocab / 1024));
-        const size_t fixed = top_n > 0 ? 12288 : 4096;
-        size_t best = SIZE_MAX;
-        for (size_t q = 1; q <= most; ++q) {
-            const size_t per_sm = (rows * q + sms - 1) / sms, time = per_sm % 5 == 1 ? per_sm + 1 : per_sm;
-            const size_t cost = time * (vocab / q + fixed + (q > 1 ? 512 * q : 0));
-            if (cost < best) {
-                best = cost;
-                a.parts = int(q);
-            }
-        }
-    }
+    a.parts = row_parts(c, rows, vocab, top_n > 0 ? 12288 : 4096);
     if (a.parts > 1) {
         const size_t b_stat = align_up(rows * a.parts * sizeof(float4), 256);
         if ((st = ensure_moe(c, b_stat + rows * a.parts * size_t(top_n) * 8)) != COLL_OK) return st;
@@ -2159,6 +2163,403 @@ static coll_status_t coll_logprobs_backward_impl(sim_comm_t c, const void* const
     a.ld_grad = ld_grad;
     cudaError_t e = launch_logprobs_grad(a, int(dt), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "log probabilities gradient launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+// ---- norm, adapters, score adjustment, distillation -------------------------------------------------
+
+static coll_status_t norm_common(sim_comm* c, const void* const* x, const void* weight, size_t rows, size_t hidden, float eps,
+                                 coll_dtype_t dt, const char* what, NormArgs& a, Spans& sp) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "rows of the norm")) != COLL_OK) return st;
+    if ((st = check_row(hidden, "hidden")) != COLL_OK) return st;
+    if (rows > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "rows must fit in int32");
+    if (!(eps >= FLT_MIN && eps <= FLT_MAX)) return fail(COLL_ERR_INVALID_ARG, "eps must be finite and at least 2^-126");
+    if (!x) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (rows == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), bytes = rows * hidden * d;
+    bool vec = hidden % (16 / d) == 0 && aligned16(weight);
+    for (int r = 0; r < c->p; ++r) {
+        if ((st = take_in(sp, x[r], bytes, d, what)) != COLL_OK) return st;
+        vec = vec && aligned16(x[r]);
+        a.x[r] = x[r];
+    }
+    if ((st = take_in(sp, weight, hidden * d, d, "norm weight")) != COLL_OK) return st;
+    a.weight = weight;
+    a.p = c->p;
+    a.rank0 = first_rank(c);
+    a.ranks = ranks_of(c);
+    a.vec = vec ? 1 : 0;
+    a.eps = eps;
+    a.T = rows;
+    a.H = hidden;
+    a.ctl = make_ctl(c);
+    return COLL_OK;
+}
+
+static coll_status_t coll_rmsnorm_impl(sim_comm_t c, const void* const* x, const void* residual, const void* weight,
+                                       size_t rows, size_t hidden, float eps, coll_dtype_t dt, void* const* total,
+                                       void* const* out, uint8_t* const* q, float* const* scale, int group,
+                                       coll_stream_t stream) {
+    NormArgs a{};
+    Spans sp;
+    coll_status_t st = norm_common(c, x, weight, rows, hidden, eps, dt, "row", a, sp);
+    if (st != COLL_OK) return st;
+    if (!total && !out && !q) return fail(COLL_ERR_INVALID_ARG, "no output is given");
+    if ((q == nullptr) != (scale == nullptr)) return fail(COLL_ERR_INVALID_ARG, "q and scale go together");
+    if (q && (group < 1 || size_t(group) != hidden)) {
+        int shift = 0;
+        if ((st = check_group(group, hidden, "hidden", &shift)) != COLL_OK) return st;
+    }
+    if (rows == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), bytes = rows * hidden * d;
+    bool vec = a.vec != 0 && aligned16(residual);
+    for (int r = a.rank0; r < a.rank0 + a.ranks; ++r) {
+        if (total) {
+            if ((st = take_out(sp, total[r], bytes, d, "total")) != COLL_OK) return st;
+            vec = vec && aligned16(total[r]);
+            a.total[r] = total[r];
+        }
+        if (out) {
+            if ((st = take_out(sp, out[r], bytes, d, "out")) != COLL_OK) return st;
+            vec = vec && aligned16(out[r]);
+            a.out[r] = out[r];
+        }
+        if (q) {
+            if ((st = take_out(sp, q[r], rows * hidden, 1, "8-bit row")) != COLL_OK) return st;
+            if ((st = take_out(sp, scale[r], rows * (hidden / size_t(group)) * 4, 4, "scale")) != COLL_OK) return st;
+            vec = vec && reinterpret_cast<uintptr_t>(q[r]) % 8 == 0;
+            a.q[r] = q[r];
+            a.scale[r] = scale[r];
+        }
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    if (residual) {
+        if ((st = check_ptr(residual, bytes, d, "residual")) != COLL_OK) return st;
+        // a residual may be one rank's total (each element is read before it is written, by the same thread)
+        if (const Spans::Span* o = sp.hit({uintptr_t(residual), uintptr_t(residual) + bytes})) {
+            bool own = false;
+            for (int r = a.rank0; total && r < a.rank0 + a.ranks; ++r) own = own || (total[r] == residual && o->lo == uintptr_t(residual));
+            if (!own) return fail(COLL_ERR_INVALID_ARG, "a residual overlaps an output and is not a rank's total");
+        }
+    }
+    a.residual = residual;
+    a.has_total = total ? 1 : 0;
+    a.has_out = out ? 1 : 0;
+    a.has_q = q ? 1 : 0;
+    a.group = q ? group : int(hidden);
+    a.vec = vec ? 1 : 0;
+    cudaError_t e = launch_rmsnorm(a, int(dt), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_rmsnorm_backward_impl(sim_comm_t c, const void* const* grad_out, const void* h, const void* weight,
+                                                const void* grad_total, size_t rows, size_t hidden, float eps, coll_dtype_t dt,
+                                                void* const* grad_x, float* const* grad_weight, coll_stream_t stream) {
+    NormArgs a{};
+    Spans sp;
+    coll_status_t st = norm_common(c, grad_out, weight, rows, hidden, eps, dt, "gradient", a, sp);
+    if (st != COLL_OK) return st;
+    if (!grad_x) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (rows == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), bytes = rows * hidden * d;
+    if ((st = take_in(sp, h, bytes, d, "row")) != COLL_OK) return st;
+    if (grad_total && (st = take_in(sp, grad_total, bytes, d, "gradient of the total")) != COLL_OK) return st;
+    bool vec = a.vec != 0 && aligned16(h) && aligned16(grad_total);
+    for (int r = a.rank0; r < a.rank0 + a.ranks; ++r) {
+        if ((st = take_out(sp, grad_x[r], bytes, d, "gradient of the rows")) != COLL_OK) return st;
+        vec = vec && aligned16(grad_x[r]);
+        a.out[r] = grad_x[r];
+        if (!grad_weight) continue;
+        if ((st = take_out(sp, grad_weight[r], hidden * 4, 4, "gradient of the weight")) != COLL_OK) return st;
+        a.grad_weight[r] = grad_weight[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.h = h;
+    a.residual = grad_total;
+    a.vec = vec ? 1 : 0;
+    a.ctas = rmsnorm_grad_ctas(rows, c->num_sms);
+    if (grad_weight) {
+        if ((st = ensure_moe(c, size_t(a.ctas) * hidden * 4)) != COLL_OK) return st;
+        a.part = reinterpret_cast<float*>(c->moe);
+    }
+    int launched = 0;
+    cudaError_t e = launch_rmsnorm_grad(a, int(dt), static_cast<cudaStream_t>(stream), &launched);
+    if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
+    c->launches += launched;
+    return COLL_OK;
+}
+
+static coll_status_t coll_adapters_impl(sim_comm_t c, const void* const* x, const int32_t* adapter, const void* const* a_,
+                                        const void* const* b_, const int32_t* rank, const float* scale, int adapters,
+                                        int max_rank, size_t tokens, size_t n, size_t k, coll_parallel_t parallel,
+                                        const void* const* base, coll_dtype_t base_dt, coll_dtype_t dt, void* const* out,
+                                        coll_stream_t stream) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "the adapters' output")) != COLL_OK) return st;
+    if (base && (st = check_float(base_dt, "the adapters' base")) != COLL_OK) return st;
+    if (parallel != COLL_PARALLEL_COLUMN && parallel != COLL_PARALLEL_ROW)
+        return fail(COLL_ERR_INVALID_ARG, "unknown parallel form");
+    if (max_rank < 1 || max_rank > kAdapterMaxRank) return fail(COLL_ERR_INVALID_ARG, "max_rank must be in [1, 256]");
+    if (adapters < 1 || adapters > (1 << 24)) return fail(COLL_ERR_INVALID_ARG, "adapters must be in [1, 2^24]");
+    if ((st = check_row(k, "k")) != COLL_OK) return st;
+    if (n > kMaxRow) return fail(COLL_ERR_INVALID_ARG, "n exceeds 2^24");
+    const bool row = parallel == COLL_PARALLEL_ROW;
+    const size_t p = size_t(c->p);
+    if ((row ? k : n) % p != 0) return fail(COLL_ERR_INVALID_ARG, row ? "k must be divisible by p" : "n must be divisible by p");
+    const size_t N = row ? n : n / p, K = row ? k / p : k;
+    if (tokens > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "tokens must fit in int32");
+    const size_t matrices = size_t(adapters) * size_t(max_rank);
+    if ((st = check_rows(tokens, std::max(N, K), "tokens")) != COLL_OK || (st = check_rows(matrices, std::max(N, K), "adapters")) != COLL_OK)
+        return st;
+    if (!x || !a_ || !b_ || !out) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (tokens == 0 || N == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt), d0 = dtype_bytes(base_dt);
+    AdapterArgs a{};
+    Spans sp;
+    a.segments = row ? c->p : 1;
+    a.rank0 = row ? 0 : first_rank(c);
+    a.out0 = first_rank(c);
+    a.outs = ranks_of(c);
+    if ((st = take_in(sp, adapter, tokens * 4, 4, "adapter")) != COLL_OK) return st;
+    if (rank && (st = take_in(sp, rank, size_t(adapters) * 4, 4, "rank")) != COLL_OK) return st;
+    if (scale && (st = take_in(sp, scale, size_t(adapters) * 4, 4, "adapter scale")) != COLL_OK) return st;
+    bool x_vec = K % 8 == 0, b_vec = max_rank % 4 == 0;
+    for (int r = a.rank0; r < a.rank0 + a.segments; ++r) {
+        if ((st = take_in(sp, x[r], tokens * K * 2, 2, "token")) != COLL_OK) return st;
+        if ((st = take_in(sp, a_[r], matrices * K * 2, 2, "A")) != COLL_OK) return st;
+        x_vec = x_vec && aligned16(x[r]) && aligned16(a_[r]);
+        a.x[r] = static_cast<const uint16_t*>(x[r]);
+        a.a[r] = static_cast<const uint16_t*>(a_[r]);
+    }
+    for (int r = a.out0; r < a.out0 + a.outs; ++r) {
+        if ((st = take_out(sp, out[r], tokens * N * d, d, "out")) != COLL_OK) return st;
+        a.out[r] = out[r];
+        if (base) {
+            if ((st = check_ptr(base[r], tokens * N * d0, d0, "base")) != COLL_OK) return st;
+            a.base[r] = base[r];
+        }
+        if (row && r > a.out0) continue;  // one copy of B is read
+        if ((st = take_in(sp, b_[r], matrices * N * 2, 2, "B")) != COLL_OK) return st;
+        b_vec = b_vec && reinterpret_cast<uintptr_t>(b_[r]) % 8 == 0;
+        a.b[r] = static_cast<const uint16_t*>(b_[r]);
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    // a base may be its own rank's output (each element is read before it is written, by the same thread), and must not
+    // overlap any other
+    for (int r = a.out0; base && r < a.out0 + a.outs; ++r) {
+        const Spans::Span* o = sp.hit({uintptr_t(base[r]), uintptr_t(base[r]) + tokens * N * d0});
+        if (o && !(base[r] == out[r] && base_dt == dt))
+            return fail(COLL_ERR_INVALID_ARG, "a base overlaps an output and is not its own rank's of the same type");
+    }
+    a.adapter = adapter;
+    a.rank = rank;
+    a.scale = scale;
+    a.adapters = adapters;
+    a.R = max_rank;
+    a.Rp = int(round_up(size_t(max_rank), 16));
+    a.row = row ? 1 : 0;
+    a.has_base = base ? 1 : 0;
+    a.base_bf16 = base ? base_dt == COLL_BF16 : dt == COLL_BF16;
+    a.out_bf16 = dt == COLL_BF16;
+    a.x_vec = x_vec ? 1 : 0;
+    a.b_vec = b_vec ? 1 : 0;
+    a.T = tokens;
+    a.N = N;
+    a.K = K;
+    a.splits = adapter_splits(tokens, K, a.segments, c->num_sms);
+    if ((st = ensure_moe(c, size_t(a.splits) * tokens * size_t(a.Rp) * 4)) != COLL_OK) return st;
+    a.u = reinterpret_cast<float*>(c->moe);
+    a.ctl = make_ctl(c);
+    cudaError_t e = launch_adapters(a, c->num_sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "adapters launch");
+    c->launches += 2;
+    return COLL_OK;
+}
+
+// The shape of sharded scores, or the refusal.
+static coll_status_t scores_shape(sim_comm* c, const void* const* logits, size_t ld, size_t rows, size_t vocab, coll_dtype_t dt,
+                                  size_t* m) {
+    coll_status_t st = check_usable(c);
+    if (st != COLL_OK) return st;
+    if ((st = check_device(c)) != COLL_OK) return st;
+    if ((st = check_float(dt, "scores")) != COLL_OK) return st;
+    if (vocab < 1 || vocab > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "vocab must be in [1, 2^31)");
+    *m = (vocab + size_t(c->p) - 1) / size_t(c->p);
+    if (ld < *m) return fail(COLL_ERR_INVALID_ARG, "ld is less than the shard's columns, ceil(vocab / p)");
+    if ((st = check_count(rows, "rows")) != COLL_OK || (st = check_count(ld, "ld")) != COLL_OK) return st;
+    if ((st = check_rows(rows, ld, "rows")) != COLL_OK) return st;
+    if (!logits) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    return COLL_OK;
+}
+
+static coll_status_t coll_adjust_logits_impl(sim_comm_t c, const void* const* logits, size_t ld, size_t rows, size_t vocab,
+                                             coll_dtype_t dt, const coll_logit_rules_t* rules, void* const* out, size_t ld_out,
+                                             coll_stream_t stream) {
+    size_t m = 0;
+    coll_status_t st = scores_shape(c, logits, ld, rows, vocab, dt, &m);
+    if (st != COLL_OK) return st;
+    if (!rules || !out) return fail(COLL_ERR_INVALID_ARG, "null rules or buffer array");
+    if (ld_out < m) return fail(COLL_ERR_INVALID_ARG, "ld_out is less than the shard's columns, ceil(vocab / p)");
+    if ((st = check_count(ld_out, "ld_out")) != COLL_OK || (st = check_rows(rows, ld_out, "rows")) != COLL_OK) return st;
+    const coll_logit_rules_t& u = *rules;
+    if (u.history_len && u.ld_history > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "ld_history must fit in int32");
+    if (u.bias_start && u.bias_count > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "bias_count must fit in int32");
+    if (u.mask) {
+        if (u.ld_mask < (vocab + 31) / 32) return fail(COLL_ERR_INVALID_ARG, "ld_mask is less than ceil(vocab / 32)");
+        if ((st = check_count(u.ld_mask, "ld_mask")) != COLL_OK || (st = check_count(u.mask_rows, "mask_rows")) != COLL_OK ||
+            (st = check_rows(u.mask_rows, u.ld_mask, "mask_rows")) != COLL_OK)
+            return st;
+        if (!u.mask_row && u.mask_rows < rows) return fail(COLL_ERR_INVALID_ARG, "fewer rows of masks than of scores");
+    }
+    if ((st = check_rows(rows, u.history_len ? u.ld_history : 0, "rows")) != COLL_OK) return st;
+    if (rows == 0) return COLL_OK;
+    Spans sp;
+    AdjustArgs a{};
+    a.rules = u;
+    if (u.history_len) {
+        if ((st = take_in(sp, u.history_len, rows * 4, 4, "history length")) != COLL_OK) return st;
+        if ((st = take_in(sp, u.history, rows * u.ld_history * 4, 4, "history")) != COLL_OK) return st;
+        if (u.prompt_len && (st = take_in(sp, u.prompt_len, rows * 4, 4, "prompt length")) != COLL_OK) return st;
+        for (const float* v : {u.repetition, u.frequency, u.presence})
+            if (v && (st = take_in(sp, v, rows * 4, 4, "penalty")) != COLL_OK) return st;
+        a.hist_vec = u.ld_history % 4 == 0 && aligned16(u.history);
+    }
+    if (u.bias_start) {
+        if ((st = take_in(sp, u.bias_start, (rows + 1) * 4, 4, "bias start")) != COLL_OK) return st;
+        if ((st = take_in(sp, u.bias_token, u.bias_count * 4, 4, "bias token")) != COLL_OK) return st;
+        if ((st = take_in(sp, u.bias_value, u.bias_count * 4, 4, "bias")) != COLL_OK) return st;
+    }
+    if (u.mask) {
+        if ((st = take_in(sp, u.mask, u.mask_rows * u.ld_mask * 4, 4, "mask")) != COLL_OK) return st;
+        if (u.mask_row && (st = take_in(sp, u.mask_row, rows * 4, 4, "mask row")) != COLL_OK) return st;
+    }
+    const size_t d = dtype_bytes(dt), in_bytes = ((rows - 1) * ld + m) * d, out_bytes = ((rows - 1) * ld_out + m) * d;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = check_ptr(logits[r], in_bytes, d, "score")) != COLL_OK) return st;
+        if ((st = take_out(sp, out[r], out_bytes, d, "out")) != COLL_OK) return st;
+        a.logits[r] = logits[r];
+        a.out[r] = out[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    // scores may be their own rank's output, and must not overlap any other
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        const Spans::Span* o = sp.hit({uintptr_t(logits[r]), uintptr_t(logits[r]) + in_bytes});
+        if (o && !(logits[r] == out[r] && ld == ld_out))
+            return fail(COLL_ERR_INVALID_ARG, "scores overlap an output and are not in place");
+    }
+    a.p = c->p;
+    a.rank0 = first_rank(c);
+    a.ranks = ranks_of(c);
+    a.rows = rows;
+    a.V = vocab;
+    a.m = m;
+    a.ld = ld;
+    a.ld_out = ld_out;
+    a.ctl = make_ctl(c);
+    cudaError_t e = launch_adjust(a, int(dt), c->num_sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "score adjustment launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t distill_common(sim_comm* c, const void* const* logits, size_t ld, const int32_t* top_idx,
+                                    const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dt,
+                                    float temperature, int tail, bool all_ranks, DistillArgs& a, Spans& sp) {
+    size_t m = 0;
+    coll_status_t st = scores_shape(c, logits, ld, rows, vocab, dt, &m);
+    if (st != COLL_OK) return st;
+    if (top_n < 1 || top_n > kDistillMaxTop) return fail(COLL_ERR_INVALID_ARG, "top_n must be in [1, 256]");
+    if (!(temperature >= FLT_MIN && temperature <= 1.0f / FLT_MIN)) return fail(COLL_ERR_INVALID_ARG, "temperature must be in [2^-126, 2^126]");
+    if (tail && temperature != 1.0f) return fail(COLL_ERR_INVALID_ARG, "with the class of the rest the temperature must be 1");
+    if (rows == 0) return COLL_OK;
+    if ((st = check_rows(rows, size_t(top_n), "rows")) != COLL_OK) return st;
+    if ((st = take_in(sp, top_idx, rows * top_n * 4, 4, "teacher's column")) != COLL_OK) return st;
+    if ((st = take_in(sp, top_value, rows * top_n * 4, 4, "teacher's value")) != COLL_OK) return st;
+    const size_t d = dtype_bytes(dt), bytes = ((rows - 1) * ld + m) * d;
+    for (int r = 0; r < c->p; ++r) {
+        if (!all_ranks && c->rank >= 0 && r != c->rank) continue;
+        if ((st = take_in(sp, logits[r], bytes, d, "score")) != COLL_OK) return st;
+        a.logits[r] = logits[r];
+    }
+    a.top_idx = top_idx;
+    a.top_value = top_value;
+    a.p = c->p;
+    a.view_rank = c->rank;
+    a.n = top_n;
+    a.tail = tail ? 1 : 0;
+    a.inv_temperature = 1.0f / temperature;
+    a.rows = rows;
+    a.V = vocab;
+    a.m = m;
+    a.ld = ld;
+    a.st = c->dstate;
+    a.ctl = make_ctl(c);
+    return COLL_OK;
+}
+
+static coll_status_t coll_distill_impl(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* top_idx,
+                                       const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dt,
+                                       float temperature, int tail, float* const* loss, float* const* stats,
+                                       coll_stream_t stream) {
+    DistillArgs a{};
+    Spans sp;
+    coll_status_t st = distill_common(c, logits, ld, top_idx, top_value, top_n, rows, vocab, dt, temperature, tail, true, a, sp);
+    if (st != COLL_OK) return st;
+    if (!loss) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    if (rows == 0) return COLL_OK;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_out(sp, loss[r], rows * 4, 4, "loss")) != COLL_OK) return st;
+        a.loss[r] = loss[r];
+        if (!stats) continue;
+        if ((st = take_out(sp, stats[r], rows * kDistillStats * 4, 4, "stats")) != COLL_OK) return st;
+        a.stats[r] = stats[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.parts = row_parts(c, rows, vocab, 8192);
+    if (a.parts > 1) {
+        if ((st = ensure_moe(c, rows * a.parts * sizeof(float2))) != COLL_OK) return st;
+        a.part_stat = reinterpret_cast<float2*>(c->moe);
+    }
+    cudaError_t e = launch_distill(a, int(dt), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "distillation launch");
+    c->launches += 1;
+    return COLL_OK;
+}
+
+static coll_status_t coll_distill_backward_impl(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* top_idx,
+                                                const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dt,
+                                                float temperature, int tail, const float* const* stats, const float* grad_loss,
+                                                void* const* grad_logits, size_t ld_grad, coll_stream_t stream) {
+    DistillArgs a{};
+    Spans sp;
+    coll_status_t st = distill_common(c, logits, ld, top_idx, top_value, top_n, rows, vocab, dt, temperature, tail, false, a, sp);
+    if (st != COLL_OK) return st;
+    if (!stats || !grad_logits) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
+    const size_t m = (vocab + size_t(c->p) - 1) / size_t(c->p);
+    if (ld_grad < m) return fail(COLL_ERR_INVALID_ARG, "ld_grad is less than the shard's columns, ceil(vocab / p)");
+    if ((st = check_count(ld_grad, "ld_grad")) != COLL_OK || (st = check_rows(rows, ld_grad, "rows")) != COLL_OK) return st;
+    if (rows == 0) return COLL_OK;
+    const size_t d = dtype_bytes(dt);
+    if ((st = take_in(sp, grad_loss, rows * 4, 4, "loss gradient")) != COLL_OK) return st;
+    for (int r = first_rank(c), n = ranks_of(c); n > 0; ++r, --n) {
+        if ((st = take_in(sp, stats[r], rows * kDistillStats * 4, 4, "stats")) != COLL_OK) return st;
+        if ((st = take_out(sp, grad_logits[r], ((rows - 1) * ld_grad + m) * d, d, "score gradient")) != COLL_OK) return st;
+        a.stats_in[r] = stats[r];
+        a.grad_logits[r] = grad_logits[r];
+    }
+    if ((st = sp.check()) != COLL_OK) return st;
+    a.grad_loss = grad_loss;
+    a.ld_grad = ld_grad;
+    cudaError_t e = launch_distill_grad(a, int(dt), static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "distillation gradient launch");
     c->launches += 1;
     return COLL_OK;
 }
@@ -2457,6 +2858,54 @@ coll_status_t coll_logprobs_backward(sim_comm_t c, const void* const* logits, si
     TraceScope ts(c, "logprobs_backward", rows, int(dt), -1, -1, -1, stream);
     return ts.done(coll_logprobs_backward_impl(c, logits, ld, tokens, rows, vocab, dt, lse, entropy, grad_logprob,
                                                grad_entropy, grad_logits, ld_grad, stream));
+}
+
+coll_status_t coll_rmsnorm(sim_comm_t c, const void* const* x, const void* residual, const void* weight, size_t rows,
+                           size_t hidden, float eps, coll_dtype_t dt, void* const* total, void* const* out,
+                           uint8_t* const* q, float* const* scale, int group, coll_stream_t stream) {
+    TraceScope ts(c, "rmsnorm", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_rmsnorm_impl(c, x, residual, weight, rows, hidden, eps, dt, total, out, q, scale, group, stream));
+}
+
+coll_status_t coll_rmsnorm_backward(sim_comm_t c, const void* const* grad_out, const void* h, const void* weight,
+                                    const void* grad_total, size_t rows, size_t hidden, float eps, coll_dtype_t dt,
+                                    void* const* grad_x, float* const* grad_weight, coll_stream_t stream) {
+    TraceScope ts(c, "rmsnorm_backward", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_rmsnorm_backward_impl(c, grad_out, h, weight, grad_total, rows, hidden, eps, dt, grad_x,
+                                              grad_weight, stream));
+}
+
+coll_status_t coll_adapters(sim_comm_t c, const void* const* x, const int32_t* adapter, const void* const* a,
+                            const void* const* b, const int32_t* rank, const float* scale, int adapters, int max_rank,
+                            size_t tokens, size_t n, size_t k, coll_parallel_t parallel, const void* const* base,
+                            coll_dtype_t base_dt, coll_dtype_t dt, void* const* out, coll_stream_t stream) {
+    TraceScope ts(c, "adapters", tokens, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_adapters_impl(c, x, adapter, a, b, rank, scale, adapters, max_rank, tokens, n, k, parallel, base,
+                                      base_dt, dt, out, stream));
+}
+
+coll_status_t coll_adjust_logits(sim_comm_t c, const void* const* logits, size_t ld, size_t rows, size_t vocab,
+                                 coll_dtype_t dt, const coll_logit_rules_t* rules, void* const* out, size_t ld_out,
+                                 coll_stream_t stream) {
+    TraceScope ts(c, "adjust_logits", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_adjust_logits_impl(c, logits, ld, rows, vocab, dt, rules, out, ld_out, stream));
+}
+
+coll_status_t coll_distill(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* top_idx,
+                           const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dt,
+                           float temperature, int tail, float* const* loss, float* const* stats, coll_stream_t stream) {
+    TraceScope ts(c, "distill", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_distill_impl(c, logits, ld, top_idx, top_value, top_n, rows, vocab, dt, temperature, tail, loss,
+                                     stats, stream));
+}
+
+coll_status_t coll_distill_backward(sim_comm_t c, const void* const* logits, size_t ld, const int32_t* top_idx,
+                                    const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dt,
+                                    float temperature, int tail, const float* const* stats, const float* grad_loss,
+                                    void* const* grad_logits, size_t ld_grad, coll_stream_t stream) {
+    TraceScope ts(c, "distill_backward", rows, int(dt), -1, -1, -1, stream);
+    return ts.done(coll_distill_backward_impl(c, logits, ld, top_idx, top_value, top_n, rows, vocab, dt, temperature, tail,
+                                              stats, grad_loss, grad_logits, ld_grad, stream));
 }
 
 }  // extern "C"

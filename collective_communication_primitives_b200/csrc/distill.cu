@@ -1,0 +1,417 @@
+// Loss against a teacher's best columns, over a vocabulary whose columns are sharded over the ranks, and the gradient
+// of the scores.
+//
+//   P = softmax(x / T) over all V columns; q over the teacher's n places: softmax(value / T), or e^value with one more
+//   class for the columns that are not listed, Q = 1 - sum q and P_rest = sum of their P
+//   loss = sum q (ln q - ln P) + Q (ln Q - ln P_rest)
+//   dx[v] = g / T (A P[v] - q[v]),  A = sum q + Q;  off the list, with the class of the rest, g / T P[v] (A - Q / P_rest)
+//
+// Forward: one pass over the scores with a running maximum and sum, as in the log probabilities; few rows are cut into
+// parts that the last CTA joins in order, and the last CTA of a row does the list. With the class of the rest the
+// pass leaves the listed columns out, so that P_rest is a sum and no difference: what is left beside a peaked
+// distribution keeps its precision. A filter in shared memory (a bit per vector of scores, modulo its size) finds the
+// vectors with a listed column, a table of them which of their scores are listed.
+//
+// Differences x - m are formed before they are scaled, so the sums are as exact for scores far from 0 as for others, and
+// a row of the type's lowest value is a row like any other. A row of nothing but -inf has P = 0.
+//
+// Gradient: off the list dx = 2^((x - m) c - l) k with three constants of the row; with the class of the rest m and l are
+// those of the rest and k = g / T (A P_rest - Q), which stays finite where P_rest vanishes. Then the CTA writes the listed columns
+// among its own over it. Both are bound by the scores' bytes, the forward pass for 2-byte scores by one exponential each too.
+#include <algorithm>
+#include <cfloat>
+
+#include "scores.cuh"
+
+namespace simcomm {
+
+constexpr int kFilterBits = 16384;
+constexpr int kTable = 512;               // at least twice the places
+constexpr uint32_t kEmpty = 0xffffffffu;  // no column: a vocabulary has fewer than 2^31
+
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Sum s of 2^((x - m) c) over a set of scores with maximum m (at least -FLT_MAX; NaN if a score is).
+struct Mass {
+    float m, s;
+};
+__device__ __forceinline__ Mass mass_none() { return Mass{-FLT_MAX, 0.0f}; }
+__device__ __forceinline__ float mass_at(const Mass& a, float m, float c) { return a.s * ex2((a.m - m) * c); }
+__device__ __forceinline__ Mass mass_join(const Mass& a, const Mass& b, float c) {
+    const float m = max_nan(a.m, b.m);
+    return Mass{m, mass_at(a, m, c) + mass_at(b, m, c)};
+}
+__device__ __forceinline__ Mass mass_warp(const Mass& a, float c) {
+    float m = a.m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float s = mass_at(a, m, c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    return Mass{m, s};
+}
+
+// The listed columns of a row, and where they lie in its vectors.
+struct Listed {
+    int32_t id[kDistillMaxTop];
+    uint32_t filter[kFilterBits / 32];
+    uint32_t key[kTable];    // first column of a vector with listed columns
+    uint32_t mask[kTable];   // which of its columns are
+};
+template <int DT> __device__ __forceinline__ uint32_t filter_bit(uint32_t col) {
+    return (col / Pack16<DT>::L) & (kFilterBits - 1);  // neighbouring vectors have neighbouring bits, whatever their phase
+}
+// A column's first place among the table's.
+__device__ __forceinline__ uint32_t table_at(uint32_t col) { return (col * 2654435761u) >> 23; }
+static_assert(kTable == 512, "table_at gives 9 bits");
+
+// Which of a vector's columns are listed.
+__device__ __forceinline__ uint32_t listed_in(const Listed& s, uint32_t col) {
+    for (uint32_t at = table_at(col), k = 0; k < kTable; at = (at + 1) % kTable, ++k) {
+        if (s.key[at] == col) return s.mask[at];
+        if (s.key[at] == kEmpty) break;
+    }
+    return 0u;
+}
+template <int DT> __device__ __forceinline__ void leave_out(uint4& v, uint32_t mask) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int l = 0; l < Pack16<DT>::L; ++l)
+        if ((mask >> l) & 1u) {
+            if constexpr (DT == COLL_BF16)
+                w[l / 2] = l % 2 ? (w[l / 2] & 0xffffu) | 0xff800000u : (w[l / 2] & 0xffff0000u) | 0xff80u;
+            else
+                w[l] = 0xff800000u;
+        }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Enters the listed columns among [v0, v1). CTA-collective; id is set.
+template <int DT> __device__ __forceinline__ void list_columns(const DistillArgs& a, size_t row, uint32_t v0, uint32_t v1, Listed& s) {
+    for (int i = threadIdx.x; i < kFilterBits / 32; i += kLpThreads) s.filter[i] = 0u;
+    for (int i = threadIdx.x; i < kTable; i += kLpThreads) {
+        s.key[i] = kEmpty;
+        s.mask[i] = 0u;
+    }
+    __syncthreads();
+    const uint32_t id = int(threadIdx.x) < a.n ? uint32_t(s.id[threadIdx.x]) : kEmpty;
+    if (id >= v0 && id < v1) {
+        const uint32_t m = uint32_t(a.m), first = max(v0, id / m * m);
+        const Piece<DT> pc(a, row, first, v1);
+        const uint32_t k = id - first;
+        constexpr int L = Piece<DT>::L;
+        if (k >= pc.head && k < pc.head + pc.vecs * L) {
+            const uint32_t l = (k - pc.head) % L, col = id - l;
+            atomicOr(&s.filter[filter_bit<DT>(col) / 32], 1u << (filter_bit<DT>(col) % 32));
+            uint32_t at = table_at(col);
+            while (true) {  // ends: the table has more entries than there are places
+                const uint32_t was = atomicCAS(&s.key[at], kEmpty, col);
+                if (was == kEmpty || was == col) break;
+                at = (at + 1) % kTable;
+            }
+            atomicOr(&s.mask[at], 1u << l);
+        }
+    }
+    __syncthreads();
+}
+
+// A thread's sum over its share of the columns [v0, v1), without the listed ones if REST.
+template <int DT, bool REST>
+__device__ __forceinline__ Mass sum_columns(const DistillArgs& a, size_t row, uint32_t v0, uint32_t v1, float c, const Listed& list) {
+    constexpr int L = Pack16<DT>::L;
+    constexpr uint32_t kNone = DT == COLL_BF16 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    float m = -FLT_MAX;
+    unsigned long long s = 0ull;
+    const unsigned long long cc = pack2(c, c), zero = 0ull;
+    auto raise = [&](float top) {
+        if (!(top <= m)) {  // larger, or NaN
+            const float f = ex2((m - top) * c);
+            s = fma2(s, pack2(f, f), zero);
+            m = top;
+        }
+    };
+    auto add = [&](const uint4& v) {
+        float x[L];
+        Pack16<DT>::unpack(v, x);
+        const unsigned long long mm = pack2(-m, -m);
+#pragma unroll
+        for (int q = 0; q < L; q += 2) {
+            float d0, d1;
+            unpack2(mul2(add2(pack2(x[q], x[q + 1]), mm), cc), d0, d1);
+            s = add2(s, pack2(ex2(d0), ex2(d1)));
+        }
+    };
+    for (uint32_t v = v0; v < v1;) {
+        const Piece<DT> pc(a, row, v, v1);
+        if (threadIdx.x < pc.head + pc.tail) {  // scores before and behind the whole vectors
+            const uint32_t at = pc.end_at(threadIdx.x);
+            float x = load_elem<DT>(pc.base, at);
+            if constexpr (REST)
+                for (int i = 0; i < a.n; ++i)
+                    if (uint32_t(list.id[i]) == v + at) x = -INFINITY;
+            raise(x);
+            s = add2(s, pack2(ex2((x - m) * c), 0.0f));
+        }
+        for (uint32_t i0 = 0; i0 < pc.vecs; i0 += kLpThreads * kLpUnroll) {
+            uint4 raw[kLpUnroll];
+#pragma unroll
+            for (int q = 0; q < kLpUnroll; ++q) {
+                const uint32_t i = i0 + q * kLpThreads + threadIdx.x;
+                raw[q] = i < pc.vecs ? ld_stream_v4(pc.vector(i)) : make_uint4(kNone, kNone, kNone, kNone);
+            }
+            if constexpr (REST) {
+#pragma unroll
+                for (int q = 0; q < kLpUnroll; ++q) {
+                    const uint32_t col = v + pc.head + (i0 + q * kLpThreads + threadIdx.x) * L, bit = filter_bit<DT>(col);
+                    if ((list.filter[bit / 32] >> (bit % 32)) & 1u) leave_out<DT>(raw[q], listed_in(list, col));
+                }
+            }
+            float top = vector_top<DT>(raw[0]);
+#pragma unroll
+            for (int q = 1; q < kLpUnroll; ++q) top = max_nan(top, vector_top<DT>(raw[q]));
+            raise(top);
+#pragma unroll
+            for (int q = 0; q < kLpUnroll; ++q) {
+                if (i0 + q * kLpThreads + (threadIdx.x & ~31u) >= pc.vecs) break;  // none of this warp's
+                add(raw[q]);
+            }
+        }
+        v = pc.end;
+    }
+    float s0, s1;
+    unpack2(s, s0, s1);
+    return Mass{m, s0 + s1};
+}
+
+template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, 5) k_distill(const __grid_constant__ DistillArgs a) {
+    __shared__ Listed s_list;
+    __shared__ Mass s_mass[kLpWarps];
+    __shared__ float s_w[kLpWarps];
+    __shared__ double s_d[kLpWarps];
+    __shared__ int s_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
+    const size_t row = blockIdx.x / a.parts;
+    const int part = int(blockIdx.x % a.parts);
+    const float c = kLpLog2e * a.inv_temperature;
+    if (t == 0) s_flag = status_failed(a.ctl);
+    if (t < a.n) {
+        int32_t id = a.top_idx[row * a.n + t];
+        if (id < -1 || (id >= 0 && size_t(id) >= a.V)) {
+            raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+            id = -1;
+        }
+        s_list.id[t] = id;
+    }
+    __syncthreads();
+    if (s_flag) return;
+    const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
+    if constexpr (TAIL) list_columns<DT>(a, row, v0, v1, s_list);
+    Mass all = mass_warp(sum_columns<DT, TAIL>(a, row, v0, v1, c, s_list), c);
+    if (lane == 0) s_mass[warp] = all;
+    __syncthreads();
+    all = s_mass[0];
+    for (int w = 1; w < kLpWarps; ++w) all = mass_join(all, s_mass[w], c);
+    if (a.parts > 1) {
+        // the parts' sums meet in scratch; the row's last CTA joins them in part order
+        if (t == 0) {
+            a.part_stat[row * a.parts + part] = make_float2(all.m, all.s);
+            __threadfence();
+            s_flag = atomicAdd(&a.st->row_ctr[row], 1u) == uint32_t(a.parts - 1);
+        }
+        __syncthreads();
+        if (!s_flag) return;
+        __threadfence();
+        if (t == 0) a.st->row_ctr[row] = 0u;
+        if (warp == 0) {
+            all = mass_none();
+            for (int q = lane; q < a.parts; q += 32) {
+                const float2 v = __ldcg(&a.part_stat[row * a.parts + q]);
+                all = mass_join(all, Mass{v.x, v.y}, c);
+            }
+            all = mass_warp(all, c);
+            if (lane == 0) s_mass[0] = all;
+        }
+        __syncthreads();
+        all = s_mass[0];
+    }
+    const Mass rest = all;  // with TAIL of the columns that are not listed
+    // the places, one to a thread
+    const int32_t id = t < a.n ? s_list.id[t] : -1;
+    const bool given = id >= 0;
+    const float x = given ? score_at(a, DT, row, size_t(id)) : -INFINITY;
+    const float value = given ? a.top_value[row * a.n + t] : -INFINITY;
+    if constexpr (TAIL) {
+        bool first = given;
+        for (int j = 0; j < t && j < a.n && first; ++j) first = s_list.id[j] != id;
+        Mass mine{cta_max(first ? max_nan(x, -FLT_MAX) : -FLT_MAX, s_w), 0.0f};
+        mine.s = cta_sum(first ? ex2((x - mine.m) * c) : 0.0f, s_w);
+        all = mass_join(rest, mine, c);
+    }
+    // The loss is a small difference of terms of the size of ln V: they are formed and added in 64 bits (in 32 the losses of 16
+    // rows of 131072 were off by 3e-6 of their size), a few operations to a place.
+    const bool none = all.s == 0.0f;  // nothing but -inf
+    const double ln_s = none ? 0.0 : log(double(all.s)), inv_t = a.inv_temperature;
+    const double lp = none ? -double(INFINITY) : (double(x) - double(all.m)) * inv_t - ln_s;
+    float top = 0.0f;
+    double inv_z = 1.0, q, lq;
+    if constexpr (TAIL) {
+        lq = value;
+        q = exp(lq);
+    } else {
+        top = cta_max(value, s_w);
+        if (top == -INFINITY) top = 0.0f;  // no teacher
+        lq = (double(value) - double(top)) * inv_t;
+        q = exp(lq);
+        const double z = cta_sum(q, s_d);
+        inv_z = z == 0.0 ? 0.0 : 1.0 / z;
+        q *= inv_z;
+        lq -= log(z);
+    }
+    double weight = cta_sum(q, s_d), loss = cta_sum(q > 0.0 ? q * (lq - lp) : q, s_d), k = weight;
+    if constexpr (TAIL) {
+        double left = 1.0 - weight;
+        if (left < 0x1p-20) left = 0.0;
+        const double ln_rest = rest.s == 0.0f ? -double(INFINITY) : ((double(rest.m) - double(all.m)) * inv_t + log(double(rest.s))) - ln_s;
+        if (left != 0.0) loss += left * (log(left) - ln_rest);
+        weight += left;
+        k = weight * exp(ln_rest) - left;
+    }
+    const int first = a.view_rank >= 0 ? a.view_rank : 0, last = a.view_rank >= 0 ? first + 1 : a.p;
+    for (int r = first + t; r < last; r += kLpThreads) {
+        a.loss[r][row] = float(loss);
+        if (!a.stats[r]) continue;
+        const bool empty = rest.s == 0.0f;  // no column off the list has a probability
+        float* o = a.stats[r] + row * kDistillStats;
+        o[0] = empty ? 0.0f : rest.m;
+        o[1] = empty ? 0.0f : log2f(rest.s);
+        o[2] = empty ? 0.0f : float(k);
+        o[3] = none ? 0.0f : all.m;
+        o[4] = float(ln_s);
+        o[5] = none ? 0.0f : float(weight);
+        o[6] = top;
+        o[7] = none ? 0.0f : float(inv_z);
+    }
+}
+
+// ---- gradient ------------------------------------------------------------------------------------
+
+// Sums a row's gradient refers to.
+struct RowSlope {
+    float m, l, k;
+};
+template <int DT> __device__ __forceinline__ uint4 slope_vector(const RowSlope& g, float c, const uint4& v) {
+    constexpr int L = Pack16<DT>::L;
+    float x[L];
+    Pack16<DT>::unpack(v, x);
+    const unsigned long long mm = pack2(-g.m, -g.m), cc = pack2(c, c), ll = pack2(-g.l, -g.l), kk = pack2(g.k, g.k);
+#pragma unroll
+    for (int q = 0; q < L; q += 2) {
+        float d0, d1;
+        unpack2(fma2(add2(pack2(x[q], x[q + 1]), mm), cc, ll), d0, d1);
+        unpack2(mul2(pack2(ex2(d0), ex2(d1)), kk), x[q], x[q + 1]);
+    }
+    return Pack16<DT>::pack(x);
+}
+
+template <int DT> __global__ void __launch_bounds__(kLpThreads, 4) k_distill_grad(const __grid_constant__ DistillArgs a) {
+    constexpr int L = Pack16<DT>::L, D = Elem<DT>::kBytes;
+    __shared__ int32_t s_id[kDistillMaxTop];
+    __shared__ float s_q[kDistillMaxTop];
+    __shared__ int s_flag;
+    const int t = threadIdx.x;
+    // CTA -> (row, rank, piece of the shard's row)
+    size_t b = blockIdx.x;
+    const size_t piece = b % a.parts;
+    b /= a.parts;
+    const int r = a.view_rank >= 0 ? a.view_rank : int(b % a.p);
+    const size_t row = a.view_rank >= 0 ? b : b / a.p;
+    const float* st = a.stats_in[r] + row * kDistillStats;
+    if (t == 0) s_flag = status_failed(a.ctl);
+    const float c = kLpLog2e * a.inv_temperature, g = a.grad_loss[row] * a.inv_temperature, weight = st[5];
+    const RowSlope slope{st[0], st[1], st[2] * g};
+    int32_t id = -1;
+    if (t < a.n) {
+        id = a.top_idx[row * a.n + t];
+        if (id < -1 || (id >= 0 && size_t(id) >= a.V)) {
+            raise_status(a.ctl, COLL_ERR_INVALID_ARG);
+            id = -1;
+        }
+        s_id[t] = id;
+        s_q[t] = id < 0 ? 0.0f : expf((a.top_value[row * a.n + t] - st[6]) * a.inv_temperature) * st[7];
+    }
+    __syncthreads();
+    if (s_flag) return;
+    const bool zero = weight == 0.0f;                                      // no teacher, or nothing but -inf
+    const size_t v0 = size_t(r) * a.m;                                     // first column of the shard
+    const size_t all = v0 < a.V ? min(a.m, a.V - v0) : 0;                  // its columns; the rest is padding
+    const size_t have = zero ? 0 : all;
+    const char* in = static_cast<const char*>(a.logits[r]) + row * a.ld * D;
+    char* out = static_cast<char*>(a.grad_logits[r]) + row * a.ld_grad * D;
+    const size_t c0 = a.m * piece / a.parts, c1 = a.m * (piece + 1) / a.parts, n = c1 - c0;
+    const uintptr_t ia = reinterpret_cast<uintptr_t>(in + c0 * D), oa = reinterpret_cast<uintptr_t>(out + c0 * D);
+    const bool together = ((ia ^ oa) & 15) == 0;  // 16-byte boundaries fall on the same columns
+    const size_t head = together ? min(n, size_t((16 - (ia & 15)) & 15) / D) : n;
+    // whole vectors of the shard's own columns; what is left of them and the padding go one by one
+    const size_t vecs = together && have > c0 + head ? (min(c1, have) - c0 - head) / L : 0, rest = n - head - vecs * L;
+    for (size_t i = t; i < head + rest; i += kLpThreads) {
+        const size_t at = c0 + (i < head ? i : i + vecs * L);
+        float y = 0.0f;
+        if (at < have) y = ex2(__fmaf_rn(load_elem<DT>(in, at) - slope.m, c, -slope.l)) * slope.k;
+        store_elem<DT>(out, at, y);
+    }
+    const size_t body = c0 + head;
+    for (size_t i0 = 0; i0 < vecs; i0 += kLpThreads * kLpUnroll) {
+        uint4 raw[kLpUnroll];
+#pragma unroll
+        for (int q = 0; q < kLpUnroll; ++q) {
+            const size_t i = i0 + q * kLpThreads + t;
+            if (i < vecs) raw[q] = ld_stream_v4(in + (body + i * L) * D);
+        }
+#pragma unroll
+        for (int q = 0; q < kLpUnroll; ++q) {
+            const size_t i = i0 + q * kLpThreads + t;
+            if (i >= vecs) break;
+            st_v4(out + (body + i * L) * D, slope_vector<DT>(slope, c, raw[q]));
+        }
+    }
+    __syncthreads();
+    // the listed columns of this piece, over what the pass has written there; the first place of a column writes it
+    const size_t at = size_t(uint32_t(id)) - v0;
+    if (zero || id < 0 || size_t(id) < v0 || at < c0 || at >= min(c1, all)) return;
+    float q = 0.0f;
+    for (int j = 0; j < a.n; ++j)
+        if (s_id[j] == id) {
+            if (j < t) return;
+            q += s_q[j];
+        }
+    const float p = expf((load_elem<DT>(in, at) - st[3]) * a.inv_temperature - st[4]);
+    store_elem<DT>(out, at, g * (weight * p - q));
+}
+
+cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s) {
+    const size_t ctas = a.rows * size_t(a.parts);
+    if (ctas > size_t(INT32_MAX)) return cudaErrorInvalidValue;
+    auto go = [&](auto kernel) {
+        kernel<<<unsigned(ctas), kLpThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    };
+    if (dtype == COLL_BF16) return a.tail ? go(k_distill<COLL_BF16, true>) : go(k_distill<COLL_BF16, false>);
+    return a.tail ? go(k_distill<COLL_FP32, true>) : go(k_distill<COLL_FP32, false>);
+}
+
+cudaError_t launch_distill_grad(const DistillArgs& args, int dtype, cudaStream_t s) {
+    DistillArgs a = args;
+    constexpr size_t kPiece = 16384;  // columns of one CTA, as in the gradient of the log probabilities
+    a.parts = int(std::max<size_t>(1, (a.m + kPiece - 1) / kPiece));
+    const size_t ctas = a.rows * size_t(a.parts) * (a.view_rank >= 0 ? 1 : size_t(a.p));
+    if (ctas > size_t(INT32_MAX)) return cudaErrorInvalidValue;
+    if (dtype == COLL_BF16) k_distill_grad<COLL_BF16><<<unsigned(ctas), kLpThreads, 0, s>>>(a);
+    else k_distill_grad<COLL_FP32><<<unsigned(ctas), kLpThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace simcomm

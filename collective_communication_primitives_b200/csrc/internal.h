@@ -25,7 +25,7 @@ struct DevState {
     uint32_t comb_done;              // MoE combine: CTAs that left the token loop (the last one resets both)
     uint32_t layer_ctr;              // expert layer: grid-barrier arrivals (zero between calls)
     uint32_t layer_done;             // expert layer: CTAs that left (the last one resets both)
-    uint32_t row_ctr[4096];          // log probabilities: parts of a row that are done (zero between calls)
+    uint32_t row_ctr[4096];          // log probabilities, distillation: parts of a row that are done (zero between calls)
 };
 
 // What a kernel needs to report errors and notice an abort.
@@ -335,6 +335,91 @@ struct LogprobArgs {
     Ctl ctl;
 };
 
+// ---- root-mean-square norm -----------------------------------------------------------------------
+
+struct NormArgs {
+    const void* x[kMaxRanks];            // the ranks' partial rows [T][H]; backward: their gradients of the normed rows
+    void* total[kMaxRanks];              // [T][H] or null
+    void* out[kMaxRanks];                // [T][H] or null; backward: the rows' gradient
+    uint8_t* q[kMaxRanks];               // [T][H] e4m3, or null
+    float* scale[kMaxRanks];             // [T][H / group]
+    float* grad_weight[kMaxRanks];       // backward: [H] or null
+    const void* residual;                // [T][H] or null; backward: the gradient past the norm
+    const void* h;                       // backward: [T][H]
+    const void* weight;                  // [H]
+    float* part;                         // backward, scratch: [ctas][H] the CTAs' sums of the weight's gradient
+    int p;
+    int rank0, ranks;                    // ranks whose outputs the call writes
+    int has_total, has_out, has_q;
+    int group;
+    int vec;                             // rows of whole 16-byte units at aligned addresses
+    int ctas;                            // backward: CTAs, each with every ctas-th row
+    float eps;
+    size_t T, H;
+    Ctl ctl;
+};
+
+// ---- low-rank adapters ---------------------------------------------------------------------------
+
+constexpr int kAdapterMaxRank = 256;
+
+struct AdapterArgs {
+    const uint16_t* x[kMaxRanks];        // bf16 [T][K]
+    const uint16_t* a[kMaxRanks];        // bf16 [adapters][R][K]
+    const uint16_t* b[kMaxRanks];        // bf16 [adapters][N][R]
+    const void* base[kMaxRanks];         // [T][N] or null
+    void* out[kMaxRanks];                // [T][N]
+    const int32_t* adapter;              // [T]
+    const int32_t* rank;                 // [adapters] or null
+    const float* scale;                  // [adapters] or null
+    int segments, rank0;                 // ranks whose columns of x and a make up K, the first of them
+    int out0, outs;                      // ranks whose outputs the call writes
+    int row;                             // every output has all rows of B (and the first one's copy of B is read)
+    int R, Rp, adapters;                 // Rp: R in whole 16s
+    int base_bf16, out_bf16, has_base;
+    int x_vec, b_vec;                    // 16-byte units of x and a, 8-byte units of b
+    size_t T, N, K;                      // of one rank's shard
+    int splits;                          // parts of the sum over k
+    float* u;                            // scratch: [splits][T][Rp]
+    Ctl ctl;
+};
+
+// ---- penalties, biases and masks on sharded scores ----------------------------------------------
+
+struct AdjustArgs {
+    const void* logits[kMaxRanks];       // [rows][ld]
+    void* out[kMaxRanks];                // [rows][ld_out]
+    coll_logit_rules_t rules;
+    int p, rank0, ranks;
+    int cols, tiles;                     // columns of one CTA, CTAs per row of a shard
+    int hist_vec;                        // history rows are 16-byte aligned
+    size_t rows, V, m, ld, ld_out;
+    Ctl ctl;
+};
+
+// ---- distillation over a sharded vocabulary ------------------------------------------------------
+
+constexpr int kDistillMaxTop = 256;      // a thread per place
+constexpr int kDistillStats = 8;         // numbers of a row that the gradient takes from the forward call
+
+struct DistillArgs {
+    const void* logits[kMaxRanks];       // [rows][ld]
+    float* loss[kMaxRanks];              // [rows]
+    float* stats[kMaxRanks];             // [rows][kDistillStats] or null
+    const float* stats_in[kMaxRanks];    // gradient
+    void* grad_logits[kMaxRanks];        // gradient: [rows][ld_grad]
+    const int32_t* top_idx;              // [rows][n]
+    const float* top_value;              // [rows][n]
+    const float* grad_loss;              // gradient: [rows]
+    int p, view_rank, n, tail;
+    int parts;                           // CTAs per row
+    float inv_temperature;
+    size_t rows, V, m, ld, ld_grad;
+    float2* part_stat;                   // scratch: [rows][parts] maximum and sum
+    DevState* st;
+    Ctl ctl;
+};
+
 // ---- HBM access-pattern probes (not collectives) --------------------------------------------------
 enum ProbeKind { PROBE_LOAD = 0, PROBE_STORE = 1, PROBE_COPY = 2, PROBE_BULK_STORE = 3, PROBE_BULK_FANOUT = 4 };
 constexpr int kProbeFanCopies = 8;  // PROBE_BULK_FANOUT writes this many copies of src
@@ -358,6 +443,14 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_moe_layer(const MoeLayerArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_logprobs_grad(const LogprobArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s);
+int rmsnorm_grad_ctas(size_t rows, int num_sms);
+cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, cudaStream_t s, int* kernels_launched);
+int adapter_splits(size_t tokens, size_t k, int segments, int num_sms);
+cudaError_t launch_adapters(const AdapterArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_adjust(const AdjustArgs& a, int dtype, int num_sms, cudaStream_t s);
+cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_probe(int kind, void* dst, const void* src, size_t bytes, int ctas_per_sm, int num_sms,
                          cudaStream_t s);
 

@@ -194,8 +194,9 @@ class RankComm(SC.SimComm):
 
     # The operators of a model's step take SimComm's arguments: tensors, lists in rank order. Of an array that the call
     # reads from every rank this rank's entry is a tensor (over its registered buffer) and the others registered
-    # pointers; of an array that is this rank's own the other entries are None. The router and its gradient and the
-    # column-parallel linear read no peer's memory and meet no barrier.
+    # pointers; of an array that is this rank's own the other entries are None. The router and its gradient, the
+    # column-parallel linear and adapters, the score adjustment and the gradient of the distillation read no peer's memory
+    # and meet no barrier.
     def linear_w4(self, x, w, scale, out, parallel="row", stream=None):
         """parallel "row": x, w and scale are every rank's (registered), out this rank's own."""
         if parallel == "column":
@@ -220,6 +221,29 @@ class RankComm(SC.SimComm):
         """logits are every rank's (registered), the other arrays this rank's own."""
         self._operator(super().logprobs_backward, logits, tokens, vocab, lse, grad_logprob, grad_logits,
                        entropy=entropy, grad_entropy=grad_entropy, stream=stream)
+
+    def rmsnorm(self, x, weight, eps, out=None, residual=None, total=None, q=None, scale=None, stream=None):
+        """x are every rank's (registered), the outputs this rank's own."""
+        self._operator(super().rmsnorm, x, weight, eps, out=out, residual=residual, total=total, q=q, scale=scale,
+                       stream=stream)
+
+    def rmsnorm_backward(self, grad_out, h, weight, eps, grad_x, grad_total=None, grad_weight=None, stream=None):
+        """grad_out are every rank's (registered), the outputs this rank's own."""
+        self._operator(super().rmsnorm_backward, grad_out, h, weight, eps, grad_x, grad_total=grad_total,
+                       grad_weight=grad_weight, stream=stream)
+
+    def adapters(self, x, adapter, a, b, out, base=None, rank=None, scale=None, parallel="row", stream=None):
+        """parallel "row": x and a are every rank's (registered), b, base and out this rank's own."""
+        if parallel == "column":
+            super().adapters(x, adapter, a, b, out, base=base, rank=rank, scale=scale, parallel=parallel, stream=stream)
+        else:
+            self._operator(super().adapters, x, adapter, a, b, out, base=base, rank=rank, scale=scale, parallel=parallel,
+                           stream=stream)
+
+    def distill(self, logits, vocab, top_idx, top_value, loss, stats=None, temperature=1.0, tail=False, stream=None):
+        """logits are every rank's (registered), the outputs this rank's own."""
+        self._operator(super().distill, logits, vocab, top_idx, top_value, loss, stats=stats, temperature=temperature,
+                       tail=tail, stream=stream)
 
     def _operator(self, fn, *args, stream, **kw):
         """_call on the caller's stream: complete on every rank before the call and after it."""

@@ -41,6 +41,15 @@ class IpcHandle(ctypes.Structure):
     _fields_ = [("reserved", ctypes.c_ubyte * 64)]
 
 
+class LogitRules(ctypes.Structure):
+    """coll_logit_rules_t: what adjust_logits changes."""
+    _fields_ = [("history", ctypes.c_void_p), ("ld_history", ctypes.c_size_t), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("bias_start", ctypes.c_void_p), ("bias_token", ctypes.c_void_p),
+                ("bias_value", ctypes.c_void_p), ("bias_count", ctypes.c_size_t), ("mask", ctypes.c_void_p),
+                ("ld_mask", ctypes.c_size_t), ("mask_rows", ctypes.c_size_t), ("mask_row", ctypes.c_void_p)]
+
+
 class TraceRecord(ctypes.Structure):
     """sim_comm_trace_record_t: one traced call."""
     _fields_ = [("seq", ctypes.c_ulonglong), ("coll", ctypes.c_char_p), ("p", ctypes.c_int), ("dtype", ctypes.c_int),
@@ -115,8 +124,16 @@ def load_library(path=LIB_PATH):
     L.coll_moe_layer.argtypes = [vp, pa, pa, pa, pa, sz, i32, sz, sz, i32, i32, i32, pa, pa, pa, pa, i32, pa, vp]
     L.coll_logprobs.argtypes = [vp, pa, sz, vp, sz, sz, i32, pa, pa, pa, i32, pa, pa, vp]
     L.coll_logprobs_backward.argtypes = [vp, pa, sz, vp, sz, sz, i32, pa, pa, vp, vp, pa, sz, vp]
+    f32 = ctypes.c_float
+    L.coll_rmsnorm.argtypes = [vp, pa, vp, vp, sz, sz, f32, i32, pa, pa, pa, pa, i32, vp]
+    L.coll_rmsnorm_backward.argtypes = [vp, pa, vp, vp, vp, sz, sz, f32, i32, pa, pa, vp]
+    L.coll_adapters.argtypes = [vp, pa, vp, pa, pa, vp, vp, i32, i32, sz, sz, sz, i32, pa, i32, i32, pa, vp]
+    L.coll_adjust_logits.argtypes = [vp, pa, sz, sz, sz, i32, ctypes.POINTER(LogitRules), pa, sz, vp]
+    L.coll_distill.argtypes = [vp, pa, sz, vp, vp, i32, sz, sz, i32, f32, i32, pa, pa, vp]
+    L.coll_distill_backward.argtypes = [vp, pa, sz, vp, vp, i32, sz, sz, i32, f32, i32, pa, vp, pa, sz, vp]
     for name in ("coll_moe_route", "coll_moe_route_backward", "coll_linear_w4", "coll_moe_layer", "coll_logprobs",
-                 "coll_logprobs_backward"):
+                 "coll_logprobs_backward", "coll_rmsnorm", "coll_rmsnorm_backward", "coll_adapters",
+                 "coll_adjust_logits", "coll_distill", "coll_distill_backward"):
         getattr(L, name).restype = st
     for name in ("coll_allreduce", "coll_reduce", "coll_broadcast", "coll_reduce_scatter", "coll_allgather",
                  "coll_alltoall", "coll_alltoallv", "coll_scatter", "coll_gather", "coll_allreduce_ring_noalloc",
@@ -388,6 +405,17 @@ class SimComm:
             raise ValueError(f"{what}: {len(out)} entries for {self.p} ranks")
         return self._pack(*out)
 
+    def _one(self, what, t, dtype, shape):
+        """The address of a single tensor that all ranks read, checked as by _tensors (None stays None)."""
+        if t is None:
+            return None
+        try:  # the usual call; anything else takes the slow way, which says what is wrong
+            if t.dtype is dtype and t.shape == shape and t.get_device() == self._device and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        return self._tensors(what, t, dtype, shape, one=True)
+
     def _launch_stream(self, stream):
         """The stream's handle; by default the current stream of the communicator's device."""
         if stream is None:
@@ -518,6 +546,154 @@ class SimComm:
             self._tensors("lse", lse, f, R), self._tensors("entropy", entropy, f, R),
             self._tensors("grad_logprob", grad_logprob, f, R, one=True),
             None if grad_entropy is None else self._tensors("grad_entropy", grad_entropy, f, R, one=True),
+            self._tensors("grad_logits", grad_logits, x.dtype, (R, m), row=(ldg, m)), ldg, self._launch_stream(stream)))
+
+    # -- norm, adapters, score adjustment, distillation ----------------------------------------------
+    def rmsnorm(self, x, weight, eps, out=None, residual=None, total=None, q=None, scale=None, stream=None):
+        """h = sum of the ranks' rows x[r] [T][H] + residual [T][H] (one tensor) into total[r], its root-mean-square norm
+        h * weight / sqrt(mean h^2 + eps) into out[r], or in 8 bits into q[r] (float8_e4m3fn or uint8 [T][H]) with
+        scale[r] fp32 [T][H / group], as many columns to a scale as its shape says. Rows fp32 or bf16, one type; weight
+        [H]. Every rank gets every output; at least one is given. residual may be one of total's tensors."""
+        torch = self._torch
+        t = self._own(x)
+        T, H = t.shape
+        dt, group, q_ptr, s_ptr = t.dtype, 0, None, None
+        if (q is None) != (scale is None):
+            raise ValueError("q and scale go together")
+        if q is not None:
+            groups = self._own(scale).shape[1]
+            if groups < 1 or H % groups:
+                raise ValueError(f"scale: {groups} groups do not divide rows of {H}")
+            group = H // groups
+            kind = self._own(q).dtype
+            if kind is not torch.uint8 and kind is not torch.float8_e4m3fn:
+                raise TypeError(f"q: {kind}, not float8_e4m3fn or uint8")
+            q_ptr = self._tensors("q", q, kind, (T, H))
+            s_ptr = self._tensors("scale", scale, torch.float32, (T, groups))
+        self._check(self._L.coll_rmsnorm(
+            self._h, self._tensors("x", x, dt, (T, H)), self._one("residual", residual, dt, (T, H)),
+            self._one("weight", weight, dt, (H,)), T, H, eps, DTYPES[_dtype_of(t)], self._tensors("total", total, dt, (T, H)),
+            self._tensors("out", out, dt, (T, H)), q_ptr, s_ptr, group, self._launch_stream(stream)))
+
+    def rmsnorm_backward(self, grad_out, h, weight, eps, grad_x, grad_total=None, grad_weight=None, stream=None):
+        """Gradient of rmsnorm at the rows h [T][H] (one tensor: the forward call's total) from the ranks' gradients
+        grad_out[r] [T][H], which are summed: into grad_x[r] [T][H], plus grad_total [T][H] (one tensor: the gradient that
+        reaches total past the norm), and into grad_weight[r] fp32 [H]."""
+        torch = self._torch
+        t = self._own(grad_out)
+        T, H = t.shape
+        dt = t.dtype
+        self._check(self._L.coll_rmsnorm_backward(
+            self._h, self._tensors("grad_out", grad_out, dt, (T, H)), self._one("h", h, dt, (T, H)),
+            self._one("weight", weight, dt, (H,)), self._one("grad_total", grad_total, dt, (T, H)), T, H, eps,
+            DTYPES[_dtype_of(t)], self._tensors("grad_x", grad_x, dt, (T, H)),
+            self._tensors("grad_weight", grad_weight, torch.float32, (H,)), self._launch_stream(stream)))
+
+    def adapters(self, x, adapter, a, b, out, base=None, rank=None, scale=None, parallel="row", stream=None):
+        """out[t] = base[t] + scale[e] * B_e (A_e x[t]) with e = adapter[t] (int32 [T], one tensor, -1: none): many
+        requests' low-rank adapters beside a shared projection. x[r] bf16 [T][K_r], a[r] bf16 [adapters][R][K_r], b[r]
+        bf16 [adapters][N_r][R]; parallel "column": the ranks have all of x and a and rows of every B, "row": columns of
+        x and of every A, whose products are summed, and all of b. base[r] (fp32 or bf16, may be out[r]) and out[r]
+        [T][N_r]. rank int32 and scale fp32 [adapters], one tensor each: how much of R an adapter has, its factor."""
+        torch = self._torch
+        if parallel not in PARALLEL:
+            raise ValueError(f"parallel must be one of {sorted(PARALLEL)}")
+        bf = torch.bfloat16
+        o = self._own(out)
+        T, K = self._own(x).shape
+        S, R = self._own(a).shape[:2]
+        N = o.shape[1]
+        row = parallel == "row"
+        bt = o if base is None else self._own(base)
+        self._check(self._L.coll_adapters(
+            self._h, self._tensors("x", x, bf, (T, K)), self._one("adapter", adapter, torch.int32, (T,)),
+            self._tensors("a", a, bf, (S, R, K)), self._tensors("b", b, bf, (S, N, R)),
+            self._one("rank", rank, torch.int32, (S,)), self._one("scale", scale, torch.float32, (S,)), S, R, T,
+            N if row else N * self.p, K * self.p if row else K, PARALLEL[parallel],
+            self._tensors("base", base, bt.dtype, (T, N)), DTYPES[_dtype_of(bt)], DTYPES[_dtype_of(o)],
+            self._tensors("out", out, o.dtype, (T, N)), self._launch_stream(stream)))
+
+    def adjust_logits(self, logits, vocab, out, history=None, history_len=None, prompt_len=None, repetition=None,
+                      frequency=None, presence=None, bias_start=None, bias_token=None, bias_value=None, mask=None,
+                      mask_row=None, stream=None):
+        """Penalties for repeated tokens, biases and masks on rows of scores whose `vocab` columns are sharded over the
+        ranks: logits[r] [R][m] (as in logprobs) into out[r] of the same type, which may be logits[r]. One tensor each:
+        history int32 [R][L] with history_len and prompt_len int32 [R], the penalties fp32 [R]; bias_start int32 [R + 1],
+        bias_token int32 and bias_value fp32 [n]; mask int32 [M][words], a bit for each allowed token, with mask_row int32
+        [R] (-1: none)."""
+        torch = self._torch
+        x, o = self._own(logits), self._own(out)
+        R, m = x.shape
+        if m != -(-int(vocab) // self.p):
+            raise ValueError(f"logits: {m} columns per rank for a vocabulary of {vocab} on {self.p} ranks")
+        ld, ld_out = (x.stride(0), o.stride(0)) if R > 1 else (m, m)
+        f, i = torch.float32, torch.int32
+        if (history is None) != (history_len is None):
+            raise ValueError("history and history_len go together")
+        if history is None and any(v is not None for v in (prompt_len, repetition, frequency, presence)):
+            raise ValueError("the penalties need history")
+        if len({bias_start is None, bias_token is None, bias_value is None}) > 1:
+            raise ValueError("bias_start, bias_token and bias_value go together")
+        if mask is None and mask_row is not None:
+            raise ValueError("mask_row needs mask")
+        u = LogitRules()
+        if history is not None:
+            u.ld_history = history.shape[1]
+            u.history = self._one("history", history, i, (R, history.shape[1]))
+            u.history_len = self._one("history_len", history_len, i, (R,))
+            u.prompt_len = self._one("prompt_len", prompt_len, i, (R,))
+            u.repetition = self._one("repetition", repetition, f, (R,))
+            u.frequency = self._one("frequency", frequency, f, (R,))
+            u.presence = self._one("presence", presence, f, (R,))
+        if bias_start is not None:
+            u.bias_count = n = bias_token.shape[0]
+            u.bias_start = self._one("bias_start", bias_start, i, (R + 1,))
+            u.bias_token = self._one("bias_token", bias_token, i, (n,))
+            u.bias_value = self._one("bias_value", bias_value, f, (n,))
+        if mask is not None:
+            u.mask_rows, u.ld_mask = mask.shape
+            u.mask = self._one("mask", mask, i, mask.shape)
+            u.mask_row = self._one("mask_row", mask_row, i, (R,))
+        self._check(self._L.coll_adjust_logits(
+            self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld, R, int(vocab),
+            DTYPES[_dtype_of(x)], ctypes.byref(u), self._tensors("out", out, x.dtype, (R, m), row=(ld_out, m)), ld_out,
+            self._launch_stream(stream)))
+
+    def distill(self, logits, vocab, top_idx, top_value, loss, stats=None, temperature=1.0, tail=False, stream=None):
+        """Loss of rows of scores, sharded as in logprobs, against a teacher's best columns top_idx int32 [R][n] (-1: not
+        given) with top_value fp32 [R][n], one tensor each: sum of q (ln q - ln P), q the softmax of top_value /
+        temperature and P that of the scores / temperature; with `tail`, top_value are log probabilities (logprobs'
+        top_logprob) and the other columns together one more class. Every rank gets loss[r] fp32 [R] and, for the
+        gradient, stats[r] fp32 [R][8]."""
+        torch = self._torch
+        x = self._own(logits)
+        R, m = x.shape
+        if m != -(-int(vocab) // self.p):
+            raise ValueError(f"logits: {m} columns per rank for a vocabulary of {vocab} on {self.p} ranks")
+        ld = x.stride(0) if R > 1 else m
+        n, f = top_idx.shape[1], torch.float32
+        self._check(self._L.coll_distill(
+            self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld,
+            self._one("top_idx", top_idx, torch.int32, (R, n)), self._one("top_value", top_value, f, (R, n)), n, R,
+            int(vocab), DTYPES[_dtype_of(x)], temperature, 1 if tail else 0, self._tensors("loss", loss, f, (R,)),
+            self._tensors("stats", stats, f, (R, 8)), self._launch_stream(stream)))
+
+    def distill_backward(self, logits, vocab, top_idx, top_value, stats, grad_loss, grad_logits, temperature=1.0,
+                         tail=False, stream=None):
+        """Gradient of distill's scores into grad_logits[r] [R][m] (of the scores' type, zeros in padding columns), from
+        grad_loss fp32 [R] (one tensor) and the forward call's stats[r]."""
+        torch = self._torch
+        x, g = self._own(logits), self._own(grad_logits)
+        R, m = x.shape
+        if m != -(-int(vocab) // self.p):
+            raise ValueError(f"logits: {m} columns per rank for a vocabulary of {vocab} on {self.p} ranks")
+        ld, ldg = (x.stride(0), g.stride(0)) if R > 1 else (m, m)
+        n, f = top_idx.shape[1], torch.float32
+        self._check(self._L.coll_distill_backward(
+            self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld,
+            self._one("top_idx", top_idx, torch.int32, (R, n)), self._one("top_value", top_value, f, (R, n)), n, R,
+            int(vocab), DTYPES[_dtype_of(x)], temperature, 1 if tail else 0, self._tensors("stats", stats, f, (R, 8)),
+            self._one("grad_loss", grad_loss, f, (R,)),
             self._tensors("grad_logits", grad_logits, x.dtype, (R, m), row=(ldg, m)), ldg, self._launch_stream(stream)))
 
 

@@ -53,7 +53,8 @@
  *     bounded device wait ran out: a ring, tree or butterfly step for its predecessor, an LL word,
  *     a bulk copy), COLL_ERR_ABORTED (sim_comm_abort was called while such a wait was running),
  *     COLL_ERR_OVERFLOW (an All-to-Allv count or an MoE dispatch exceeds a capacity; nothing is
- *     copied), COLL_ERR_INVALID_ARG (an MoE expert id, routing-map entry or given token out of range),
+ *     copied), COLL_ERR_INVALID_ARG (an MoE expert id, routing-map entry, given token or another index that an
+ *     operator reads on the device out of range),
  *     COLL_ERR_INTERNAL (an invariant check failed). Collectives are not transactions: after an
  *     asynchronous error the outputs of the failed call are unspecified, and later calls do no
  *     work until sim_comm_reset ([Primer] "Collective 的故障语义不是事务").
@@ -145,7 +146,8 @@ sim_comm_t sim_comm_create(int p);
  * send_cap and recv_cap: every rank's capacities; only this rank's blocks are copied), Scatter,
  * Gather, COLL_ALGO_DIRECT only (the other schedules wait on other ranks inside their kernels:
  * COLL_ERR_UNSUPPORTED), the MoE dispatch (fused kernel only) and combine, the router, the 4-bit linear,
- * the expert layer, the log probabilities and the gradients (see there; the expert layer's sums may be
+ * the expert layer, the log probabilities, the norm, the adapters, the score adjustment, the distillation and the
+ * gradients (see there; the expert layer's sums may be
  * split otherwise than the whole communicator's, by the view's number of assignments).
  * Reduce and Gather enqueue nothing
  * on a non-root rank. No output may overlap any rank's input (a peer may still be reading it), except
@@ -263,15 +265,15 @@ coll_status_t sim_comm_launch_count(sim_comm_t comm, unsigned long long* out);
  * call's first kernel and one just after its last. */
 typedef struct {
     unsigned long long seq;   /* number of the call among the traced calls of this communicator */
-    const char* coll;         /* "allreduce", "reduce", ..., "logprobs_backward" (a static string) */
+    const char* coll;         /* "allreduce", "reduce", ..., "distill_backward" (a static string) */
     int p;                    /* ranks */
     int dtype;                /* coll_dtype_t */
     int op;                   /* coll_op_t, or -1 where the call takes none */
     int root;                 /* root rank, or -1 where the call takes none */
     int algo;                 /* coll_algo_t, or -1 where the call takes none */
     int status;               /* coll_status_t the call returned (asynchronous errors are not here) */
-    unsigned long long n;     /* element count as passed; tokens for the MoE calls and the 4-bit
-                                 linear, rows for the log probabilities; 0 for All-to-Allv, whose
+    unsigned long long n;     /* element count as passed; tokens for the MoE calls, the 4-bit
+                                 linear and the adapters, rows for the other operators; 0 for All-to-Allv, whose
                                  counts stay on the device */
     unsigned int launches;    /* kernels the call enqueued */
     float device_ms;          /* time between the two events; -1 when the call launched nothing or its
@@ -534,6 +536,160 @@ coll_status_t coll_logprobs_backward(sim_comm_t comm, const void* const* logits,
                                      size_t rows, size_t vocab, coll_dtype_t dtype, const float* const* lse,
                                      const float* const* entropy, const float* grad_logprob, const float* grad_entropy,
                                      void* const* grad_logits, size_t ld_grad, coll_stream_t stream);
+
+/* ---- root-mean-square norm of rows that lie on the ranks as partial sums -------------------------- */
+
+/* What stands between a row-parallel product and the next one, in one pass: the AllReduce of the ranks' partial
+ * rows, the residual's addition and the root-mean-square norm, if asked with 8-bit rows.
+ *   h[t] = sum_q x[q][t] + residual[t]                        (fp32, rank order, the residual last)
+ *   y[t][i] = h[t][i] weight[i] / sqrt(mean_j h[t][j]^2 + eps)
+ *   x         HOST array of p DEVICE pointers, [T][H] partial rows.
+ *   residual  DEVICE [T][H], the one copy that is read (Replicated), or NULL: none. It may be the very buffer
+ *             total[r] of one rank (in place).
+ *   weight    DEVICE [H], the one copy that is read.
+ *   dtype     of x, residual, weight, total and out: fp32 or bf16 (int32: COLL_ERR_UNSUPPORTED).
+ *   total     HOST array of p DEVICE pointers, output h [T][H], rounded once, or NULL. The norm is of the unrounded h.
+ *   out       HOST array of p DEVICE pointers, output y [T][H], rounded once, or NULL.
+ *   q, scale  HOST arrays of p DEVICE pointers, or both NULL: y in 8 bits (e4m3: 4 bits of exponent, 3 of mantissa, no
+ *             infinities) [T][H] and fp32 scales [T][H / group]; q stands for q * scale. Per `group` columns scale =
+ *             max |y| / 448, at least 2^-126 (0 where all are 0), q = the nearest of y / scale. A NaN among the
+ *             columns makes the scale and their q NaN.
+ *   group     H, or a power of two, 32 or more, that divides H (ignored without q).
+ * Every rank gets every output. At least one of total, out and q is given. eps is finite and at least 2^-126; h whose
+ * squares pass fp32 are summed scaled. H in [1, 2^24]. No output may overlap another buffer but as said. T = 0
+ * enqueues nothing. On a rank view x holds every rank's rows as this process maps them, the outputs this rank's entry. */
+coll_status_t coll_rmsnorm(sim_comm_t comm, const void* const* x, const void* residual, const void* weight, size_t rows,
+                           size_t hidden, float eps, coll_dtype_t dtype, void* const* total, void* const* out,
+                           uint8_t* const* q, float* const* scale, int group, coll_stream_t stream);
+
+/* Gradient of the norm at h, the total that the forward call stored (or any rows):
+ *   g = sum_q grad_out[q]  (the column-parallel products behind the norm leave partial sums on the ranks: their AllReduce)
+ *   u = h / sqrt(mean h^2 + eps),  grad_x = (weight g - u mean(weight g u)) / sqrt(mean h^2 + eps) + grad_total
+ *   grad_weight[i] = sum_t g[t][i] u[t][i]
+ *   grad_out     HOST array of p DEVICE pointers, [T][H].
+ *   h            DEVICE [T][H], the one copy that is read.     weight  DEVICE [H].
+ *   grad_total   DEVICE [T][H], what reaches total past the norm, the one copy that is read, or NULL: none.
+ *   grad_x       HOST array of p DEVICE pointers, output [T][H], rounded once: the gradient of every rank's x and of
+ *                the residual alike.
+ *   grad_weight  HOST array of p DEVICE pointers, output fp32 [H], or NULL. Written, not added to.
+ * Sums over the rows run in a fixed order. Other arguments and refusals as above; T = 0 enqueues nothing (grad_weight is
+ * left as it was). On a rank view grad_out holds every rank's rows, the outputs this rank's entry. */
+coll_status_t coll_rmsnorm_backward(sim_comm_t comm, const void* const* grad_out, const void* h, const void* weight,
+                                    const void* grad_total, size_t rows, size_t hidden, float eps, coll_dtype_t dtype,
+                                    void* const* grad_x, float* const* grad_weight, coll_stream_t stream);
+
+/* ---- low-rank adapters of many requests -------------------------------------------------------- */
+
+/* What the requests' own low-rank adapters add to a shared projection (coll_linear_w4 or any other): with e =
+ * adapter[t] the adapter of token t's request,
+ *   out[t] = base[t] + scale[e] * B_e (A_e x[t]),   A_e [R][K], B_e [N][R]
+ * COLUMN: every rank has x [T][K] and all of A, and rows [r N/p, (r+1) N/p) of B; base and out are [T][N/p].
+ * ROW:    rank r has columns [r K/p, (r+1) K/p) of x and of A, and all of B; the partial A x are summed over the ranks
+ *         (the AllReduce, of R numbers to a token) and base and out are [T][N] on every rank.
+ *   x        HOST array of p DEVICE pointers, bf16 [T][K] (COLUMN, of which one copy is read) or [T][K/p] (ROW).
+ *   adapter  DEVICE int32 [T], the one array all ranks read: -1 or an adapter in [0, adapters). -1: out = base.
+ *   a        HOST array of p DEVICE pointers, bf16 [adapters][max_rank][K] (COLUMN, one copy is read) or [...][K/p] (ROW).
+ *   b        HOST array of p DEVICE pointers, bf16 [adapters][N/p][max_rank] (COLUMN) or [adapters][N][max_rank] (ROW, of
+ *            which one copy is read).
+ *   rank     DEVICE int32 [adapters] in [0, max_rank], or NULL: max_rank for all. Adapter e is the first rank[e] rows of
+ *            A and columns of B; the others are not read as numbers.
+ *   scale    DEVICE fp32 [adapters], or NULL: 1.
+ *   base     HOST array of p DEVICE pointers of base_dtype, or NULL: 0. base[r] may be out[r] when the types are equal.
+ *   base_dtype, dtype  types of base and of out: fp32 or bf16 (int32: COLL_ERR_UNSUPPORTED).
+ * max_rank in [1, 256], adapters in [1, 2^24], n divisible by p (COLUMN) or k by p (ROW), n and k at most 2^24, tokens
+ * at most 2^31 - 1. Sums are fp32; A x goes into the second product in two bf16 parts (2^-16 of it is lost); one rounding
+ * to out's type. A token's result does not depend on the other tokens of a call of the same size. An adapter or rank out of range is
+ * reported asynchronously as COLL_ERR_INVALID_ARG. Tokens of one request that follow each other share its matrices'
+ * loads. No output may overlap another buffer but as said. T = 0 or n = 0 enqueues nothing. On a rank view COLUMN uses
+ * this rank's entries only; ROW reads every rank's x and a as this process maps them and this rank's b, base and out. */
+coll_status_t coll_adapters(sim_comm_t comm, const void* const* x, const int32_t* adapter, const void* const* a,
+                            const void* const* b, const int32_t* rank, const float* scale, int adapters, int max_rank,
+                            size_t tokens, size_t n, size_t k, coll_parallel_t parallel, const void* const* base,
+                            coll_dtype_t base_dtype, coll_dtype_t dtype, void* const* out, coll_stream_t stream);
+
+/* ---- penalties, biases and masks on sharded scores --------------------------------------------- */
+
+/* What changes a row's scores before a token is picked. All arrays are DEVICE arrays, the one copy that all ranks read;
+ * a NULL one (and a NULL history_len, bias_start or mask) leaves its rule out.
+ *   history      int32 [rows][ld_history] the tokens of row t's request so far, history_len[t] of them (int32, in [0,
+ *                ld_history]); the first prompt_len[t] (in [0, history_len[t]]; NULL: 0) are its prompt. -1: no token.
+ *   repetition   fp32 [rows]: a score x of a token that occurs becomes x / repetition where x > 0, else x * repetition.
+ *   frequency, presence  fp32 [rows]: a token that occurs c > 0 times behind the prompt loses frequency * c and presence.
+ *   bias_start   int32 [rows + 1], rising, in [0, bias_count]: row t's biases are entries [bias_start[t],
+ *                bias_start[t + 1]) of bias_token (int32, -1: none) and bias_value (fp32), added to the tokens' scores. Of entries
+ *                of one row with the same token the last one counts.
+ *   mask         uint32 [mask_rows][ld_mask], ld_mask >= ceil(vocab / 32): bit v % 32 of word v / 32 tells whether token v
+ *                is allowed; other scores become -inf, whatever they were. Row t uses row mask_row[t] (int32; -1: none),
+ *                or, with mask_row NULL, row t (mask_rows >= rows then). */
+typedef struct {
+    const int32_t* history;
+    size_t ld_history;
+    const int32_t* history_len;
+    const int32_t* prompt_len;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_start;
+    const int32_t* bias_token;
+    const float* bias_value;
+    size_t bias_count;
+    const uint32_t* mask;
+    size_t ld_mask;
+    size_t mask_rows;
+    const int32_t* mask_row;
+} coll_logit_rules_t;
+
+/* Penalties for repeated tokens, biases and masks, in this order, on rows of scores whose V columns are on the ranks as
+ * coll_logprobs takes them (and coll_linear_w4's COLUMN form leaves them): out[r][t][c] from logits[r][t][c].
+ *   logits    HOST array of p DEVICE pointers, [rows][ld], m = ceil(V / p) columns used, fp32 or bf16.
+ *   rules     HOST struct, read during the call; the arrays it names are read when the kernel runs.
+ *   out       HOST array of p DEVICE pointers, [rows][ld_out] of the scores' type. out[r] may be logits[r] with ld_out =
+ *             ld (in place: then only what changes is written); no other overlap. Columns past the shard's own
+ *             (padding) are not written.
+ * Computed in fp32, rounded once; scores that no rule touches keep their bits. A token, length, start or mask row out of
+ * range is reported asynchronously as COLL_ERR_INVALID_ARG. V in [1, 2^31), ld_history at most 2^31 - 1. rows = 0 enqueues
+ * nothing. On a rank view only this rank's entries are used. */
+coll_status_t coll_adjust_logits(sim_comm_t comm, const void* const* logits, size_t ld, size_t rows, size_t vocab,
+                                 coll_dtype_t dtype, const coll_logit_rules_t* rules, void* const* out, size_t ld_out,
+                                 coll_stream_t stream);
+
+/* ---- distillation over a sharded vocabulary ----------------------------------------------------- */
+
+/* Loss of rows of scores x, their V columns on the ranks as coll_logprobs takes them, against a teacher's best columns:
+ * with P = softmax(x / temperature) over all columns,
+ *   tail = 0:  q = softmax(top_value / temperature) over the row's given places;  loss = sum_i q_i (ln q_i - ln P_i)
+ *   tail = 1:  q = e^top_value (log probabilities, as coll_logprobs' top_logprob), and all other columns are one more
+ *              class, of Q = 1 - sum_i q_i and P_rest = sum of their P: loss as above + Q (ln Q - ln P_rest). A Q below
+ *              2^-20, where rounding of the q_i decides, counts as 0. temperature must be 1.
+ *   top_idx      DEVICE int32 [rows][top_n], the one array all ranks read: columns, -1: the place is not given (what
+ *                coll_logprobs leaves there).      top_value  DEVICE fp32 [rows][top_n].
+ *   top_n        in [1, 256].     temperature  in [2^-126, 2^126].
+ *   loss         HOST array of p DEVICE pointers, output fp32 [rows] (Replicated).
+ *   stats        HOST array of p DEVICE pointers, output fp32 [rows][8], what the backward call reads, or NULL.
+ * A place of -inf has q = 0. With tail = 0 a row without a given place above -inf has no teacher: its loss is 0, whatever
+ * its scores. A column that occurs twice counts for each of its places, and once in the
+ * probabilities. q > 0 where P is 0 makes the loss +inf; NaN or +inf among a row's scores makes it NaN, likewise a
+ * NaN among its given values. Scores fp32 or bf16, computed in fp32. A column outside [-1, V) is reported asynchronously as
+ * COLL_ERR_INVALID_ARG. No output may overlap another buffer. rows = 0 enqueues nothing. On a rank view logits holds
+ * every rank's buffers as this process maps them, the outputs this rank's entry. */
+coll_status_t coll_distill(sim_comm_t comm, const void* const* logits, size_t ld, const int32_t* top_idx,
+                           const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dtype,
+                           float temperature, int tail, float* const* loss, float* const* stats, coll_stream_t stream);
+
+/* Gradient of coll_distill's scores from the gradient g of its loss:
+ *   grad_logits[r][t][c] = g[t] / temperature * (P[v] A - q[v]),  v = r m + c,  A = sum_i q_i + Q (without Q: sum_i q_i),
+ * q[v] the sum over the places of column v; with tail, columns without a place have P[v] (A - Q / P_rest). For the shard's m
+ * columns, 0 in padding columns and throughout rows without a teacher or of nothing but -inf.
+ *   logits, ld, top_idx, top_value, top_n, rows, vocab, dtype, temperature, tail  as in the forward call, unchanged since.
+ *   stats        HOST array of p DEVICE pointers: the forward call's output.
+ *   grad_loss    DEVICE fp32 [rows].
+ *   grad_logits  HOST array of p DEVICE pointers, output [rows][ld_grad] of the scores' type, ld_grad >= m; columns past m
+ *                are left untouched. Never in place.
+ * On a rank view only this rank's entries are used. */
+coll_status_t coll_distill_backward(sim_comm_t comm, const void* const* logits, size_t ld, const int32_t* top_idx,
+                                    const float* top_value, int top_n, size_t rows, size_t vocab, coll_dtype_t dtype,
+                                    float temperature, int tail, const float* const* stats, const float* grad_loss,
+                                    void* const* grad_logits, size_t ld_grad, coll_stream_t stream);
 
 /* ---- diagnostics ------------------------------------------------------------------------------ */
 
