@@ -2196,6 +2196,8 @@ static coll_status_t norm_common(sim_comm* c, const void* const* x, const void* 
     a.eps = eps;
     a.T = rows;
     a.H = hidden;
+    a.timeout_ns = uint64_t(c->timeout_ns);
+    a.fault_cta = int(c->fault_skip_rank);
     a.ctl = make_ctl(c);
     return COLL_OK;
 }
@@ -2210,10 +2212,8 @@ static coll_status_t coll_rmsnorm_impl(sim_comm_t c, const void* const* x, const
     if (st != COLL_OK) return st;
     if (!total && !out && !q) return fail(COLL_ERR_INVALID_ARG, "no output is given");
     if ((q == nullptr) != (scale == nullptr)) return fail(COLL_ERR_INVALID_ARG, "q and scale go together");
-    if (q && (group < 1 || size_t(group) != hidden)) {
-        int shift = 0;
-        if ((st = check_group(group, hidden, "hidden", &shift)) != COLL_OK) return st;
-    }
+    int shift = -1;
+    if (q && (group < 1 || size_t(group) != hidden) && (st = check_group(group, hidden, "hidden", &shift)) != COLL_OK) return st;
     if (rows == 0) return COLL_OK;
     const size_t d = dtype_bytes(dt), bytes = rows * hidden * d;
     bool vec = a.vec != 0 && aligned16(residual);
@@ -2251,8 +2251,9 @@ static coll_status_t coll_rmsnorm_impl(sim_comm_t c, const void* const* x, const
     a.has_out = out ? 1 : 0;
     a.has_q = q ? 1 : 0;
     a.group = q ? group : int(hidden);
+    a.shift = shift;
     a.vec = vec ? 1 : 0;
-    cudaError_t e = launch_rmsnorm(a, int(dt), static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_rmsnorm(a, int(dt), c->num_sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "norm launch");
     c->launches += 1;
     return COLL_OK;
@@ -2283,13 +2284,13 @@ static coll_status_t coll_rmsnorm_backward_impl(sim_comm_t c, const void* const*
     a.h = h;
     a.residual = grad_total;
     a.vec = vec ? 1 : 0;
-    a.ctas = rmsnorm_grad_ctas(rows, c->num_sms);
+    a.ctas = rmsnorm_grad_ctas(a, int(dt), c->num_sms);
     if (grad_weight) {
         if ((st = ensure_moe(c, size_t(a.ctas) * hidden * 4)) != COLL_OK) return st;
         a.part = reinterpret_cast<float*>(c->moe);
     }
     int launched = 0;
-    cudaError_t e = launch_rmsnorm_grad(a, int(dt), static_cast<cudaStream_t>(stream), &launched);
+    cudaError_t e = launch_rmsnorm_grad(a, int(dt), c->num_sms, static_cast<cudaStream_t>(stream), &launched);
     if (e != cudaSuccess) return cuda_fail(e, "norm gradient launch");
     c->launches += launched;
     return COLL_OK;

@@ -351,11 +351,13 @@ struct NormArgs {
     int p;
     int rank0, ranks;                    // ranks whose outputs the call writes
     int has_total, has_out, has_q;
-    int group;
+    int group, shift;                    // columns to a scale; log2 of them, -1: a whole row
     int vec;                             // rows of whole 16-byte units at aligned addresses
     int ctas;                            // backward: CTAs, each with every ctas-th row
     float eps;
     size_t T, H;
+    uint64_t timeout_ns;
+    int fault_cta;                       // fault injection: the copying warp of this CTA falls silent (-1: none)
     Ctl ctl;
 };
 
@@ -443,9 +445,9 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_moe_layer(const MoeLayerArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_logprobs(const LogprobArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_logprobs_grad(const LogprobArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s);
-int rmsnorm_grad_ctas(size_t rows, int num_sms);
-cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, cudaStream_t s, int* kernels_launched);
+cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, int num_sms, cudaStream_t s);
+int rmsnorm_grad_ctas(const NormArgs& a, int dtype, int num_sms);
+cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, int num_sms, cudaStream_t s, int* kernels_launched);
 int adapter_splits(size_t tokens, size_t k, int segments, int num_sms);
 cudaError_t launch_adapters(const AdapterArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_adjust(const AdjustArgs& a, int dtype, int num_sms, cudaStream_t s);

@@ -31,31 +31,45 @@ template <int DT, int L> struct Unit {
     using Raw = uint4;
     __device__ static Raw load(const void* base, size_t e) { return ld_stream_v4(static_cast<const char*>(base) + e * D); }
     __device__ static void unpack(const Raw& v, float (&a)[L]) { Pack16<DT>::unpack(v, a); }
-    __device__ static void store(void* base, size_t e, const float (&a)[L]) {
-        st_v4(static_cast<char*>(base) + e * D, Pack16<DT>::pack(a));
-    }
+    __device__ static Raw pack(const float (&a)[L]) { return Pack16<DT>::pack(a); }
+    __device__ static void store(void* base, size_t e, const Raw& v) { st_v4(static_cast<char*>(base) + e * D, v); }
 };
 template <int DT> struct Unit<DT, 1> {
     using Raw = float;
     __device__ static Raw load(const void* base, size_t e) { return load_elem<DT>(base, e); }
     __device__ static void unpack(const Raw& v, float (&a)[1]) { a[0] = v; }
-    __device__ static void store(void* base, size_t e, const float (&a)[1]) { store_elem<DT>(base, e, a[0]); }
+    __device__ static Raw pack(const float (&a)[1]) { return a[0]; }
+    __device__ static void store(void* base, size_t e, const Raw& v) { store_elem<DT>(base, e, v); }
 };
+// A unit to the same place of every rank's buffer.
+template <int DT, int L> __device__ __forceinline__ void store_all(const NormArgs& a, void* const (&to)[kMaxRanks], size_t e, const float (&v)[L]) {
+    const typename Unit<DT, L>::Raw raw = Unit<DT, L>::pack(v);
+#pragma unroll 4
+    for (int r = a.rank0; r < a.rank0 + a.ranks; ++r) Unit<DT, L>::store(to[r], e, raw);
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
 }
-// The CTA's sums of two values per thread, in a fixed order, the same for every thread. buf: 2 x 32, free to be
-// written again after another barrier.
-__device__ __forceinline__ float2 cta_sum2(float a, float b, float2* buf) {
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+// The n threads that compute (whole warps, from thread 0 on) meet; whether any of them is `bad`.
+__device__ __forceinline__ bool meet(int n, bool bad) {
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(any) : "r"(uint32_t(bad)), "r"(n) : "memory");
+    return any != 0u;
+}
+// Their sums of two values each, in a fixed order, the same for every thread. Rows that follow each other use two
+// buffers in turn: what a thread writes for one row the others have read two rows ago, before they met for the last one.
+__device__ __forceinline__ float2 cta_sum2(float a, float b, float2 (&buf)[32], int n, bool& bad) {
+    const int lane = threadIdx.x & 31;
     a = warp_sum(a);
     b = warp_sum(b);
     if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+    bad = meet(n, bad);
+    const float2 v = lane < n >> 5 ? buf[lane] : make_float2(0.0f, 0.0f);
     return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
@@ -72,21 +86,25 @@ __device__ __forceinline__ float over(float y, float scale) { return scale == 0.
 __device__ __forceinline__ uint8_t e4m3(float v) {
     return uint8_t(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
 }
-template <int L> __device__ __forceinline__ void store_q(uint8_t* p, const float (&v)[L]) {
-    if constexpr (L == 1) {
-        *p = e4m3(v[0]);
-    } else {
-        uint32_t w[L / 4];
-#pragma unroll
-        for (int i = 0; i < L / 4; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | (hi << 16);
-        }
-        if constexpr (L == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(p) = w[0];
-    }
+template <int L> struct Q8 {
+    using T = uint8_t;
+    __device__ static T pack(const float (&v)[1]) { return e4m3(v[0]); }
+};
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
 }
+template <> struct Q8<4> {
+    using T = uint32_t;
+    __device__ static T pack(const float (&v)[4]) { return e4m3x4(v[0], v[1], v[2], v[3]); }
+};
+template <> struct Q8<8> {
+    using T = uint2;
+    __device__ static T pack(const float (&v)[8]) {
+        return make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+    }
+};
 
 // The sum of all ranks' units, V of them per thread (unit v at element e0 + (v blockDim + tid) L), loads of as many ranks
 // in flight as registers allow.
@@ -104,14 +122,14 @@ __device__ __forceinline__ void sum_ranks(const NormArgs& a, size_t row, float (
         for (int j = 0; j < kAhead; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const size_t e = (size_t(v) * blockDim.x + threadIdx.x) * L;
+                const uint32_t e = (v * blockDim.x + threadIdx.x) * L;
                 if (q0 + j < a.p && e < a.H) raw[j][v] = U::load(a.x[q0 + j], row * a.H + e);
             }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const size_t e = (size_t(v) * blockDim.x + threadIdx.x) * L;
+                const uint32_t e = (v * blockDim.x + threadIdx.x) * L;
                 if (q0 + j < a.p && e < a.H) {
                     float x[L];
                     U::unpack(raw[j][v], x);
@@ -122,48 +140,36 @@ __device__ __forceinline__ void sum_ranks(const NormArgs& a, size_t row, float (
     }
 }
 
-template <int DT, int L, int V> __global__ void __launch_bounds__(V == 8 ? 1024 : 512)
-k_rmsnorm(const __grid_constant__ NormArgs a) {
+// What the rows of a CTA share; each array for two rows in turn.
+struct NormShared {
+    float2 sum[2][32], again[2][32];
+    uint32_t most[2][256];  // largest |y| of groups wider than a warp's units
+};
+
+// A row from its sum on: total, norm, 8 bits. w: the weight's units. n: threads that compute. False if any is bad.
+template <int DT, int L, int V>
+__device__ __forceinline__ bool finish_row(const NormArgs& a, size_t row, float (&h)[V][L], const typename Unit<DT, L>::Raw (&w)[V],
+                                           NormShared& s, int turn, int n, bool bad) {
     using U = Unit<DT, L>;
-    __shared__ float2 s_sum[32], s_again[32];
-    __shared__ uint32_t s_most[256];  // largest |y| of groups wider than a warp's units
-    const bool failed = status_failed(a.ctl);
-    const size_t row = blockIdx.x;
+    const auto at = [&](int v) { return (uint32_t(v) * n + threadIdx.x) * L; };
     // groups of fewer than 32 units are aligned lanes of one warp; in others a warp's 32 units, which start at a multiple of
     // 32 L, share a group
-    const bool narrow = a.has_q && size_t(a.group) < size_t(32 * L) && size_t(a.group) < a.H;
-    const bool whole = a.has_q && !narrow && size_t(a.group) == a.H;
+    const uint32_t H = uint32_t(a.H);
+    const bool whole = a.shift < 0, narrow = !whole && (1 << a.shift) < 32 * L;
     if (a.has_q && !narrow)
-        for (int i = threadIdx.x; i < 256; i += blockDim.x) s_most[i] = 0u;
-    float h[V][L], w[V][L];
-    const auto at = [&](int v) { return (size_t(v) * blockDim.x + threadIdx.x) * L; };
-    typename U::Raw res[V], wr[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (at(v) < a.H) {
-            if (a.residual) res[v] = U::load(a.residual, row * a.H + at(v));
-            if (a.has_out || a.has_q) wr[v] = U::load(a.weight, at(v));
-        }
-    sum_ranks<DT, L, V>(a, row, h);
-    if (__syncthreads_or(failed)) return;
+        for (int i = threadIdx.x; i < 256; i += n) s.most[turn][i] = 0u;
     float ss = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const bool in = at(v) < a.H;
-        if (in && a.residual) {
-            float x[L];
-            U::unpack(res[v], x);
-#pragma unroll
-            for (int l = 0; l < L; ++l) h[v][l] += x[l];
-        }
-        if (in && (a.has_out || a.has_q)) U::unpack(wr[v], w[v]);
+    for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int l = 0; l < L; ++l) ss += h[v][l] * h[v][l];
-        if (in && a.has_total)
-            for (int r = a.rank0; r < a.rank0 + a.ranks; ++r) U::store(a.total[r], row * a.H + at(v), h[v]);
-    }
-    if (!(a.has_out || a.has_q)) return;
-    ss = cta_sum2(ss, 0.0f, s_sum).x;
+    ss = cta_sum2(ss, 0.0f, s.sum[turn], n, bad).x;
+    if (bad) return false;
+    if (a.has_total)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (at(v) < H) store_all<DT, L>(a, a.total, row * a.H + at(v), h[v]);
+    if (!(a.has_out || a.has_q)) return true;
     float eps = a.eps;
     if (ss == INFINITY) {  // the same for every thread
         ss = 0.0f;
@@ -174,20 +180,22 @@ k_rmsnorm(const __grid_constant__ NormArgs a) {
                 h[v][l] *= kNormDown;
                 ss += h[v][l] * h[v][l];
             }
-        ss = cta_sum2(ss, 0.0f, s_again).x;
+        ss = cta_sum2(ss, 0.0f, s.again[turn], n, bad).x;
         eps = 0.0f;
     }
     const float r = 1.0f / sqrtf(ss / float(a.H) + eps);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+        float f[L];
+        if (at(v) < a.H) U::unpack(w[v], f);
 #pragma unroll
-        for (int l = 0; l < L; ++l) h[v][l] = at(v) < a.H ? h[v][l] * r * w[v][l] : 0.0f;
+        for (int l = 0; l < L; ++l) h[v][l] = at(v) < a.H ? h[v][l] * r * f[l] : 0.0f;
+    }
     if (a.has_out)
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (at(v) < a.H)
-                for (int r2 = a.rank0; r2 < a.rank0 + a.ranks; ++r2) U::store(a.out[r2], row * a.H + at(v), h[v]);
-    if (!a.has_q) return;
+            if (at(v) < H) store_all<DT, L>(a, a.out, row * a.H + at(v), h[v]);
+    if (!a.has_q) return true;
     uint32_t most[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -195,25 +203,247 @@ k_rmsnorm(const __grid_constant__ NormArgs a) {
 #pragma unroll
         for (int l = 0; l < L; ++l) most[v] = max(most[v], magnitude(h[v][l]));
         if (narrow) {
-            for (int d = a.group / L / 2; d > 0; d >>= 1) most[v] = max(most[v], __shfl_xor_sync(0xffffffffu, most[v], d));
+            for (int d = (1 << a.shift) / L / 2; d > 0; d >>= 1) most[v] = max(most[v], __shfl_xor_sync(0xffffffffu, most[v], d));
         } else {
             most[v] = __reduce_max_sync(0xffffffffu, most[v]);
-            if ((threadIdx.x & 31) == 0 && at(v) < a.H) atomicMax(&s_most[whole ? 0 : at(v) / a.group], most[v]);
+            if ((threadIdx.x & 31) == 0 && at(v) < H) atomicMax(&s.most[turn][whole ? 0 : at(v) >> a.shift], most[v]);
         }
     }
-    if (!narrow) __syncthreads();
+    if (!narrow) meet(n, false);
+    const uint32_t groups = whole ? 1u : H >> a.shift;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        if (at(v) >= a.H) continue;
-        const size_t g = whole ? 0 : at(v) / a.group;
-        const float scale = scale_of(__uint_as_float(narrow ? most[v] : s_most[g]));
+        if (at(v) >= H) continue;
+        const uint32_t g = whole ? 0u : at(v) >> a.shift;
+        const float scale = scale_of(__uint_as_float(narrow ? most[v] : s.most[turn][g]));
 #pragma unroll
         for (int l = 0; l < L; ++l) h[v][l] = over(h[v][l], scale);
-        const bool first = whole ? at(v) == 0 : at(v) % a.group == 0;
-        for (int r2 = a.rank0; r2 < a.rank0 + a.ranks; ++r2) {
-            store_q<L>(a.q[r2] + row * a.H + at(v), h[v]);
-            if (first) a.scale[r2][row * (a.H / a.group) + g] = scale;
+        const typename Q8<L>::T q = Q8<L>::pack(h[v]);
+#pragma unroll 4
+        for (int k = a.rank0; k < a.rank0 + a.ranks; ++k) *reinterpret_cast<typename Q8<L>::T*>(a.q[k] + row * a.H + at(v)) = q;
+        if (whole ? at(v) == 0 : (at(v) & ((1u << a.shift) - 1u)) == 0u)
+            for (int k = a.rank0; k < a.rank0 + a.ranks; ++k) a.scale[k][row * groups + g] = scale;
+    }
+    return true;
+}
+
+// A row's gradient, and its share of the weight's. False if any thread is bad.
+template <int DT, int L, int V>
+__device__ __forceinline__ bool finish_grad(const NormArgs& a, size_t row, float (&h)[V][L], const float (&g)[V][L],
+                                            const typename Unit<DT, L>::Raw (&past)[V], const float (&w)[V][L], float (&dw)[V][L],
+                                            NormShared& s, int turn, int n, bool bad) {
+    using U = Unit<DT, L>;
+    const auto at = [&](int v) { return (uint32_t(v) * n + threadIdx.x) * L; };
+    float ss = 0.0f, wgh = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            ss += h[v][l] * h[v][l];
+            wgh += w[v][l] * g[v][l] * h[v][l];
         }
+    float2 sums = cta_sum2(ss, wgh, s.sum[turn], n, bad);
+    if (bad) return false;
+    float eps = a.eps, down = 1.0f;
+    if (sums.x == INFINITY) {
+        down = kNormDown;
+        ss = wgh = eps = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int l = 0; l < L; ++l) {
+                h[v][l] *= down;
+                ss += h[v][l] * h[v][l];
+                wgh += w[v][l] * g[v][l] * h[v][l];
+            }
+        sums = cta_sum2(ss, wgh, s.again[turn], n, bad);
+    }
+    const float r = 1.0f / sqrtf(sums.x / float(a.H) + eps), along = sums.y * r / float(a.H);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float dx[L], add[L];
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+            const float u = h[v][l] * r;
+            dw[v][l] += g[v][l] * u;
+            dx[l] = (w[v][l] * g[v][l] - u * along) * (r * down);
+        }
+        if (at(v) >= a.H) continue;
+        if (a.residual) {
+            U::unpack(past[v], add);
+#pragma unroll
+            for (int l = 0; l < L; ++l) dx[l] += add[l];
+        }
+        store_all<DT, L>(a, a.out, row * a.H + at(v), dx);
+    }
+    return true;
+}
+
+// One row to a CTA, all its loads in registers.
+template <int DT, int L, int V> __global__ void __launch_bounds__(V == 8 || L == 1 ? 1024 : 512)
+k_rmsnorm(const __grid_constant__ NormArgs a) {
+    using U = Unit<DT, L>;
+    __shared__ NormShared s;
+    const bool failed = status_failed(a.ctl);
+    const size_t row = blockIdx.x;
+    const auto at = [&](int v) { return (uint32_t(v) * blockDim.x + threadIdx.x) * L; };
+    float h[V][L];
+    typename U::Raw res[V], w[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (at(v) < a.H) {
+            if (a.residual) res[v] = U::load(a.residual, row * a.H + at(v));
+            if (a.has_out || a.has_q) w[v] = U::load(a.weight, at(v));
+        }
+    sum_ranks<DT, L, V>(a, row, h);
+    if (a.residual)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (at(v) >= a.H) continue;
+            float x[L];
+            U::unpack(res[v], x);
+#pragma unroll
+            for (int l = 0; l < L; ++l) h[v][l] += x[l];
+        }
+    finish_row<DT, L, V>(a, row, h, w, s, 0, blockDim.x, failed);
+}
+
+// ---- rows through a ring -------------------------------------------------------------------------
+
+// With many rows a CTA takes every gridDim-th. A warp of its own copies the ranks' rows, one after the other, into a ring
+// of slots in shared memory (bulk copies, each completing on the slot's mbarrier), so that copies of this and the next
+// rows are in flight whatever the other warps do; these add up a row from its slots and hand each back.
+constexpr int kNormSlots = 32;
+
+struct NormRing {
+    NormShared s;
+    uint64_t full[kNormSlots], empty[kNormSlots];
+    uint32_t stop;  // the computing warps have given up
+};
+
+// The copying warp's one thread: source k of a row is rank k's, then the extra ones.
+template <int DT> __device__ __forceinline__ void copy_rows(const NormArgs& a, NormRing& ring, unsigned char* slots, int n_slots, int sources,
+                                                            const void* extra0, const void* extra1) {
+    const uint32_t bytes = uint32_t(a.H * Elem<DT>::kBytes);
+    uint32_t it = 0;
+    bool ok = true;
+    for (size_t row = blockIdx.x; row < a.T && ok; row += gridDim.x)
+        for (int k = 0; k < sources && ok; ++k, ++it) {
+            const uint32_t slot = it % n_slots, round = it / n_slots;
+            if (round > 0) ok = mbar_wait_bounded(a.ctl, &ring.empty[slot], (round - 1) & 1, a.timeout_ns);
+            if (*reinterpret_cast<volatile uint32_t*>(&ring.stop)) ok = false;
+            if (!ok) break;
+            const void* base = k < a.p ? a.x[k] : k == a.p ? extra0 : extra1;
+            mbar_arrive_expect_tx(&ring.full[slot], bytes);
+            bulk_g2s(slots + size_t(slot) * bytes, static_cast<const char*>(base) + row * bytes, bytes, &ring.full[slot]);
+        }
+    // the CTA stays until its copies have landed: the last n_slots of them
+    for (uint32_t i = it > uint32_t(n_slots) ? it - n_slots : 0; i < it; ++i)
+        mbar_wait_bounded(a.ctl, &ring.full[i % n_slots], (i / n_slots) & 1, kLandNs);
+}
+
+template <int DT, int V, bool GRAD> __global__ void __launch_bounds__(544, V == 1 ? 2 : 1) k_rmsnorm_ring(const __grid_constant__ NormArgs a, int n_slots) {
+    constexpr int L = Pack16<DT>::L;
+    using U = Unit<DT, L>;
+    extern __shared__ __align__(128) unsigned char slots[];
+    __shared__ NormRing ring;
+    const int n = blockDim.x - 32;  // threads that compute
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < n_slots; ++i) {
+            mbar_init(&ring.full[i], 1);
+            mbar_init(&ring.empty[i], n / 32);
+        }
+        ring.stop = 0u;
+        fence_barrier_init();
+    }
+    if (__syncthreads_or(status_failed(a.ctl))) return;
+    // the gradient has the rows h behind the ranks', and both forms the residual or what stands in its place
+    const int sources = a.p + (GRAD ? 1 : 0) + (a.residual ? 1 : 0);
+    if (int(threadIdx.x) >= n) {
+        if (int(blockIdx.x) == a.fault_cta) return;  // fault injection
+        if (int(threadIdx.x) == n) copy_rows<DT>(a, ring, slots, n_slots, sources, GRAD ? a.h : a.residual, a.residual);
+        return;
+    }
+    const uint32_t bytes = uint32_t(a.H * Elem<DT>::kBytes);
+    const auto at = [&](int v) { return (uint32_t(v) * n + threadIdx.x) * L; };
+    typename U::Raw wr[V];
+    float w[V][L], dw[V][L];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int l = 0; l < L; ++l) w[v][l] = dw[v][l] = 0.0f;
+        if (at(v) < a.H && (GRAD || a.has_out || a.has_q)) {
+            wr[v] = U::load(a.weight, at(v));
+            if constexpr (GRAD) U::unpack(wr[v], w[v]);
+        }
+    }
+    uint32_t slot = 0, phase = 0;
+    bool bad = false;
+    int turn = 0;
+    // takes the next slot's units; every warp hands it back for itself
+    auto take = [&](typename U::Raw (&raw)[V]) {
+        if (!bad) bad = !mbar_wait_bounded(a.ctl, &ring.full[slot], phase, a.timeout_ns);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (!bad && at(v) < a.H) raw[v] = *reinterpret_cast<const uint4*>(slots + size_t(slot) * bytes + at(v) * Elem<DT>::kBytes);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0 && !bad) mbar_arrive(&ring.empty[slot]);
+        if (++slot == uint32_t(n_slots)) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    for (size_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
+        float sum[V][L];
+        typename U::Raw raw[V], past[V];
+        for (int k = 0; k < a.p; ++k) {
+            take(raw);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float x[L];
+                U::unpack(raw[v], x);
+#pragma unroll
+                for (int l = 0; l < L; ++l) sum[v][l] = at(v) < a.H ? (k == 0 ? x[l] : sum[v][l] + x[l]) : 0.0f;
+            }
+        }
+        if constexpr (GRAD) {
+            float h[V][L];
+            take(raw);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                U::unpack(raw[v], h[v]);
+#pragma unroll
+                for (int l = 0; l < L; ++l) h[v][l] = at(v) < a.H ? h[v][l] : 0.0f;
+            }
+            if (a.residual) take(past);
+            if (!finish_grad<DT, L, V>(a, row, h, sum, past, w, dw, ring.s, turn, n, bad)) {
+                ring.stop = 1u;
+                return;
+            }
+        } else {
+            if (a.residual) {
+                take(raw);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float x[L];
+                    U::unpack(raw[v], x);
+#pragma unroll
+                    for (int l = 0; l < L; ++l) sum[v][l] = at(v) < a.H ? sum[v][l] + x[l] : 0.0f;
+                }
+            }
+            if (!finish_row<DT, L, V>(a, row, sum, wr, ring.s, turn, n, bad)) {
+                ring.stop = 1u;
+                return;
+            }
+        }
+    }
+    if constexpr (GRAD) {
+        if (!a.part) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int l = 0; l < L; ++l)
+                if (at(v) < a.H) a.part[blockIdx.x * a.H + at(v) + l] = dw[v][l];
     }
 }
 
@@ -229,6 +459,7 @@ template <int DT> __device__ __forceinline__ float sum_elem(const NormArgs& a, s
 template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_long(const __grid_constant__ NormArgs a) {
     __shared__ float2 s_sum[32], s_again[32];
     __shared__ uint32_t s_most;
+    bool bad = false;
     if (__syncthreads_or(status_failed(a.ctl))) return;
     const size_t row = blockIdx.x, o = row * a.H;
     const bool res = a.residual != nullptr, normed = a.has_out || a.has_q;
@@ -240,7 +471,7 @@ template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_long(const _
             const float h = sum_elem<DT>(a, o + i, res);
             ss += h * h;
         }
-        ss = cta_sum2(ss, 0.0f, s_sum).x;
+        ss = cta_sum2(ss, 0.0f, s_sum, blockDim.x, bad).x;
         float eps = a.eps;
         if (ss == INFINITY) {
             down = kNormDown;
@@ -249,7 +480,7 @@ template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_long(const _
                 const float h = sum_elem<DT>(a, o + i, res) * down;
                 ss += h * h;
             }
-            ss = cta_sum2(ss, 0.0f, s_again).x;
+            ss = cta_sum2(ss, 0.0f, s_again, blockDim.x, bad).x;
             eps = 0.0f;
         }
         r = 1.0f / sqrtf(ss / float(a.H) + eps);
@@ -294,12 +525,12 @@ template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_long(const _
 
 // ---- gradient ------------------------------------------------------------------------------------
 
-template <int DT, int L, int V> __global__ void __launch_bounds__(V == 8 ? 1024 : 512)
+template <int DT, int L, int V> __global__ void __launch_bounds__(V == 8 || L == 1 ? 1024 : 512)
 k_rmsnorm_grad(const __grid_constant__ NormArgs a) {
     using U = Unit<DT, L>;
-    __shared__ float2 s_sum[2][32], s_again[32];
-    if (__syncthreads_or(status_failed(a.ctl))) return;
-    const auto at = [&](int v) { return (size_t(v) * blockDim.x + threadIdx.x) * L; };
+    __shared__ NormShared s;
+    const bool failed = status_failed(a.ctl);
+    const auto at = [&](int v) { return (uint32_t(v) * blockDim.x + threadIdx.x) * L; };
     float w[V][L], dw[V][L];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -308,7 +539,7 @@ k_rmsnorm_grad(const __grid_constant__ NormArgs a) {
         if (at(v) < a.H) U::unpack(U::load(a.weight, at(v)), w[v]);
     }
     int turn = 0;
-    for (size_t row = blockIdx.x; row < a.T; row += a.ctas, turn ^= 1) {
+    for (size_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
         float h[V][L], g[V][L];
         typename U::Raw hr[V], past[V];
 #pragma unroll
@@ -318,55 +549,13 @@ k_rmsnorm_grad(const __grid_constant__ NormArgs a) {
                 if (a.residual) past[v] = U::load(a.residual, row * a.H + at(v));
             }
         sum_ranks<DT, L, V>(a, row, g);
-        float ss = 0.0f, wgh = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
 #pragma unroll
             for (int l = 0; l < L; ++l) h[v][l] = 0.0f;
             if (at(v) < a.H) U::unpack(hr[v], h[v]);
-#pragma unroll
-            for (int l = 0; l < L; ++l) {
-                ss += h[v][l] * h[v][l];
-                wgh += w[v][l] * g[v][l] * h[v][l];
-            }
         }
-        // the buffers alternate: the next row's are written after this row's barrier, which no thread passes that
-        // still reads the row's before
-        float2 sums = cta_sum2(ss, wgh, s_sum[turn]);
-        float eps = a.eps, down = 1.0f;
-        if (sums.x == INFINITY) {
-            down = kNormDown;
-            ss = wgh = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    h[v][l] *= down;
-                    ss += h[v][l] * h[v][l];
-                    wgh += w[v][l] * g[v][l] * h[v][l];
-                }
-            sums = cta_sum2(ss, wgh, s_again);
-            __syncthreads();
-            eps = 0.0f;
-        }
-        const float r = 1.0f / sqrtf(sums.x / float(a.H) + eps), along = sums.y * r / float(a.H);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float dx[L], add[L];
-#pragma unroll
-            for (int l = 0; l < L; ++l) {
-                const float u = h[v][l] * r;
-                dw[v][l] += g[v][l] * u;
-                dx[l] = (w[v][l] * g[v][l] - u * along) * (r * down);
-            }
-            if (at(v) >= a.H) continue;
-            if (a.residual) {
-                U::unpack(past[v], add);
-#pragma unroll
-                for (int l = 0; l < L; ++l) dx[l] += add[l];
-            }
-            for (int k = a.rank0; k < a.rank0 + a.ranks; ++k) U::store(a.out[k], row * a.H + at(v), dx);
-        }
+        if (!finish_grad<DT, L, V>(a, row, h, g, past, w, dw, s, turn, blockDim.x, failed)) return;
     }
     if (!a.part) return;
 #pragma unroll
@@ -377,10 +566,11 @@ k_rmsnorm_grad(const __grid_constant__ NormArgs a) {
 }
 
 template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_grad_long(const __grid_constant__ NormArgs a) {
-    __shared__ float2 s_sum[2][32], s_again[32];
+    __shared__ float2 s_sum[2][32], s_again[2][32];
+    bool bad = false;
     if (__syncthreads_or(status_failed(a.ctl))) return;
     int turn = 0;
-    for (size_t row = blockIdx.x; row < a.T; row += a.ctas, turn ^= 1) {
+    for (size_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
         const size_t o = row * a.H;
         float ss = 0.0f, wgh = 0.0f, eps = a.eps, down = 1.0f;
         auto add = [&](size_t i) {
@@ -389,13 +579,12 @@ template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_grad_long(co
             wgh += load_elem<DT>(a.weight, i) * sum_elem<DT>(a, o + i, false) * h;
         };
         for (size_t i = threadIdx.x; i < a.H; i += blockDim.x) add(i);
-        float2 sums = cta_sum2(ss, wgh, s_sum[turn]);
+        float2 sums = cta_sum2(ss, wgh, s_sum[turn], blockDim.x, bad);
         if (sums.x == INFINITY) {
             down = kNormDown;
             ss = wgh = 0.0f;
             for (size_t i = threadIdx.x; i < a.H; i += blockDim.x) add(i);
-            sums = cta_sum2(ss, wgh, s_again);
-            __syncthreads();
+            sums = cta_sum2(ss, wgh, s_again[turn], blockDim.x, bad);
             eps = 0.0f;
         }
         const float r = 1.0f / sqrtf(sums.x / float(a.H) + eps), along = sums.y * r / float(a.H);
@@ -412,87 +601,116 @@ template <int DT> __global__ void __launch_bounds__(1024) k_rmsnorm_grad_long(co
     }
 }
 
-// The weight's gradient: the CTAs' sums, 8 warps each an eighth of them, then the eighths in order.
-__global__ void __launch_bounds__(256) k_rmsnorm_grad_weight(const __grid_constant__ NormArgs a) {
-    __shared__ float s_part[8][32];
+// The weight's gradient: the CTAs' sums, each warp a share of them, then the shares in order. With 8 warps instead of 32 the
+// sums of 296 CTAs for 4,096 columns took 8.3 us.
+constexpr int kWeightWarps = 32;
+__global__ void __launch_bounds__(32 * kWeightWarps) k_rmsnorm_grad_weight(const __grid_constant__ NormArgs a) {
+    __shared__ float s_part[kWeightWarps][32];
     if (__syncthreads_or(status_failed(a.ctl))) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t i = size_t(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (i < a.H)
 #pragma unroll 8
-        for (int c = a.ctas * warp / 8; c < a.ctas * (warp + 1) / 8; ++c) s += __ldcg(a.part + c * a.H + i);
+        for (int c = a.ctas * warp / kWeightWarps; c < a.ctas * (warp + 1) / kWeightWarps; ++c) s += __ldcg(a.part + c * a.H + i);
     s_part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || i >= a.H) return;
-    for (int k = 1; k < 8; ++k) s += s_part[k][lane];
+    for (int k = 1; k < kWeightWarps; ++k) s += s_part[k][lane];
     for (int k = a.rank0; k < a.rank0 + a.ranks; ++k) a.grad_weight[k][i] = s;
 }
 
-// CTAs of the gradient, whatever the row's length: each one's sums of the weight's gradient are H numbers of scratch.
-int rmsnorm_grad_ctas(size_t rows, int num_sms) { return int(std::min(rows, size_t(num_sms) * 2)); }
-
-// How a row lies in a CTA: units of 16 bytes, 1 to 4 of them on up to 1024 threads; single elements, 1 or 8 to a thread, where rows
-// are not whole vectors; or the kernels for any length.
+// How a row lies in a CTA: units of 16 bytes, 1 to 4 of them on up to 512 threads; single elements, 1, 2 or 8 to a thread, where
+// rows are not whole vectors; or the kernels for any length. slots > 0: through a ring, per_sm CTAs to an SM.
 struct NormShape {
-    int form;     // 0: any length, 1: 1 vector, 2: 2, 4: 4 vectors, 11: 1 element, 18: 8 elements
+    int form;     // 0: any length; 1, 2, 4: so many vectors to a thread; 11, 12, 18: 1, 2, 8 elements
     int threads;
+    int slots, per_sm;
 };
-static NormShape norm_shape(const NormArgs& a, int dtype) {
+static NormShape norm_shape(const NormArgs& a, int dtype, bool grad, int num_sms) {
     const size_t L = dtype == COLL_BF16 ? 8 : 4, n = a.vec ? a.H / L : a.H;
     auto threads = [&](size_t per) { return int(((n + per - 1) / per + 31) / 32 * 32); };
-    if (a.vec) {
-        if (n <= 512) return {1, threads(1)};
-        if (n <= 1024) return {2, threads(2)};
-        if (n <= 2048) return {4, threads(4)};
-        return {0, 1024};
+    if (!a.vec) {
+        if (n <= 256) return {11, threads(1), 0, 0};
+        if (n <= 2048) return {12, threads(2), 0, 0};
+        if (n <= 8192) return {18, threads(8), 0, 0};
+        return {0, 1024, 0, 0};
     }
-    if (n <= 256) return {11, threads(1)};
-    if (n <= 8192) return {18, threads(8)};
-    return {0, 1024};
+    if (n > 2048) return {0, 1024, 0, 0};
+    const int V = n <= 512 ? 1 : n <= 1024 ? 2 : 4;
+    NormShape s{V, threads(V), 0, 0};
+    // A ring pays where a row is long and each CTA has some. Measured on B200, 8 ranks bf16, us with the ring and without: 592
+    // rows of 4096 23 and 27 (gradient 31 and 32), of 8192 43 and 47 (49 and 53); 296 rows alike; 4800 rows of 2048 89 and 91
+    // (90 and 77), of 1024 47 and 42 (50 and 57), of 256 32 and 13 (44 and 42). Two CTAs of one vector to a thread fit an SM by
+    // their registers, and one forms its sums while the other stores (2048 rows of 4096 in 8 bits 66 us, with one 79).
+    s.per_sm = V > 1 ? 1 : 2;
+    const size_t bytes = n * 16, slots = std::min<size_t>(kNormSlots, (size_t(220) * 1024 / s.per_sm - 8192) / bytes);
+    if (n >= 512 && slots >= 4 && !(grad && V == 4) && a.T >= size_t(2 * num_sms * s.per_sm)) s.slots = int(slots);
+    return s;
+}
+static int ring_ctas(const NormArgs& a, const NormShape& n, int num_sms) { return int(std::min(a.T, size_t(num_sms * n.per_sm))); }
+
+// CTAs of the gradient: each one's sums of the weight's gradient are H numbers of scratch.
+int rmsnorm_grad_ctas(const NormArgs& a, int dtype, int num_sms) {
+    const NormShape n = norm_shape(a, dtype, true, num_sms);
+    return n.slots ? ring_ctas(a, n, num_sms) : int(std::min(a.T, size_t(num_sms) * std::max(1, 512 / n.threads)));
 }
 
-template <int DT> static void go_norm(const NormArgs& a, const NormShape& n, unsigned ctas, cudaStream_t s) {
+template <int DT, int V, bool GRAD> static cudaError_t go_ring(const NormArgs& a, const NormShape& n, int ctas, cudaStream_t s) {
+    const size_t smem = size_t(n.slots) * a.H * Elem<DT>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_ring<DT, V, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    k_rmsnorm_ring<DT, V, GRAD><<<ctas, n.threads + 32, smem, s>>>(a, n.slots);
+    return cudaGetLastError();
+}
+
+template <int DT> static cudaError_t go_norm(const NormArgs& a, const NormShape& n, int num_sms, cudaStream_t s) {
     constexpr int L = Pack16<DT>::L;
+    const unsigned ctas = unsigned(a.T);
+    if (n.slots) {
+        const int c = ring_ctas(a, n, num_sms);
+        return n.form == 1 ? go_ring<DT, 1, false>(a, n, c, s) : n.form == 2 ? go_ring<DT, 2, false>(a, n, c, s) : go_ring<DT, 4, false>(a, n, c, s);
+    }
     switch (n.form) {
         case 1: k_rmsnorm<DT, L, 1><<<ctas, n.threads, 0, s>>>(a); break;
         case 2: k_rmsnorm<DT, L, 2><<<ctas, n.threads, 0, s>>>(a); break;
         case 4: k_rmsnorm<DT, L, 4><<<ctas, n.threads, 0, s>>>(a); break;
         case 11: k_rmsnorm<DT, 1, 1><<<ctas, n.threads, 0, s>>>(a); break;
+        case 12: k_rmsnorm<DT, 1, 2><<<ctas, n.threads, 0, s>>>(a); break;
         case 18: k_rmsnorm<DT, 1, 8><<<ctas, n.threads, 0, s>>>(a); break;
         default: k_rmsnorm_long<DT><<<ctas, n.threads, 0, s>>>(a);
     }
+    return cudaGetLastError();
 }
 
-template <int DT> static void go_norm_grad(const NormArgs& a, const NormShape& n, cudaStream_t s) {
+template <int DT> static cudaError_t go_norm_grad(const NormArgs& a, const NormShape& n, cudaStream_t s) {
     constexpr int L = Pack16<DT>::L;
     const unsigned ctas = unsigned(a.ctas);
+    if (n.slots) return n.form == 1 ? go_ring<DT, 1, true>(a, n, a.ctas, s) : go_ring<DT, 2, true>(a, n, a.ctas, s);
     switch (n.form) {
         case 1: k_rmsnorm_grad<DT, L, 1><<<ctas, n.threads, 0, s>>>(a); break;
         case 2: k_rmsnorm_grad<DT, L, 2><<<ctas, n.threads, 0, s>>>(a); break;
         case 4: k_rmsnorm_grad<DT, L, 4><<<ctas, n.threads, 0, s>>>(a); break;
         case 11: k_rmsnorm_grad<DT, 1, 1><<<ctas, n.threads, 0, s>>>(a); break;
+        case 12: k_rmsnorm_grad<DT, 1, 2><<<ctas, n.threads, 0, s>>>(a); break;
         case 18: k_rmsnorm_grad<DT, 1, 8><<<ctas, n.threads, 0, s>>>(a); break;
         default: k_rmsnorm_grad_long<DT><<<ctas, n.threads, 0, s>>>(a);
     }
-}
-
-cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, cudaStream_t s) {
-    if (a.T > size_t(INT32_MAX)) return cudaErrorInvalidValue;
-    const NormShape n = norm_shape(a, dtype);
-    if (dtype == COLL_BF16) go_norm<COLL_BF16>(a, n, unsigned(a.T), s);
-    else go_norm<COLL_FP32>(a, n, unsigned(a.T), s);
     return cudaGetLastError();
 }
 
-cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, cudaStream_t s, int* kernels_launched) {
-    const NormShape n = norm_shape(a, dtype);
-    if (dtype == COLL_BF16) go_norm_grad<COLL_BF16>(a, n, s);
-    else go_norm_grad<COLL_FP32>(a, n, s);
+cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, int num_sms, cudaStream_t s) {
+    if (a.T > size_t(INT32_MAX)) return cudaErrorInvalidValue;
+    const NormShape n = norm_shape(a, dtype, false, num_sms);
+    return dtype == COLL_BF16 ? go_norm<COLL_BF16>(a, n, num_sms, s) : go_norm<COLL_FP32>(a, n, num_sms, s);
+}
+
+cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, int num_sms, cudaStream_t s, int* kernels_launched) {
+    const NormShape n = norm_shape(a, dtype, true, num_sms);
+    cudaError_t e = dtype == COLL_BF16 ? go_norm_grad<COLL_BF16>(a, n, s) : go_norm_grad<COLL_FP32>(a, n, s);
     *kernels_launched = 1;
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.part) return e;
-    k_rmsnorm_grad_weight<<<unsigned((a.H + 31) / 32), 256, 0, s>>>(a);
+    k_rmsnorm_grad_weight<<<unsigned((a.H + 31) / 32), 32 * kWeightWarps, 0, s>>>(a);
     *kernels_launched = 2;
     return cudaGetLastError();
 }

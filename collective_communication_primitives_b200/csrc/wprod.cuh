@@ -324,12 +324,6 @@ __device__ __forceinline__ void init_panels(const ProductSmem& s) {
     fence_barrier_init();
 }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
-}
-
-constexpr uint64_t kLandNs = 1000000000ull;  // longest wait for copies in flight before a CTA may leave
-
 // The copying warp's side of a unit. False after a wait that ran out.
 template <int NT, int PARTS, typename Job>
 __device__ __forceinline__ bool copy_tokens(const Job& job, const Ctl& ctl, uint64_t timeout_ns, const ProductSmem& s,
