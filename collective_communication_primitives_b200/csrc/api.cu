@@ -2375,7 +2375,7 @@ static coll_status_t coll_adapters_impl(sim_comm_t c, const void* const* x, cons
     a.T = tokens;
     a.N = N;
     a.K = K;
-    a.splits = adapter_splits(tokens, K, a.segments, c->num_sms);
+    a.splits = adapter_splits(a, c->num_sms);
     if ((st = ensure_moe(c, size_t(a.splits) * tokens * size_t(a.Rp) * 4)) != COLL_OK) return st;
     a.u = reinterpret_cast<float*>(c->moe);
     a.ctl = make_ctl(c);

@@ -448,7 +448,7 @@ cudaError_t launch_logprobs_grad(const LogprobArgs& a, int dtype, cudaStream_t s
 cudaError_t launch_rmsnorm(const NormArgs& a, int dtype, int num_sms, cudaStream_t s);
 int rmsnorm_grad_ctas(const NormArgs& a, int dtype, int num_sms);
 cudaError_t launch_rmsnorm_grad(const NormArgs& a, int dtype, int num_sms, cudaStream_t s, int* kernels_launched);
-int adapter_splits(size_t tokens, size_t k, int segments, int num_sms);
+int adapter_splits(const AdapterArgs& a, int num_sms);
 cudaError_t launch_adapters(const AdapterArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_adjust(const AdjustArgs& a, int dtype, int num_sms, cudaStream_t s);
 cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s);
