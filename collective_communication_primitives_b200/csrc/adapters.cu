@@ -75,16 +75,16 @@ k_adapter_down(const __grid_constant__ AdapterArgs a, int slots) {
     constexpr int kPart = MT * NT > 8 ? 8 / MT : NT;          // eights of tokens whose sums the warps exchange at a time
     __shared__ float s_sum[kAdWarps][16 * MT * 8 * kPart];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (__syncthreads_or(status_failed(a.ctl))) return;
+    const bool failed = status_failed(a.ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    size_t b = blockIdx.x;
-    const int split = int(b % a.splits);
-    b /= a.splits;
-    const int sub = int(b % slots);
-    const size_t t0 = b / slots * (8 * NT);
+    const uint32_t b = blockIdx.x / a.splits, groups = gridDim.x / a.splits / slots;
+    const int split = int(blockIdx.x % a.splits), sub = slots - 1 - int(b / groups);  // CTAs that may have nothing to do come first
+    const size_t t0 = size_t(b % groups) * (8 * NT);
     const uint32_t steps = uint32_t((a.K + kAdChunk - 1) / kAdChunk), all = steps * a.segments;
     const uint32_t s0 = uint32_t(uint64_t(all) * split / a.splits), s1 = uint32_t(uint64_t(all) * (split + 1) / a.splits);
     const Crews crews = crews_of(a, t0, 8 * NT, false);
+    if (__popc(crews.firsts) <= sub) return;
+    if (__syncthreads_or(failed)) return;
     uint32_t todo = crews.firsts;
     for (int crew = 0; todo; ++crew) {
         const int slot = __ffs(todo) - 1;
@@ -180,16 +180,16 @@ template <int MT> __global__ void __launch_bounds__(kAdThreads, 2) k_adapter_dow
     static_assert(kAdWarps * 16 * MT * 8 * NT * 4 <= kTileStages * tile_bytes<MT>(), "the warps' sums lie where the stages did");
     extern __shared__ __align__(128) unsigned char s_tile[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (__syncthreads_or(status_failed(a.ctl))) return;
+    const bool failed = status_failed(a.ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    size_t b = blockIdx.x;
-    const int split = int(b % a.splits);
-    b /= a.splits;
-    const int sub = int(b % slots);
-    const size_t t0 = b / slots * (8 * NT);
+    const uint32_t b = blockIdx.x / a.splits, groups = gridDim.x / a.splits / slots;
+    const int split = int(blockIdx.x % a.splits), sub = slots - 1 - int(b / groups);  // CTAs that may have nothing to do come first
+    const size_t t0 = size_t(b % groups) * (8 * NT);
     const uint32_t per = uint32_t((a.K + kTileK - 1) / kTileK), all = per * a.segments;  // stages of a rank's columns, in all
     const uint32_t s0 = uint32_t(uint64_t(all) * split / a.splits), s1 = uint32_t(uint64_t(all) * (split + 1) / a.splits);
     const Crews crews = crews_of(a, t0, 8 * NT, false);
+    if (__popc(crews.firsts) <= sub) return;
+    if (__syncthreads_or(failed)) return;
     const uint32_t base = smem_u32(s_tile);
     float* const sums = reinterpret_cast<float*>(s_tile);
     uint32_t todo = crews.firsts;
@@ -362,11 +362,10 @@ k_adapter_up(const __grid_constant__ AdapterArgs a, int slots, int chunks, int t
     const bool failed = status_failed(a.ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t N = uint32_t(a.N);
-    size_t b = blockIdx.x;
-    const int first = int(b % chunks) * tiles, last = min(first + tiles, a.row ? per_rank : per_rank * a.outs);
-    b /= chunks;
-    const int sub = int(b % slots);
-    const size_t t0 = b / slots * kGroup;
+    const uint32_t b = blockIdx.x / chunks, groups = gridDim.x / chunks / slots;
+    const int first = int(blockIdx.x % chunks) * tiles, last = min(first + tiles, a.row ? per_rank : per_rank * a.outs);
+    const int sub = slots - 1 - int(b / groups);
+    const size_t t0 = size_t(b % groups) * kGroup;
     const int outs = a.row ? a.outs : 1;  // a tile of the row-parallel form goes to every rank
     const Crews crews = crews_of(a, t0, kGroup, true);
     bool waited = false;
@@ -573,9 +572,9 @@ static size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Tokens of a group: eight while there are few, since then each has an adapter of its own; else 32, since one pass over a matrix
 // then serves more of a prompt's tokens.
 static int group_tiles(size_t tokens) { return tokens <= 64 ? 1 : 4; }
-// CTAs that share a group's adapters: a CTA to each while there are few groups; with many, four, so that a group on the border of
-// two requests takes no longer than the others.
-static int group_slots(size_t tokens) { return tokens <= 512 ? 8 * group_tiles(tokens) : 4; }
+// CTAs that share a group's adapters: a CTA to each while there are few groups; with many, two, so that a group on the border of two
+// requests takes no longer than the others.
+static int group_slots(size_t tokens) { return tokens <= 512 ? 8 * group_tiles(tokens) : 2; }
 
 // Parts of the sum over k: as many as give the first kernel a CTA to an SM (two of the form with stages), each of at least 8
 // steps or 2 stages; the second kernel waits for all parts (32 tokens of 64 adapters, k 4096, us with 4, 5, 10 and 16 parts: 16.8,
@@ -605,7 +604,7 @@ template <int NT, int MT> static cudaError_t go_down(const AdapterArgs& a, unsig
 }
 
 template <int MT> static cudaError_t go_up(const AdapterArgs& a, int num_sms, cudaStream_t s) {
-    const size_t groups = (a.T + 16 * MT - 1) / (16 * MT), slots = a.T <= 512 ? 16 * MT : 4;
+    const size_t groups = (a.T + 16 * MT - 1) / (16 * MT), slots = a.T <= 512 ? 16 * MT : 2;
     // tiles of a CTA: as many to each warp as leave two CTAs to an SM
     const size_t units = a.T <= 512 ? a.T : groups, per_rank = (a.N + kAdCols - 1) / kAdCols, all = per_rank * (a.row ? 1 : a.outs);
     if (all > size_t(INT32_MAX)) return cudaErrorInvalidValue;
