@@ -393,8 +393,9 @@ struct AdjustArgs {
     void* out[kMaxRanks];                // [rows][ld_out]
     coll_logit_rules_t rules;
     int p, rank0, ranks;
-    int cols, tiles;                     // columns of one CTA, CTAs per row of a shard
     int hist_vec;                        // history rows are 16-byte aligned
+    uint32_t first, last, cols, parts;   // set by the launcher: the call's columns, those of a CTA, CTAs per row
+    int words, hash_shift;               // set by the launcher: words of counts of a CTA; 32 - log2 of a table's places
     size_t rows, V, m, ld, ld_out;
     Ctl ctl;
 };
