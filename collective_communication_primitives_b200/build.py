@@ -1,4 +1,5 @@
-"""Build the CUDA library ``libsimcomm.so`` (sm_100a) in the package directory with nvcc.
+"""Build the CUDA library ``libsimcomm.so`` (sm_100a) in the package directory with nvcc, and the binding's helper
+``_marshal.so`` (the checks of a call's tensors) with g++.
 
     python -m collective_communication_primitives_b200.build [--force] [-v]
 
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsimcomm.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 OBJ_DIR = os.path.join(ROOT, "_build", "simcomm")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -56,7 +59,25 @@ def _newer(target, deps):
 
 
 def _stale():
-    return _newer(LIB, sources() + _headers())
+    return _newer(LIB, sources() + _headers()) or _newer(MARSHAL, [MARSHAL_SRC])
+
+
+def build_marshal(verbose: bool = False):
+    """The helper is built against the headers of the torch that this interpreter imports."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_path("include"), os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += ["-o", MARSHAL + ".tmp", MARSHAL_SRC, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -76,10 +97,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(obj + ".tmp", obj)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        helper = ex.submit(build_marshal, verbose) if force or _newer(MARSHAL, [MARSHAL_SRC]) else None
         objs = list(ex.map(compile_one, sources()))
-    subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
-    os.replace(LIB + ".tmp", LIB)
+        if helper is not None:
+            helper.result()
+    if force or _newer(LIB, objs):
+        subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
+        os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

@@ -2177,6 +2177,7 @@ static coll_status_t norm_common(sim_comm* c, const void* const* x, const void* 
     if ((st = check_float(dt, "rows of the norm")) != COLL_OK) return st;
     if ((st = check_row(hidden, "hidden")) != COLL_OK) return st;
     if (rows > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "rows must fit in int32");
+    if ((st = check_rows(rows, hidden, "rows")) != COLL_OK) return st;
     if (!(eps >= FLT_MIN && eps <= FLT_MAX)) return fail(COLL_ERR_INVALID_ARG, "eps must be finite and at least 2^-126");
     if (!x) return fail(COLL_ERR_INVALID_ARG, "null buffer array");
     if (rows == 0) return COLL_OK;

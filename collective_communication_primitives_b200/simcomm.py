@@ -24,6 +24,18 @@ ALGOS = {"direct": 0, "ring": 1, "rd": 2, "hd": 3, "tree": 4, "dbtree": 5, "ll":
 PARALLEL = {"column": 0, "row": 1}
 
 _lib = None
+_marshal = None  # the helper that looks at a call's tensors (csrc/marshal.cpp); False: not built, Python looks at them
+
+
+def _load_marshal():
+    global _marshal
+    import torch  # noqa: F401  (the helper uses its libraries)
+    try:
+        from . import _marshal as helper
+        _marshal = helper
+    except ImportError:
+        _marshal = False
+    return _marshal
 
 
 class SimCommError(RuntimeError):
@@ -367,19 +379,14 @@ class SimComm:
         if tensors is None:
             return None
         dev = self._device
+        # the usual call in one sweep; anything else takes the slow way, which says what is wrong
+        fast = _marshal if _marshal is not None else _load_marshal()
+        if fast:
+            got = fast.address(tensors, dtype, shape, dev) if one else \
+                fast.addresses(tensors, dtype, shape, dev, self.p, -1 if row is None else row[0])
+            if got is not None:
+                return got
         vector = isinstance(shape, int)
-        if not one:
-            try:  # the usual call in one sweep; anything else takes the slow way, which says what is wrong
-                if vector:
-                    out = [t.data_ptr() for t in tensors
-                           if t.dtype is dtype and t.get_device() == dev and t.numel() == shape and t.is_contiguous()]
-                else:
-                    out = [t.data_ptr() for t in tensors
-                           if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()]
-            except AttributeError:
-                out = ()
-            if len(out) == self.p == len(tensors) and (row is None or row[0] == row[1]):
-                return self._pack(*out)
         out, numel = [], shape if vector else math.prod(shape)
         for t in ((tensors,) if one else tensors):
             if t is None or isinstance(t, int):
@@ -407,13 +414,6 @@ class SimComm:
 
     def _one(self, what, t, dtype, shape):
         """The address of a single tensor that all ranks read, checked as by _tensors (None stays None)."""
-        if t is None:
-            return None
-        try:  # the usual call; anything else takes the slow way, which says what is wrong
-            if t.dtype is dtype and t.shape == shape and t.get_device() == self._device and t.is_contiguous():
-                return t.data_ptr()
-        except AttributeError:
-            pass
         return self._tensors(what, t, dtype, shape, one=True)
 
     def _launch_stream(self, stream):

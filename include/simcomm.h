@@ -201,8 +201,8 @@ const char* coll_status_string(coll_status_t status);
  *   "fault_skip_rank"  debugging: this rank is silenced (the ring and tree executors never signal
  *                  its chunks, the butterfly executor never counts its tasks, the LL kernels never
  *                  send its words, the fused MoE dispatch's CTA of this index never arrives at its
- *                  first grid barrier, and a warp of the 4-bit linear's or the expert layer's CTA of
- *                  this index falls silent), so the waits on it time out (-1 = off, the default).
+ *                  first grid barrier, and a warp of the 4-bit linear's, the expert layer's or the norm's
+ *                  CTA of this index falls silent), so the waits on it time out (-1 = off, the default).
  *                  Host-side fault injection only.
  *   "copy_variant" copy path of the direct Broadcast/AllGather/All-to-All(v)/Scatter/Gather: -1 = the
  *                  default (Broadcast and AllGather: 9, the equal All-to-All: 11, where the buffers
