@@ -2412,7 +2412,8 @@ static coll_status_t coll_adjust_logits_impl(sim_comm_t c, const void* const* lo
     if (ld_out < m) return fail(COLL_ERR_INVALID_ARG, "ld_out is less than the shard's columns, ceil(vocab / p)");
     if ((st = check_count(ld_out, "ld_out")) != COLL_OK || (st = check_rows(rows, ld_out, "rows")) != COLL_OK) return st;
     const coll_logit_rules_t& u = *rules;
-    if (u.history_len && u.ld_history > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "ld_history must fit in int32");
+    // a column's count has 30 bits of its word
+    if (u.history_len && u.ld_history >= (size_t(1) << 30)) return fail(COLL_ERR_INVALID_ARG, "ld_history must be below 2^30");
     if (u.bias_start && u.bias_count > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "bias_count must fit in int32");
     if (u.mask) {
         if (u.ld_mask < (vocab + 31) / 32) return fail(COLL_ERR_INVALID_ARG, "ld_mask is less than ceil(vocab / 32)");

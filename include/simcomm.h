@@ -647,7 +647,7 @@ typedef struct {
  *             ld (in place: then only what changes is written); no other overlap. Columns past the shard's own
  *             (padding) are not written.
  * Computed in fp32, rounded once; scores that no rule touches keep their bits. A token, length, start or mask row out of
- * range is reported asynchronously as COLL_ERR_INVALID_ARG. V in [1, 2^31), ld_history at most 2^31 - 1. rows = 0 enqueues
+ * range is reported asynchronously as COLL_ERR_INVALID_ARG. V in [1, 2^31), ld_history below 2^30. rows = 0 enqueues
  * nothing. On a rank view only this rank's entries are used. */
 coll_status_t coll_adjust_logits(sim_comm_t comm, const void* const* logits, size_t ld, size_t rows, size_t vocab,
                                  coll_dtype_t dtype, const coll_logit_rules_t* rules, void* const* out, size_t ld_out,
