@@ -15,7 +15,8 @@
 // Bound by the scores' bytes; with few rows by the latency of history, counts and scores in turn. Measured on B200, 256 rows
 // of 131072 bf16 with 1024 tokens and masks, us: with a word per column, 8192 to a CTA, 53 (the words looked at while the scores are
 // copied: 56, since every warp with one such column in 256 goes the long way), and of these 15 the counts and 8 the end, which
-// every CTA of a row waits for alone.
+// every CTA of a row waits for alone; with a table of 2048 places, 65536 columns to a CTA, 40 (136 MB, 3.4 TB/s), of which the
+// copy alone would be 23 and the masks 7. 8 rows of 131072 fp32 with 4096 tokens, biases and masks 9.3, 33 of 50257 6.9.
 #include <algorithm>
 
 #include "common.cuh"
