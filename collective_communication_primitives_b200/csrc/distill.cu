@@ -32,12 +32,6 @@ constexpr int kFilterBits = 16384;
 constexpr int kTable = 512;               // at least twice the places
 constexpr uint32_t kEmpty = 0xffffffffu;  // no column: a vocabulary has fewer than 2^31
 
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Sum s of 2^((x - m) c) over a set of scores with maximum m (at least -FLT_MAX; NaN if a score is).
 struct Mass {
     float m, s;

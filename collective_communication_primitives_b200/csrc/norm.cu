@@ -8,8 +8,8 @@
 // and write the finished row to every rank: p + 1 rows in, p (2 bytes or more) rows out. Bound by these bytes; for a few
 // rows by the latency of one load, one reduction and one store. Rows too long for registers are summed again for
 // each use. Measured on B200, 8 ranks bf16, replayed in a graph: 1 row of 4096 4.7 us; 2048 rows of 4096 with total and 8-bit
-// rows in groups of 128 66 us (355 MB: 5.4 TB/s), total and norm 69 us and their gradient 65 and 6 us (721 MB in 148 us: 4.9).
-// Under a profiler the 8-bit form issues in 62% of its slots and the gradient in 60%, waiting for shared memory more than for DRAM.
+// rows in groups of 128 66.5 us (355 MB: 5.3 TB/s; a row written to 8 ranks by bulk stores alone reaches 5.9), total and norm 72 us and
+// their gradient 59.5 and 6 us (721 MB in 141 us: 5.1). Arithmetic takes two elements at a time: with one the gradient took 65.
 //
 // In the gradient a CTA takes every ctas-th row and keeps its sums of the weight's gradient in registers; a second kernel
 // adds the CTAs' sums in order.
@@ -108,6 +108,64 @@ template <> struct Q8<8> {
     }
 };
 
+// Units' elements two at a time.
+template <int L> __device__ __forceinline__ void add_to(float (&h)[L], const float (&x)[L]) {
+    if constexpr (L % 2 == 0) {
+#pragma unroll
+        for (int l = 0; l < L; l += 2) unpack2(add2(pack2(h[l], h[l + 1]), pack2(x[l], x[l + 1])), h[l], h[l + 1]);
+    } else {
+#pragma unroll
+        for (int l = 0; l < L; ++l) h[l] += x[l];
+    }
+}
+// a = a b, with b a factor per element or one for all
+template <int L> __device__ __forceinline__ void mul_by(float (&a)[L], const float (&b)[L]) {
+    if constexpr (L % 2 == 0) {
+#pragma unroll
+        for (int l = 0; l < L; l += 2) unpack2(mul2(pack2(a[l], a[l + 1]), pack2(b[l], b[l + 1])), a[l], a[l + 1]);
+    } else {
+#pragma unroll
+        for (int l = 0; l < L; ++l) a[l] *= b[l];
+    }
+}
+template <int L> __device__ __forceinline__ void mul_by(float (&a)[L], float b) {
+    float f[L];
+#pragma unroll
+    for (int l = 0; l < L; ++l) f[l] = b;
+    mul_by<L>(a, f);
+}
+// c = a b + c
+template <int L> __device__ __forceinline__ void mul_add(const float (&a)[L], const float (&b)[L], float (&c)[L]) {
+    if constexpr (L % 2 == 0) {
+#pragma unroll
+        for (int l = 0; l < L; l += 2)
+            unpack2(fma2(pack2(a[l], a[l + 1]), pack2(b[l], b[l + 1]), pack2(c[l], c[l + 1])), c[l], c[l + 1]);
+    } else {
+#pragma unroll
+        for (int l = 0; l < L; ++l) c[l] = fmaf(a[l], b[l], c[l]);
+    }
+}
+// The sum of a b over all units: an even and an odd chain
+template <int L, int V> __device__ __forceinline__ float dot(const float (&a)[V][L], const float (&b)[V][L]) {
+    if constexpr (L % 2 == 0) {
+        unsigned long long s = 0ull;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int l = 0; l < L; l += 2) s = fma2(pack2(a[v][l], a[v][l + 1]), pack2(b[v][l], b[v][l + 1]), s);
+        float even, odd;
+        unpack2(s, even, odd);
+        return even + odd;
+    } else {
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int l = 0; l < L; ++l) s = fmaf(a[v][l], b[v][l], s);
+        return s;
+    }
+}
+
 // The sum of all ranks' units, V of them per thread (unit v at element e0 + (v blockDim + tid) L), loads of as many ranks
 // in flight as registers allow.
 template <int DT, int L, int V>
@@ -117,7 +175,7 @@ __device__ __forceinline__ void sum_ranks(const NormArgs& a, size_t row, float (
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int l = 0; l < L; ++l) h[v][l] = 0.0f;
+        for (int l = 0; l < L; ++l) h[v][l] = -0.0f;  // the first addition leaves what it adds
     for (int q0 = 0; q0 < a.p; q0 += kAhead) {
         typename U::Raw raw[kAhead][V];
 #pragma unroll
@@ -135,8 +193,7 @@ __device__ __forceinline__ void sum_ranks(const NormArgs& a, size_t row, float (
                 if (q0 + j < a.p && e < a.H) {
                     float x[L];
                     U::unpack(raw[j][v], x);
-#pragma unroll
-                    for (int l = 0; l < L; ++l) h[v][l] = q0 + j == 0 ? x[l] : h[v][l] + x[l];
+                    add_to<L>(h[v], x);
                 }
             }
     }
@@ -160,12 +217,7 @@ __device__ __forceinline__ bool finish_row(const NormArgs& a, size_t row, float 
     const bool whole = a.shift < 0, narrow = !whole && (1 << a.shift) < 32 * L;
     if (a.has_q && !narrow)
         for (int i = threadIdx.x; i < 256; i += n) s.most[turn][i] = 0u;
-    float ss = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int l = 0; l < L; ++l) ss += h[v][l] * h[v][l];
-    ss = cta_sum2(ss, 0.0f, s.sum[turn], n, bad).x;
+    float ss = cta_sum2(dot<L, V>(h, h), 0.0f, s.sum[turn], n, bad).x;
     if (bad) return false;
     if (a.has_total)
 #pragma unroll
@@ -174,24 +226,23 @@ __device__ __forceinline__ bool finish_row(const NormArgs& a, size_t row, float 
     if (!(a.has_out || a.has_q)) return true;
     float eps = a.eps;
     if (ss == INFINITY) {  // the same for every thread
-        ss = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int l = 0; l < L; ++l) {
-                h[v][l] *= kNormDown;
-                ss += h[v][l] * h[v][l];
-            }
-        ss = cta_sum2(ss, 0.0f, s.again[turn], n, bad).x;
+        for (int v = 0; v < V; ++v) mul_by<L>(h[v], kNormDown);
+        ss = cta_sum2(dot<L, V>(h, h), 0.0f, s.again[turn], n, bad).x;
         eps = 0.0f;
     }
     const float r = 1.0f / sqrtf(ss / float(a.H) + eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float f[L];
-        if (at(v) < a.H) U::unpack(w[v], f);
+        if (at(v) >= H) {
 #pragma unroll
-        for (int l = 0; l < L; ++l) h[v][l] = at(v) < a.H ? h[v][l] * r * f[l] : 0.0f;
+            for (int l = 0; l < L; ++l) h[v][l] = 0.0f;
+            continue;
+        }
+        float f[L];
+        U::unpack(w[v], f);
+        mul_by<L>(h[v], r);
+        mul_by<L>(h[v], f);
     }
     if (a.has_out)
 #pragma unroll
@@ -236,47 +287,40 @@ __device__ __forceinline__ bool finish_grad(const NormArgs& a, size_t row, float
                                             NormShared& s, int turn, int n, bool bad) {
     using U = Unit<DT, L>;
     const auto at = [&](int v) { return (uint32_t(v) * n + threadIdx.x) * L; };
-    float ss = 0.0f, wgh = 0.0f;
+    float wg[V][L];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            ss += h[v][l] * h[v][l];
-            wgh += w[v][l] * g[v][l] * h[v][l];
-        }
-    float2 sums = cta_sum2(ss, wgh, s.sum[turn], n, bad);
+        for (int l = 0; l < L; ++l) wg[v][l] = g[v][l];
+        mul_by<L>(wg[v], w[v]);
+    }
+    float2 sums = cta_sum2(dot<L, V>(h, h), dot<L, V>(wg, h), s.sum[turn], n, bad);
     if (bad) return false;
     float eps = a.eps, down = 1.0f;
     if (sums.x == INFINITY) {
         down = kNormDown;
-        ss = wgh = eps = 0.0f;
+        eps = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int l = 0; l < L; ++l) {
-                h[v][l] *= down;
-                ss += h[v][l] * h[v][l];
-                wgh += w[v][l] * g[v][l] * h[v][l];
-            }
-        sums = cta_sum2(ss, wgh, s.again[turn], n, bad);
+        for (int v = 0; v < V; ++v) mul_by<L>(h[v], down);
+        sums = cta_sum2(dot<L, V>(h, h), dot<L, V>(wg, h), s.again[turn], n, bad);
     }
     const float r = 1.0f / sqrtf(sums.x / float(a.H) + eps), along = sums.y * r / float(a.H);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        float dx[L], add[L];
+        float away[L];
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-            const float u = h[v][l] * r;
-            dw[v][l] += g[v][l] * u;
-            dx[l] = (w[v][l] * g[v][l] - u * along) * (r * down);
-        }
+        for (int l = 0; l < L; ++l) away[l] = -along;
+        mul_by<L>(h[v], r);  // u
+        mul_add<L>(g[v], h[v], dw[v]);
+        mul_add<L>(h[v], away, wg[v]);
+        mul_by<L>(wg[v], r * down);
         if (at(v) >= a.H) continue;
         if (a.residual) {
+            float add[L];
             U::unpack(past[v], add);
-#pragma unroll
-            for (int l = 0; l < L; ++l) dx[l] += add[l];
+            add_to<L>(wg[v], add);
         }
-        store_all<DT, L>(a, a.out, row * a.H + at(v), dx);
+        store_all<DT, L>(a, a.out, row * a.H + at(v), wg[v]);
     }
     return true;
 }
@@ -304,8 +348,7 @@ k_rmsnorm(const __grid_constant__ NormArgs a) {
             if (at(v) >= a.H) continue;
             float x[L];
             U::unpack(res[v], x);
-#pragma unroll
-            for (int l = 0; l < L; ++l) h[v][l] += x[l];
+            add_to<L>(h[v], x);
         }
     finish_row<DT, L, V>(a, row, h, w, s, 0, blockDim.x, failed);
 }
@@ -398,41 +441,32 @@ template <int DT, int V, bool GRAD> __global__ void __launch_bounds__(544, V == 
     for (size_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
         float sum[V][L];
         typename U::Raw raw[V], past[V];
-        for (int k = 0; k < a.p; ++k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            raw[v] = make_uint4(0, 0, 0, 0);  // stays where a thread has no unit
+#pragma unroll
+            for (int l = 0; l < L; ++l) sum[v][l] = -0.0f;  // the first addition leaves what it adds
+        }
+        for (int k = 0; k < a.p + (!GRAD && a.residual ? 1 : 0); ++k) {
             take(raw);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float x[L];
                 U::unpack(raw[v], x);
-#pragma unroll
-                for (int l = 0; l < L; ++l) sum[v][l] = at(v) < a.H ? (k == 0 ? x[l] : sum[v][l] + x[l]) : 0.0f;
+                add_to<L>(sum[v], x);
             }
         }
         if constexpr (GRAD) {
             float h[V][L];
             take(raw);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                U::unpack(raw[v], h[v]);
-#pragma unroll
-                for (int l = 0; l < L; ++l) h[v][l] = at(v) < a.H ? h[v][l] : 0.0f;
-            }
+            for (int v = 0; v < V; ++v) U::unpack(raw[v], h[v]);
             if (a.residual) take(past);
             if (!finish_grad<DT, L, V>(a, row, h, sum, past, w, dw, ring.s, turn, n, bad)) {
                 ring.stop = 1u;
                 return;
             }
         } else {
-            if (a.residual) {
-                take(raw);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float x[L];
-                    U::unpack(raw[v], x);
-#pragma unroll
-                    for (int l = 0; l < L; ++l) sum[v][l] = at(v) < a.H ? sum[v][l] + x[l] : 0.0f;
-                }
-            }
             if (!finish_row<DT, L, V>(a, row, sum, wr, ring.s, turn, n, bad)) {
                 ring.stop = 1u;
                 return;
