@@ -9,8 +9,8 @@
 // Forward: one pass over the scores with a running maximum and sum, as in the log probabilities; few rows are cut into
 // parts that the last CTA joins in order, and the last CTA of a row does the list. With the class of the rest the
 // pass leaves the listed columns out, so that P_rest is a sum and no difference: what is left beside a peaked
-// distribution keeps its precision. A filter in shared memory (a bit per vector of scores, modulo its size) finds the
-// vectors with a listed column, a table of them which of their scores are listed.
+// distribution keeps its precision. Two words of a thread, a bit for each of its vectors modulo 64, tell which have a listed
+// column, a table of them which of their scores are listed.
 //
 // Differences x - m are formed before they are scaled, so the sums are as exact for scores far from 0 as for others, and
 // a row of the type's lowest value is a row like any other. A row of nothing but -inf has P = 0.
@@ -28,7 +28,7 @@
 
 namespace simcomm {
 
-constexpr int kFilterBits = 16384;
+constexpr uint32_t kFilterBatches = 16;   // a bit per vector of so many of a thread's batches
 constexpr int kTable = 512;               // at least twice the places
 constexpr uint32_t kEmpty = 0xffffffffu;  // no column: a vocabulary has fewer than 2^31
 
@@ -55,12 +55,15 @@ __device__ __forceinline__ Mass mass_warp(const Mass& a, float c) {
 // The listed columns of a row, and where they lie in its vectors.
 struct Listed {
     int32_t id[kDistillMaxTop];
-    uint32_t filter[kFilterBits / 32];
+    uint32_t filter[kFilterBatches / 8][kLpThreads];
     uint32_t key[kTable];    // first column of a vector with listed columns
     uint32_t mask[kTable];   // which of its columns are
 };
-template <int DT> __device__ __forceinline__ uint32_t filter_bit(uint32_t col) {
-    return (col / Pack16<DT>::L) & (kFilterBits - 1);  // neighbouring vectors have neighbouring bits, whatever their phase
+// Batches of vectors: a CTA's threads take kLpUnroll vectors each at a time. The first of a shard has this number, modulo
+// kFilterBatches, whose vectors have four bits of a thread's words.
+static_assert(kLpUnroll == 4, "eight batches to a word");
+template <int DT> __device__ __forceinline__ uint32_t first_batch(const DistillArgs& a, uint32_t rank) {
+    return rank * (uint32_t(a.m) / (Pack16<DT>::L * kLpThreads * kLpUnroll) + 1);
 }
 // A column's first place among the table's.
 __device__ __forceinline__ uint32_t table_at(uint32_t col) { return (col * 2654435761u) >> 23; }
@@ -102,7 +105,8 @@ __device__ __forceinline__ uint32_t enter(Listed& s, uint32_t col, bool* there =
 
 // Enters the listed columns among [v0, v1). CTA-collective; id is set.
 template <int DT> __device__ __forceinline__ void list_columns(const DistillArgs& a, size_t row, uint32_t v0, uint32_t v1, Listed& s) {
-    for (int i = threadIdx.x; i < kFilterBits / 32; i += kLpThreads) s.filter[i] = 0u;
+#pragma unroll
+    for (uint32_t i = 0; i < kFilterBatches / 8; ++i) s.filter[i][threadIdx.x] = 0u;
     for (int i = threadIdx.x; i < kTable; i += kLpThreads) {
         s.key[i] = kEmpty;
         s.mask[i] = 0u;
@@ -115,8 +119,12 @@ template <int DT> __device__ __forceinline__ void list_columns(const DistillArgs
         const uint32_t k = id - first;
         constexpr int L = Piece<DT>::L;
         // a score outside of the whole vectors stands for itself
-        const uint32_t l = k >= pc.head && k < pc.head + pc.vecs * L ? (k - pc.head) % L : 0u, col = id - l;
-        atomicOr(&s.filter[filter_bit<DT>(col) / 32], 1u << (filter_bit<DT>(col) % 32));
+        const bool vector = k >= pc.head && k < pc.head + pc.vecs * L;
+        const uint32_t l = vector ? (k - pc.head) % L : 0u, col = id - l;
+        if (vector) {
+            const uint32_t i = (k - pc.head) / L, batch = first_batch<DT>(a, id / m) + i / (kLpThreads * kLpUnroll);
+            atomicOr(&s.filter[batch / 8 % (kFilterBatches / 8)][i % kLpThreads], 1u << (batch % 8 * 4 + i / kLpThreads % kLpUnroll));
+        }
         atomicOr(&s.mask[enter(s, col)], 1u << l);
     }
     __syncthreads();
@@ -140,6 +148,8 @@ __device__ __forceinline__ Mass sum_columns(const DistillArgs& a, size_t row, ui
     float m = -FLT_MAX;
     unsigned long long s = 0ull;
     const unsigned long long cc = pack2(c, c), zero = 0ull;
+    static_assert(kFilterBatches == 16, "two words");
+    const uint32_t filter0 = REST ? list.filter[0][threadIdx.x] : 0u, filter1 = REST ? list.filter[1][threadIdx.x] : 0u;
     auto raise = [&](float top) {
         if (!(top <= m)) {  // larger, or NaN
             const float f = ex2((m - top) * c);
@@ -163,20 +173,20 @@ __device__ __forceinline__ Mass sum_columns(const DistillArgs& a, size_t row, ui
         if (threadIdx.x < pc.head + pc.tail) {  // scores before and behind the whole vectors
             const uint32_t at = pc.end_at(threadIdx.x);
             float x = load_elem<DT>(pc.base, at);
-            if constexpr (REST) {
-                const uint32_t bit = filter_bit<DT>(v + at);
-                if ((list.filter[bit / 32] >> (bit % 32)) & 1u && listed_in(list, v + at)) x = -INFINITY;
-            }
+            if constexpr (REST)
+                if (listed_in(list, v + at)) x = -INFINITY;
             raise(x);
             s = add2(s, pack2(ex2((x - m) * c), 0.0f));
         }
-        for (uint32_t i0 = 0; i0 < pc.vecs; i0 += kLpThreads * kLpUnroll) {
+        uint32_t batch = REST ? first_batch<DT>(a, v / uint32_t(a.m)) : 0u;
+        for (uint32_t i0 = 0; i0 < pc.vecs; i0 += kLpThreads * kLpUnroll, ++batch) {
             if (i0 > 0 || v != v0) load_batch<DT>(pc, i0, raw);
             if constexpr (REST) {
+                const uint32_t hit = ((batch & 8 ? filter1 : filter0) >> (batch % 8 * 4)) & 15u;
+                if (hit) {
 #pragma unroll
-                for (int q = 0; q < kLpUnroll; ++q) {
-                    const uint32_t col = v + pc.head + (i0 + q * kLpThreads + threadIdx.x) * L, bit = filter_bit<DT>(col);
-                    if ((list.filter[bit / 32] >> (bit % 32)) & 1u) leave_out<DT>(raw[q], listed_in(list, col));
+                    for (int q = 0; q < kLpUnroll; ++q)
+                        if ((hit >> q) & 1u) leave_out<DT>(raw[q], listed_in(list, v + pc.head + (i0 + q * kLpThreads + threadIdx.x) * L));
                 }
             }
             float top = vector_top<DT>(raw[0]);
