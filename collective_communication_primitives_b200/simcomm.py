@@ -414,6 +414,12 @@ class SimComm:
 
     def _one(self, what, t, dtype, shape):
         """The address of a single tensor that all ranks read, checked as by _tensors (None stays None)."""
+        if t is None:
+            return None
+        if _marshal:
+            got = _marshal.address(t, dtype, shape, self._device)
+            if got is not None:
+                return got
         return self._tensors(what, t, dtype, shape, one=True)
 
     def _launch_stream(self, stream):
@@ -636,24 +642,21 @@ class SimComm:
             raise ValueError("bias_start, bias_token and bias_value go together")
         if mask is None and mask_row is not None:
             raise ValueError("mask_row needs mask")
-        u = LogitRules()
+        one = self._one
+        length = n = words = masks = 0
         if history is not None:
-            u.ld_history = history.shape[1]
-            u.history = self._one("history", history, i, (R, history.shape[1]))
-            u.history_len = self._one("history_len", history_len, i, (R,))
-            u.prompt_len = self._one("prompt_len", prompt_len, i, (R,))
-            u.repetition = self._one("repetition", repetition, f, (R,))
-            u.frequency = self._one("frequency", frequency, f, (R,))
-            u.presence = self._one("presence", presence, f, (R,))
+            length = history.shape[1]
         if bias_start is not None:
-            u.bias_count = n = bias_token.shape[0]
-            u.bias_start = self._one("bias_start", bias_start, i, (R + 1,))
-            u.bias_token = self._one("bias_token", bias_token, i, (n,))
-            u.bias_value = self._one("bias_value", bias_value, f, (n,))
+            n = bias_token.shape[0]
         if mask is not None:
-            u.mask_rows, u.ld_mask = mask.shape
-            u.mask = self._one("mask", mask, i, mask.shape)
-            u.mask_row = self._one("mask_row", mask_row, i, (R,))
+            masks, words = mask.shape
+        rows = (R,)
+        u = LogitRules(
+            one("history", history, i, (R, length)), length, one("history_len", history_len, i, rows),
+            one("prompt_len", prompt_len, i, rows), one("repetition", repetition, f, rows), one("frequency", frequency, f, rows),
+            one("presence", presence, f, rows), one("bias_start", bias_start, i, (R + 1,)),
+            one("bias_token", bias_token, i, (n,)), one("bias_value", bias_value, f, (n,)), n,
+            one("mask", mask, i, (masks, words)), words, masks, one("mask_row", mask_row, i, rows))
         self._check(self._L.coll_adjust_logits(
             self._h, self._tensors("logits", logits, x.dtype, (R, m), row=(ld, m)), ld, R, int(vocab),
             DTYPES[_dtype_of(x)], ctypes.byref(u), self._tensors("out", out, x.dtype, (R, m), row=(ld_out, m)), ld_out,
