@@ -11,8 +11,9 @@
 // are neighbours (both operands alike, so the sum is the same), which makes them 16-byte (down) and 8-byte (up) loads
 // without shared memory, and the rows of B so that a lane's four results of a token are neighbours.
 //
-// u is fp32, its parts over k joined in order by the second kernel, which splits it into two bf16 parts (what is lost is
-// 2^-16 of it or less) since B u would otherwise carry a rounding of 2^-9. The second kernel starts while the first ends and
+// u is fp32, its parts over k joined in order by the second kernel, which splits it into bf16 numbers that add up to it, since B u
+// would otherwise carry a rounding of 2^-9: two where out is bf16 (what is lost is 2^-16 of it or less), three where it is fp32 (2^-24).
+// The second kernel starts while the first ends and
 // waits for it only where it needs u. Bound by the bytes of the tokens, outputs and met adapters; in a decode step by the
 // latency of loads that wait for each other (a token's adapter, its matrices, u, the base). Measured on B200, replayed in a
 // graph: 32 tokens of 64 adapters of rank 16, row-parallel over 8 ranks, 14 us (13 MB, 0.9 TB/s); 4099 tokens of 8
@@ -350,7 +351,8 @@ template <bool BF16, bool FAST> __device__ __forceinline__ void store_eight(void
 
 constexpr int kAdCols = 32;      // columns of a warp's tile: four 8-column operands
 constexpr int kAdSteps = 4;      // steps of j whose loads are in flight
-template <int MT> constexpr int up_smem(int Rp) { return 2 * Rp / 16 * MT * 32 * 16; }
+constexpr int up_parts(bool out_bf16) { return out_bf16 ? 2 : 3; }
+template <int MT> constexpr int up_smem(int Rp, bool out_bf16) { return up_parts(out_bf16) * (Rp / 16) * MT * 32 * 16; }
 
 // Tokens are the 16 rows of an operand here, B's rows its 8 columns: an operand of B is then two neighbouring words of a row, and
 // as the columns are dealt a lane has eight neighbouring results of a token, one or two 16-byte accesses of the base and of the
@@ -361,8 +363,8 @@ template <int MT> constexpr int up_smem(int Rp) { return 2 * Rp / 16 * MT * 32 *
 // FAST: runs of eight columns of base and output are aligned and whole.
 template <int MT, int S, bool FAST, bool BASE_BF16, bool OUT_BF16> __global__ void __launch_bounds__(kAdThreads, 2)
 k_adapter_up(const __grid_constant__ AdapterArgs a, int slots, int chunks, int tiles, int per_rank) {
-    constexpr int kGroup = 16 * MT;
-    extern __shared__ __align__(128) uint4 s_u[];  // [2][steps][MT][32]: what rounding to bf16 leaves, then what it leaves out
+    constexpr int kGroup = 16 * MT, kParts = up_parts(OUT_BF16);
+    extern __shared__ __align__(128) uint4 s_u[];  // [kParts][steps][MT][32]: what rounding to bf16 leaves, then what it leaves out, ..
     const bool failed = status_failed(a.ctl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t N = uint32_t(a.N);
@@ -482,21 +484,20 @@ k_adapter_up(const __grid_constant__ AdapterArgs a, int slots, int chunks, int t
                         v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
                     }
                 }
-                float y[4], left[4];
+                float y[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    y[q] = j + q < R ? v[q] * scale : 0.0f;  // behind R nothing was written
-                    // an infinity or NaN is in the first part
-                    left[q] = fabsf(y[q]) < 3e38f ? y[q] - bf16_bits_to_float(float_to_bf16_bits(y[q])) : 0.0f;
-                }
+                for (int q = 0; q < 4; ++q) y[q] = j + q < R ? v[q] * scale : 0.0f;  // behind R nothing was written
                 // step and lane that have these j's; words 0 and 2 are the first eight tokens', 1 and 3 the second's
                 const int in = j % (16 * S), step = j / (16 * S) * S + in % (4 * S) / 4;
                 uint32_t* to = reinterpret_cast<uint32_t*>(s_u + (step * MT + t / 16) * 32 + 4 * (t % 8) + in / (4 * S)) + t % 16 / 8;
-                uint32_t* rest = to + steps * MT * 32 * 4;
-                to[0] = bf16_pair(y[0], y[1]);
-                to[2] = bf16_pair(y[2], y[3]);
-                rest[0] = bf16_pair(left[0], left[1]);
-                rest[2] = bf16_pair(left[2], left[3]);
+#pragma unroll
+                for (int h = 0; h < kParts; ++h, to += steps * MT * 32 * 4) {
+                    to[0] = bf16_pair(y[0], y[1]);
+                    to[2] = bf16_pair(y[2], y[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)  // an infinity or NaN is in the first part
+                        y[q] = fabsf(y[q]) < 3e38f ? y[q] - bf16_bits_to_float(float_to_bf16_bits(y[q])) : 0.0f;
+                }
             }
         }
         __syncthreads();
@@ -512,18 +513,19 @@ k_adapter_up(const __grid_constant__ AdapterArgs a, int slots, int chunks, int t
                 for (int m = 0; m < MT; ++m) acc[i][m][0] = acc[i][m][1] = acc[i][m][2] = acc[i][m][3] = 0.0f;
             for (int s0 = 0; s0 < steps; s0 += kAdSteps) {
                 if (s0 > 0) fetch_rows(out0, n0, s0);
+                // small parts first: an addition of the matrix instruction cuts what is beyond the sum's last bits
 #pragma unroll
-                for (int s = 0; s < kAdSteps; ++s) {
-                    if (s0 + s >= steps) break;
+                for (int h = kParts - 1; h >= 0; --h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int s = 0; s < kAdSteps; ++s) {
+                        if (s0 + s >= steps) break;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             const uint4 u = s_u[((h * steps + s0 + s) * MT + m) * 32 + lane];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) mma_bf16(acc[i][m], u.x, u.y, u.z, u.w, w[s][i].x, w[s][i].y);
                         }
-                }
+                    }
             }
             if (more) fetch_rows(next_out, next_n, 0);
             if (!spread) {
@@ -582,12 +584,15 @@ static int group_slots(size_t tokens) { return tokens <= 512 ? 8 * group_tiles(t
 
 // Parts of the sum over k: as many as give the first kernel a CTA to an SM (two of the form with stages), each of at least 8
 // steps or 2 stages; the second kernel waits for all parts (32 tokens of 64 adapters, k 4096, us with 4, 5, 10 and 16 parts: 16.8,
-// 17.7, 20.7, 22.3). They depend on the call's sizes alone, so that a token's sums do not depend on the others' adapters.
+// 17.7, 20.7, 22.3). At least one for 4096 k's: an addition of the matrix instruction cuts what is beyond the sum's last bits,
+// always to the same side, and a warp's chain of 64 of them (8192 k's) was off by 1e-6, one of 32 by half of that.
+// The parts depend on the call's sizes alone, so that a token's sums do not depend on the others' adapters.
 int adapter_splits(const AdapterArgs& a, int num_sms) {
     const size_t per = 8 * group_tiles(a.T), groups = (a.T + per - 1) / per, units = a.T <= 512 ? a.T : groups;
     const bool staged = a.x_vec && group_tiles(a.T) > 1;
     const size_t work = staged ? (a.K + kTileK - 1) / kTileK * a.segments / 2 : (a.K + kAdChunk - 1) / kAdChunk * a.segments / 8;
-    return int(std::max<size_t>(1, std::min({size_t(num_sms) * (staged ? 2 : 1) / units, work, size_t(16)})));
+    const size_t least = (a.K * a.segments + 4095) / 4096;
+    return int(std::max<size_t>(1, std::min({std::max(size_t(num_sms) * (staged ? 2 : 1) / units, least), work, size_t(16)})));
 }
 
 template <int NT, int MT> static cudaError_t go_down(const AdapterArgs& a, unsigned ctas, int slots, cudaStream_t s) {
@@ -627,11 +632,17 @@ template <int MT> static cudaError_t go_up(const AdapterArgs& a, int num_sms, cu
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(ctas));
     cfg.blockDim = dim3(kAdThreads);
-    cfg.dynamicSmemBytes = size_t(up_smem<MT>(a.Rp));  // 32 KiB at most
+    cfg.dynamicSmemBytes = size_t(up_smem<MT>(a.Rp, a.out_bf16));  // 48 KiB at most
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    auto go = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, a, int(slots), int(chunks), int(tiles), int(per_rank)); };
+    auto go = [&](auto kernel) {
+        if (cfg.dynamicSmemBytes > 47 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(cfg.dynamicSmemBytes));
+            if (e != cudaSuccess) return e;
+        }
+        return cudaLaunchKernelEx(&cfg, kernel, a, int(slots), int(chunks), int(tiles), int(per_rank));
+    };
     auto types = [&](auto at_once, auto aligned) {
         constexpr int S = decltype(at_once)::value;
         constexpr bool F = decltype(aligned)::value;
