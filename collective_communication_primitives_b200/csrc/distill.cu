@@ -273,6 +273,11 @@ template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, DT ==
         all = s_mass[0];
     }
     const Mass rest = all;  // with TAIL of the columns that are not listed
+    // The loss is a small difference of terms of the size of ln V: they are formed and added in 64 bits (in 32 the losses of 16
+    // rows of 131072 were off by 3e-6 of their size), a few operations to a place. The listed columns' part of the sum too: with
+    // it the error of the rest's sum, 1e-7 of it, enters the loss times the difference of P_rest and Q only.
+    const double inv_t = a.inv_temperature;
+    double total = all.s;
     if constexpr (TAIL) {
         // a column's first place counts. Whether any column has two is seen in a table of all of them
         for (int i = t; i < kTable; i += kLpThreads) s_list.key[i] = kEmpty;
@@ -281,14 +286,12 @@ template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, DT ==
         if (given) enter(s_list, uint32_t(id), &twice);
         if (__syncthreads_or(twice))
             for (int j = 0; j < t && j < a.n && first; ++j) first = s_list.id[j] != id;
-        Mass mine{cta_max(first ? max_nan(x, -FLT_MAX) : -FLT_MAX, s_w), 0.0f};
-        mine.s = cta_sum(first ? ex2((x - mine.m) * c) : 0.0f, s_w);
-        all = mass_join(rest, mine, c);
+        all.m = max_nan(rest.m, cta_max(first ? max_nan(x, -FLT_MAX) : -FLT_MAX, s_w));
+        total = double(rest.s) * exp((double(rest.m) - double(all.m)) * inv_t) +
+                cta_sum(first ? exp((double(x) - double(all.m)) * inv_t) : 0.0, s_d);
     }
-    // The loss is a small difference of terms of the size of ln V: they are formed and added in 64 bits (in 32 the losses of 16
-    // rows of 131072 were off by 3e-6 of their size), a few operations to a place.
-    const bool none = all.s == 0.0f;  // nothing but -inf
-    const double ln_s = none ? 0.0 : log(double(all.s)), inv_t = a.inv_temperature;
+    const bool none = total == 0.0;  // nothing but -inf
+    const double ln_s = none ? 0.0 : log(total);
     const double lp = none ? -double(INFINITY) : (double(x) - double(all.m)) * inv_t - ln_s;
     float top = 0.0f;
     double inv_z = 1.0, q, lq;
