@@ -18,9 +18,9 @@
 // Gradient: off the list dx = 2^((x - m) c - l) k with three constants of the row; with the class of the rest m and l are
 // those of the rest and k = g / T (A P_rest - Q), which stays finite where P_rest vanishes. Then the CTA writes the listed columns
 // among its own over it. Both are bound by the scores' bytes, the forward pass for 2-byte scores by instructions: one exponential
-// each and its sum (75% of the issue slots used, 4.3 TB/s). Measured on B200, us forward and gradient: 2048 x 131072 bf16, 32
-// places and the rest, 125 and 183 (537 MB, 4.3 TB/s, and 1074 MB, 5.9); 1023 x 50257 fp32, 20 places, 47 and 65 (4.4 and 6.4);
-// 16 x 131072 fp32, 12 and 8.
+// each and its sum. Measured on B200, us forward and gradient: 2048 x 131072 bf16, 32 places and the rest, 118 and 186 (537 MB,
+// 4.5 TB/s, and 1074 MB, 5.8; with a filter looked up for every vector the forward pass took 125, 75% of the issue slots
+// used); 1023 x 50257 fp32, 20 places, 48 and 65 (4.3 and 6.3); 16 x 131072 fp32, 11 and 9.
 #include <algorithm>
 #include <cfloat>
 
