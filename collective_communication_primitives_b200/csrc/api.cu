@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "rules.h"
 #include "simcomm.h"
 
 using namespace simcomm;
@@ -2411,10 +2412,10 @@ static coll_status_t coll_adjust_logits_impl(sim_comm_t c, const void* const* lo
     if (!rules || !out) return fail(COLL_ERR_INVALID_ARG, "null rules or buffer array");
     if (ld_out < m) return fail(COLL_ERR_INVALID_ARG, "ld_out is less than the shard's columns, ceil(vocab / p)");
     if ((st = check_count(ld_out, "ld_out")) != COLL_OK || (st = check_rows(rows, ld_out, "rows")) != COLL_OK) return st;
-    const coll_logit_rules_t& u = *rules;
+    const coll_logit_rules_t u = rules_in_use(*rules);
     // a column's count has 30 bits of its word
-    if (u.history_len && u.ld_history >= (size_t(1) << 30)) return fail(COLL_ERR_INVALID_ARG, "ld_history must be below 2^30");
-    if (u.bias_start && u.bias_count > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "bias_count must fit in int32");
+    if (u.ld_history >= (size_t(1) << 30)) return fail(COLL_ERR_INVALID_ARG, "ld_history must be below 2^30");
+    if (u.bias_count > size_t(INT32_MAX)) return fail(COLL_ERR_INVALID_ARG, "bias_count must fit in int32");
     if (u.mask) {
         if (u.ld_mask < (vocab + 31) / 32) return fail(COLL_ERR_INVALID_ARG, "ld_mask is less than ceil(vocab / 32)");
         if ((st = check_count(u.ld_mask, "ld_mask")) != COLL_OK || (st = check_count(u.mask_rows, "mask_rows")) != COLL_OK ||
@@ -2422,7 +2423,7 @@ static coll_status_t coll_adjust_logits_impl(sim_comm_t c, const void* const* lo
             return st;
         if (!u.mask_row && u.mask_rows < rows) return fail(COLL_ERR_INVALID_ARG, "fewer rows of masks than of scores");
     }
-    if ((st = check_rows(rows, u.history_len ? u.ld_history : 0, "rows")) != COLL_OK) return st;
+    if ((st = check_rows(rows, u.ld_history, "rows")) != COLL_OK) return st;
     if (rows == 0) return COLL_OK;
     Spans sp;
     AdjustArgs a{};

@@ -610,7 +610,7 @@ coll_status_t coll_adapters(sim_comm_t comm, const void* const* x, const int32_t
 /* ---- penalties, biases and masks on sharded scores --------------------------------------------- */
 
 /* What changes a row's scores before a token is picked. All arrays are DEVICE arrays, the one copy that all ranks read;
- * a NULL one (and a NULL history_len, bias_start or mask) leaves its rule out.
+ * a NULL one (and a NULL history_len, bias_start or mask) leaves its rule out, whose other arrays are then not looked at.
  *   history      int32 [rows][ld_history] the tokens of row t's request so far, history_len[t] of them (int32, in [0,
  *                ld_history]); the first prompt_len[t] (in [0, history_len[t]]; NULL: 0) are its prompt. -1: no token.
  *   repetition   fp32 [rows]: a score x of a token that occurs becomes x / repetition where x > 0, else x * repetition.
