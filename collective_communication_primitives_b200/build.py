@@ -1,5 +1,6 @@
 """Build the CUDA library ``libsimcomm.so`` (sm_100a) in the package directory with nvcc, and the binding's helper
-``_marshal.so`` (the checks of a call's tensors) with g++.
+``_marshal.so`` (the checks of a call's tensors) with g++. The library needs neither Python nor torch; where the helper cannot be
+built that is said, and the binding does without it.
 
     python -m collective_communication_primitives_b200.build [--force] [-v]
 
@@ -100,11 +101,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
         helper = ex.submit(build_marshal, verbose) if force or _newer(MARSHAL, [MARSHAL_SRC]) else None
         objs = list(ex.map(compile_one, sources()))
-        if helper is not None:
-            helper.result()
-    if force or _newer(LIB, objs):
-        subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
-        os.replace(LIB + ".tmp", LIB)
+        if force or _newer(LIB, objs):
+            subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
+            os.replace(LIB + ".tmp", LIB)
+        try:
+            if helper is not None:
+                helper.result()
+        except (ImportError, OSError, subprocess.CalledProcessError) as e:  # no torch, no g++, no headers
+            print(f"{os.path.basename(MARSHAL)} was not built, the binding looks at tensors in Python: {e}", file=sys.stderr)
     return LIB
 
 
