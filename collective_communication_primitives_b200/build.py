@@ -1,5 +1,5 @@
 """Build the CUDA library ``libsimcomm.so`` (sm_100a) in the package directory with nvcc, and the binding's helper
-``_marshal.so`` (the checks of a call's tensors) with g++. The library needs neither Python nor torch; where the helper cannot be
+``_marshal`` (the checks of a call's tensors; its file's name says which Python and torch it is for) with g++. The library needs neither Python nor torch; where the helper cannot be
 built that is said, and the binding does without it.
 
     python -m collective_communication_primitives_b200.build [--force] [-v]
@@ -19,7 +19,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsimcomm.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 MARSHAL_SRC = os.path.join(CSRC, "marshal.cpp")
 OBJ_DIR = os.path.join(ROOT, "_build", "simcomm")
 
@@ -59,8 +58,26 @@ def _newer(target, deps):
     return any(os.path.getmtime(f) > t for f in deps)
 
 
+def marshal_path():
+    """The helper's file. It reads tensors where this interpreter's torch holds them, so the name has what that depends on: a
+    helper of another Python or torch is another file, which is neither loaded nor taken for this one. Raises ImportError
+    without torch."""
+    import sysconfig
+
+    import torch
+    for_ = f"{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}-abi{int(torch.compiled_with_cxx11_abi())}"
+    return os.path.join(PKG, f"_marshal.{for_}.so")
+
+
+def _marshal_stale():
+    try:
+        return _newer(marshal_path(), [MARSHAL_SRC])
+    except ImportError:
+        return False  # nothing to build it for
+
+
 def _stale():
-    return _newer(LIB, sources() + _headers()) or _newer(MARSHAL, [MARSHAL_SRC])
+    return _newer(LIB, sources() + _headers()) or _marshal_stale()
 
 
 def build_marshal(verbose: bool = False):
@@ -68,17 +85,18 @@ def build_marshal(verbose: bool = False):
     import sysconfig
 
     import torch
+    path = marshal_path()
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_path("include"), os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")]
     cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     for d in inc:
         cmd += ["-isystem", d]
-    cmd += ["-o", MARSHAL + ".tmp", MARSHAL_SRC, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    cmd += ["-o", path + ".tmp", MARSHAL_SRC, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
+    os.replace(path + ".tmp", path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -99,7 +117,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
-        helper = ex.submit(build_marshal, verbose) if force or _newer(MARSHAL, [MARSHAL_SRC]) else None
+        helper = ex.submit(build_marshal, verbose) if force or _marshal_stale() else None
         objs = list(ex.map(compile_one, sources()))
         if force or _newer(LIB, objs):
             subprocess.run([nvcc, *ARCH, "-shared", "-o", LIB + ".tmp", *objs], check=True)
@@ -108,7 +126,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if helper is not None:
                 helper.result()
         except (ImportError, OSError, subprocess.CalledProcessError) as e:  # no torch, no g++, no headers
-            print(f"{os.path.basename(MARSHAL)} was not built, the binding looks at tensors in Python: {e}", file=sys.stderr)
+            print("the helper _marshal was not built, the binding looks at tensors in Python:", e, file=sys.stderr)
     return LIB
 
 

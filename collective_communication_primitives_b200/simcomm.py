@@ -28,13 +28,21 @@ _marshal = None  # the helper that looks at a call's tensors (csrc/marshal.cpp);
 
 
 def _load_marshal():
+    """Only the helper that was built for this very Python and torch: of another one every address would be wrong."""
     global _marshal
-    import torch  # noqa: F401  (the helper uses its libraries)
+    from importlib import util
+
+    from .build import marshal_path
+    _marshal = False
     try:
-        from . import _marshal as helper
-        _marshal = helper
+        path = marshal_path()
+        if os.path.exists(path):
+            spec = util.spec_from_file_location(__package__ + "._marshal", path)
+            helper = util.module_from_spec(spec)
+            spec.loader.exec_module(helper)
+            _marshal = helper
     except ImportError:
-        _marshal = False
+        pass
     return _marshal
 
 

@@ -21,7 +21,7 @@ def tools(monkeypatch, tmp_path):
             f.write(cmd[0])
 
     monkeypatch.setattr(B.subprocess, "run", run)
-    for name, path in (("LIB", "lib.so"), ("MARSHAL", "helper.so"), ("OBJ_DIR", "objects")):
+    for name, path in (("LIB", "lib.so"), ("OBJ_DIR", "objects"), ("PKG", "")):
         monkeypatch.setattr(B, name, str(tmp_path / path))
     return ran, how
 
@@ -31,11 +31,11 @@ def test_without_a_compiler_or_headers(tools, fails, capsys):
     ran, how = tools
     how["fails"] = fails
     assert B.build() == B.LIB
-    assert os.path.exists(B.LIB) and not os.path.exists(B.MARSHAL)
+    assert os.path.exists(B.LIB) and not os.path.exists(B.marshal_path())
     assert "not built" in capsys.readouterr().err
     n = len(ran)
     del how["fails"]
-    assert B.build() == B.LIB and os.path.exists(B.MARSHAL)  # it is made up for
+    assert B.build() == B.LIB and os.path.exists(B.marshal_path())  # it is made up for
     assert ran[n:] == ["g++"]
 
 
