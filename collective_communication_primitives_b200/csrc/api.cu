@@ -2499,7 +2499,8 @@ static coll_status_t distill_common(sim_comm* c, const void* const* logits, size
     a.view_rank = c->rank;
     a.n = top_n;
     a.tail = tail ? 1 : 0;
-    a.inv_temperature = 1.0f / temperature;
+    a.inv_temperature = 1.0 / double(temperature);
+    a.log2e_over = float(1.4426950408889634 / double(temperature));
     a.rows = rows;
     a.V = vocab;
     a.m = m;

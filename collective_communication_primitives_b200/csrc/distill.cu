@@ -217,7 +217,7 @@ template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, DT ==
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = threadIdx.x;
     const size_t row = blockIdx.x / a.parts;
     const int part = int(blockIdx.x % a.parts);
-    const float c = kLpLog2e * a.inv_temperature;
+    const float c = a.log2e_over;
     const uint32_t v0 = uint32_t(a.V * part / a.parts), v1 = uint32_t(a.V * (part + 1) / a.parts);
     uint4 raw[kLpUnroll];  // on their way while the list is put together
     load_batch<DT>(Piece<DT>(a, row, v0, v1), 0, raw);
@@ -389,7 +389,7 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
     fetch(0);  // on their way while the row's numbers are read
     const float* st = a.stats_in[r] + row * kDistillStats;
     if (t == 0) s_flag = status_failed(a.ctl);
-    const float c = kLpLog2e * a.inv_temperature, g = a.grad_loss[row] * a.inv_temperature, weight = st[5];
+    const float c = a.log2e_over, g = float(a.grad_loss[row] * a.inv_temperature), weight = st[5];
     const RowSlope slope{st[0], st[1], st[2] * g};
     int32_t id = -1;
     if (t < a.n) {
@@ -399,7 +399,7 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
             id = -1;
         }
         s_id[t] = id;
-        s_q[t] = id < 0 ? 0.0f : expf((a.top_value[row * a.n + t] - st[6]) * a.inv_temperature) * st[7];
+        s_q[t] = id < 0 ? 0.0f : expf(float((a.top_value[row * a.n + t] - st[6]) * a.inv_temperature)) * st[7];
     }
     __syncthreads();
     if (s_flag) return;
@@ -450,7 +450,7 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
     }
     __syncthreads();
     if (!mine) return;
-    const float p = expf((mine_x - st[3]) * a.inv_temperature - st[4]);
+    const float p = expf(float((mine_x - st[3]) * a.inv_temperature) - st[4]);
     store_elem<DT>(out, at, g * (weight * p - mine_q));
 }
 

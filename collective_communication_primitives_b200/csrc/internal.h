@@ -416,7 +416,8 @@ struct DistillArgs {
     const float* grad_loss;              // gradient: [rows]
     int p, view_rank, n, tail;
     int parts;                           // CTAs per row
-    float inv_temperature;
+    double inv_temperature;              // for rows and places
+    float log2e_over;                    // log2(e) / temperature, rounded once: for the columns
     size_t rows, V, m, ld, ld_grad;
     float2* part_stat;                   // scratch: [rows][parts] maximum and sum
     DevState* st;
