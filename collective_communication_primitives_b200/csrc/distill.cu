@@ -15,8 +15,10 @@
 // Differences x - m are formed before they are scaled, so the sums are as exact for scores far from 0 as for others, and
 // a row of the type's lowest value is a row like any other. A row of nothing but -inf has P = 0.
 //
-// Gradient: off the list dx = 2^((x - m) c - l) k with three constants of the row; with the class of the rest m and l are
-// those of the rest and k = g / T (A P_rest - Q), which stays finite where P_rest vanishes. Then the CTA writes the listed columns
+// Gradient: off the list dx = 2^((x - m) c) g / T k with two constants of the row, k = A / s of the row's maximum m and sum s;
+// with the class of the rest m and s are those of the rest and k = (A P_rest - Q) / s, which stays finite where P_rest
+// vanishes. s is at least 1 and at most V, so that k neither overflows nor vanishes, and it is formed in 64 bits: with the logarithm of s,
+// subtracted from the exponent in 32, the results were off by up to 2^-20. Then the CTA writes the listed columns
 // among its own over it. Both are bound by the scores' bytes, the forward pass for 2-byte scores by instructions: one exponential
 // each and its sum. Measured on B200, us forward and gradient: 2048 x 131072 bf16, 32 places and the rest, 118 and 186 (537 MB,
 // 4.5 TB/s, and 1074 MB, 5.8; with a filter looked up for every vector the forward pass took 125, 75% of the issue slots
@@ -324,13 +326,12 @@ template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, DT ==
         const bool empty = rest.s == 0.0f;  // no column off the list has a probability
         float* o = a.stats[r] + row * kDistillStats;
         o[0] = empty ? 0.0f : rest.m;
-        o[1] = empty ? 0.0f : log2f(rest.s);
-        o[2] = empty ? 0.0f : float(k);
-        o[3] = none ? 0.0f : all.m;
-        o[4] = float(ln_s);
-        o[5] = none ? 0.0f : float(weight);
-        o[6] = top;
-        o[7] = none ? 0.0f : float(inv_z);
+        o[1] = empty ? 0.0f : float(k / double(rest.s));
+        o[2] = none ? 0.0f : all.m;
+        o[3] = none ? 0.0f : float(weight / total);  // 0: no teacher, or nothing but -inf
+        o[4] = top;
+        o[5] = none ? 0.0f : float(inv_z);
+        o[6] = o[7] = 0.0f;
     }
 }
 
@@ -338,17 +339,17 @@ template <int DT, bool TAIL> __global__ void __launch_bounds__(kLpThreads, DT ==
 
 // Sums a row's gradient refers to.
 struct RowSlope {
-    float m, l, k;
+    float m, k;
 };
 template <int DT> __device__ __forceinline__ uint4 slope_vector(const RowSlope& g, float c, const uint4& v) {
     constexpr int L = Pack16<DT>::L;
     float x[L];
     Pack16<DT>::unpack(v, x);
-    const unsigned long long mm = pack2(-g.m, -g.m), cc = pack2(c, c), ll = pack2(-g.l, -g.l), kk = pack2(g.k, g.k);
+    const unsigned long long mm = pack2(-g.m, -g.m), cc = pack2(c, c), kk = pack2(g.k, g.k);
 #pragma unroll
     for (int q = 0; q < L; q += 2) {
         float d0, d1;
-        unpack2(fma2(add2(pack2(x[q], x[q + 1]), mm), cc, ll), d0, d1);
+        unpack2(mul2(add2(pack2(x[q], x[q + 1]), mm), cc), d0, d1);
         unpack2(mul2(pack2(ex2(d0), ex2(d1)), kk), x[q], x[q + 1]);
     }
     return Pack16<DT>::pack(x);
@@ -389,8 +390,8 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
     fetch(0);  // on their way while the row's numbers are read
     const float* st = a.stats_in[r] + row * kDistillStats;
     if (t == 0) s_flag = status_failed(a.ctl);
-    const float c = a.log2e_over, g = float(a.grad_loss[row] * a.inv_temperature), weight = st[5];
-    const RowSlope slope{st[0], st[1], st[2] * g};
+    const float c = a.log2e_over, g = float(a.grad_loss[row] * a.inv_temperature), scale = st[3];
+    const RowSlope slope{st[0], st[1] * g};
     int32_t id = -1;
     if (t < a.n) {
         id = a.top_idx[row * a.n + t];
@@ -399,11 +400,11 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
             id = -1;
         }
         s_id[t] = id;
-        s_q[t] = id < 0 ? 0.0f : expf(float((a.top_value[row * a.n + t] - st[6]) * a.inv_temperature)) * st[7];
+        s_q[t] = id < 0 ? 0.0f : expf(float((a.top_value[row * a.n + t] - st[4]) * a.inv_temperature)) * st[5];
     }
     __syncthreads();
     if (s_flag) return;
-    const bool zero = weight == 0.0f;  // no teacher, or nothing but -inf
+    const bool zero = scale == 0.0f;  // no teacher, or nothing but -inf
     const size_t have = zero ? 0 : all;
     if (zero) vecs = 0;
     const size_t rest = n - head - vecs * L;
@@ -436,7 +437,7 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
     for (size_t i = t; i < head + rest; i += kLpThreads) {
         const size_t at = c0 + (i < head ? i : i + vecs * L);
         float y = 0.0f;
-        if (at < have) y = ex2(__fmaf_rn(load_elem<DT>(in, at) - slope.m, c, -slope.l)) * slope.k;
+        if (at < have) y = ex2((load_elem<DT>(in, at) - slope.m) * c) * slope.k;
         store_elem<DT>(out, at, y);
     }
     for (size_t i0 = 0; i0 < vecs; i0 += kLpThreads * kLpUnroll) {
@@ -450,8 +451,8 @@ template <int DT> __global__ void __launch_bounds__(kLpThreads, 6) k_distill_gra
     }
     __syncthreads();
     if (!mine) return;
-    const float p = expf(float((mine_x - st[3]) * a.inv_temperature) - st[4]);
-    store_elem<DT>(out, at, g * (weight * p - mine_q));
+    const float p = expf(float((mine_x - st[2]) * a.inv_temperature)) * scale;  // A P
+    store_elem<DT>(out, at, g * (p - mine_q));
 }
 
 cudaError_t launch_distill(const DistillArgs& a, int dtype, cudaStream_t s) {
