@@ -584,15 +584,16 @@ static int group_slots(size_t tokens) { return tokens <= 512 ? 8 * group_tiles(t
 
 // Parts of the sum over k: as many as give the first kernel a CTA to an SM (two of the form with stages), each of at least 8
 // steps or 2 stages; the second kernel waits for all parts (32 tokens of 64 adapters, k 4096, us with 4, 5, 10 and 16 parts: 16.8,
-// 17.7, 20.7, 22.3). At least one for 4096 k's: an addition of the matrix instruction cuts what is beyond the sum's last bits,
-// always to the same side, and a warp's chain of 64 of them (8192 k's) was off by 1e-6, one of 32 by half of that.
+// 17.7, 20.7, 22.3). At least one for 4096 k's, however many: an addition of the matrix instruction cuts what is beyond the sum's
+// last bits, always to the same side, and a warp's chain of 64 of them (8192 k's) was off by 1e-6, one of 32 by half of that (2^22 k's
+// in 16 parts by 1.5e-4). The parts' sums take at most an eighth of the tokens' memory.
 // The parts depend on the call's sizes alone, so that a token's sums do not depend on the others' adapters.
 int adapter_splits(const AdapterArgs& a, int num_sms) {
     const size_t per = 8 * group_tiles(a.T), groups = (a.T + per - 1) / per, units = a.T <= 512 ? a.T : groups;
     const bool staged = a.x_vec && group_tiles(a.T) > 1;
     const size_t work = staged ? (a.K + kTileK - 1) / kTileK * a.segments / 2 : (a.K + kAdChunk - 1) / kAdChunk * a.segments / 8;
     const size_t least = (a.K * a.segments + 4095) / 4096;
-    return int(std::max<size_t>(1, std::min({std::max(size_t(num_sms) * (staged ? 2 : 1) / units, least), work, size_t(16)})));
+    return int(std::max(least, std::min({size_t(num_sms) * (staged ? 2 : 1) / units, work, size_t(16)})));
 }
 
 template <int NT, int MT> static cudaError_t go_down(const AdapterArgs& a, unsigned ctas, int slots, cudaStream_t s) {
