@@ -30,6 +30,8 @@ namespace simcomm {
 constexpr int kAdThreads = 256;
 constexpr int kAdWarps = kAdThreads / 32;
 constexpr int kAdChunk = 32;   // k's of one step of k_adapter_down: two matrix instructions
+constexpr int kAdChain = 4096; // k's that are summed by matrix instructions alone
+constexpr int kAdParts = 16;   // parts of the sum over k at most
 
 // The group's tokens by adapter: each lane's own adapter (-1: none), the lanes with the same one, and a bit for each first of
 // them. The same for every warp.
@@ -74,7 +76,8 @@ template <bool VEC> __device__ __forceinline__ uint4 load8(const uint16_t* row, 
 
 // NT: tokens of a group in eights. MT: tiles of 16 rows of A that a warp takes at once; the warps share the steps of k, so that a
 // CTA loads tokens and rows once (with the tiles on different warps 4099 tokens at rank 64 took 66 us, the tokens loaded four times).
-template <int NT, int MT, bool VEC> __global__ void __launch_bounds__(kAdThreads, NT * MT > 4 ? 1 : 2)
+// LONG: a part has more than kAdChain k's, and the warps' sums are added to u after as many of them.
+template <int NT, int MT, bool VEC, bool LONG> __global__ void __launch_bounds__(kAdThreads, NT * MT > 4 ? 1 : 2)
 k_adapter_down(const __grid_constant__ AdapterArgs a, int slots) {
     constexpr int kAhead = 2 * MT + NT > 8 ? 2 : 4;           // steps whose loads are in flight
     constexpr int kPart = MT * NT > 8 ? 8 / MT : NT;          // eights of tokens whose sums the warps exchange at a time
@@ -99,66 +102,71 @@ k_adapter_down(const __grid_constant__ AdapterArgs a, int slots) {
         const uint32_t tokens = __shfl_sync(0xffffffffu, crews.same, slot);
         const int R = rank_of(a, adapter), tiles = (R + 15) / 16;
         for (int tile0 = 0; tile0 < tiles; tile0 += MT) {
-            float acc[MT][NT][4];
+            uint32_t b1 = 0;
+            for (uint32_t b0 = s0; b0 < s1; b0 = b1) {
+                b1 = LONG ? min(b0 + kAdChain / kAdChunk, s1) : s1;
+                float acc[MT][NT][4];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
+                for (int m = 0; m < MT; ++m) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
-            }
-            size_t at_row[MT][2];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)  // rows past the adapter's: its last one
-                    at_row[m][i] = (size_t(adapter) * a.R + min((tile0 + m) * 16 + g + 8 * i, R - 1)) * a.K;
-            for (uint32_t s = s0 + warp; s < s1; s += kAdWarps * kAhead) {
-                uint4 w[kAhead][MT][2], x[kAhead][NT];
-#pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    const uint32_t at = s + q * kAdWarps;
-                    const uint32_t seg = at < s1 && a.segments > 1 ? at / steps : 0u;
-                    const size_t k = at < s1 ? size_t(at - seg * steps) * kAdChunk + c * 8 : a.K;
-                    const uint16_t* matrix = a.a[a.rank0 + seg];
-                    const uint16_t* v = a.x[a.rank0 + seg];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            w[q][m][i] = tile0 + m < tiles ? load8<VEC>(matrix + at_row[m][i], k, a.K) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        x[q][n] = (tokens >> (8 * n + g)) & 1u ? load8<VEC>(v + (t0 + 8 * n + g) * a.K, k, a.K) : make_uint4(0, 0, 0, 0);
+                    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
                 }
-#pragma unroll
-                for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const uint4 &w0 = w[q][m][0], &w1 = w[q][m][1];
-                            mma_bf16(acc[m][n], w0.x, w1.x, w0.y, w1.y, x[q][n].x, x[q][n].y);
-                            mma_bf16(acc[m][n], w0.z, w1.z, w0.w, w1.w, x[q][n].z, x[q][n].w);
-                        }
-            }
-            // a lane's sums: row g or g + 8 of a tile, tokens 2c and 2c + 1 of eight n
-#pragma unroll
-            for (int n0 = 0; n0 < NT; n0 += kPart) {
-                if (n0 > 0 || tile0 > 0) __syncthreads();
+                size_t at_row[MT][2];
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int n = 0; n < kPart; ++n)
+                    for (int i = 0; i < 2; ++i)  // rows past the adapter's: its last one
+                        at_row[m][i] = (size_t(adapter) * a.R + min((tile0 + m) * 16 + g + 8 * i, R - 1)) * a.K;
+                for (uint32_t s = b0 + warp; s < b1; s += kAdWarps * kAhead) {
+                    uint4 w[kAhead][MT][2], x[kAhead][NT];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s_sum[warp][(8 * n + 2 * c + (i & 1)) * (16 * MT) + m * 16 + g + 8 * (i >> 1)] = acc[m][n0 + n][i];
-                __syncthreads();
-                for (int i = threadIdx.x; i < 16 * MT * 8 * kPart; i += kAdThreads) {
-                    const int row = tile0 * 16 + i % (16 * MT), t = 8 * n0 + i / (16 * MT);
-                    if (row >= R || !((tokens >> t) & 1u)) continue;
-                    float v = s_sum[0][i];
+                    for (int q = 0; q < kAhead; ++q) {
+                        const uint32_t at = s + q * kAdWarps;
+                        const uint32_t seg = at < b1 && a.segments > 1 ? at / steps : 0u;
+                        const size_t k = at < b1 ? size_t(at - seg * steps) * kAdChunk + c * 8 : a.K;
+                        const uint16_t* matrix = a.a[a.rank0 + seg];
+                        const uint16_t* v = a.x[a.rank0 + seg];
 #pragma unroll
-                    for (int d = 1; d < kAdWarps; ++d) v += s_sum[d][i];
-                    a.u[(size_t(split) * a.T + t0 + t) * a.Rp + row] = v;
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                w[q][m][i] = tile0 + m < tiles ? load8<VEC>(matrix + at_row[m][i], k, a.K) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            x[q][n] = (tokens >> (8 * n + g)) & 1u ? load8<VEC>(v + (t0 + 8 * n + g) * a.K, k, a.K) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint4 &w0 = w[q][m][0], &w1 = w[q][m][1];
+                                mma_bf16(acc[m][n], w0.x, w1.x, w0.y, w1.y, x[q][n].x, x[q][n].y);
+                                mma_bf16(acc[m][n], w0.z, w1.z, w0.w, w1.w, x[q][n].z, x[q][n].w);
+                            }
+                }
+                // a lane's sums: row g or g + 8 of a tile, tokens 2c and 2c + 1 of eight n
+#pragma unroll
+                for (int n0 = 0; n0 < NT; n0 += kPart) {
+                    if (n0 > 0 || tile0 > 0 || (LONG && b0 > s0)) __syncthreads();
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int n = 0; n < kPart; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                s_sum[warp][(8 * n + 2 * c + (i & 1)) * (16 * MT) + m * 16 + g + 8 * (i >> 1)] = acc[m][n0 + n][i];
+                    __syncthreads();
+                    for (int i = threadIdx.x; i < 16 * MT * 8 * kPart; i += kAdThreads) {
+                        const int row = tile0 * 16 + i % (16 * MT), t = 8 * n0 + i / (16 * MT);
+                        if (row >= R || !((tokens >> t) & 1u)) continue;
+                        float v = s_sum[0][i];
+#pragma unroll
+                        for (int d = 1; d < kAdWarps; ++d) v += s_sum[d][i];
+                        float* u = a.u + (size_t(split) * a.T + t0 + t) * a.Rp + row;
+                        *u = LONG && b0 > s0 ? *u + v : v;  // an element is one thread's every time
+                    }
                 }
             }
         }
@@ -179,7 +187,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t smem) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(smem) : "memory");
 }
 
-template <int MT> __global__ void __launch_bounds__(kAdThreads, 2) k_adapter_down_tiles(const __grid_constant__ AdapterArgs a, int slots) {
+template <int MT, bool LONG> __global__ void __launch_bounds__(kAdThreads, 2) k_adapter_down_tiles(const __grid_constant__ AdapterArgs a, int slots) {
     constexpr int NT = 4;
     static_assert(kAdWarps * 16 == kTileK, "a warp has 16 k's of a stage");
     static_assert(kAdWarps * 16 * MT * 8 * NT * 4 <= kTileStages * tile_bytes<MT>(), "the warps' sums lie where the stages did");
@@ -217,63 +225,68 @@ template <int MT> __global__ void __launch_bounds__(kAdThreads, 2) k_adapter_dow
                 at[i] = i < MT ? (size_t(adapter) * a.R + min((tile0 + i) * 16 + row0, R - 1)) * a.K
                                : (t0 + (some[i] ? t : 0)) * a.K;
             }
-            auto copy = [&](uint32_t s) {
-                if (s < s1) {
-                    const uint32_t seg = a.segments > 1 ? s / per : 0u;
-                    const size_t k = size_t(s - seg * per) * kTileK + piece * 8;
-                    const uint16_t* m = a.a[a.rank0 + seg];
-                    const uint16_t* x = a.x[a.rank0 + seg];
-                    const uint32_t to = base + (s % kTileStages) * tile_bytes<MT>() + row0 * kTilePitch + piece * 16;
-                    const bool in = k < a.K;
+            uint32_t b1 = 0;
+            for (uint32_t b0 = s0; b0 < s1; b0 = b1) {
+                b1 = LONG ? min(b0 + kAdChain / kTileK, s1) : s1;
+                auto copy = [&](uint32_t s) {
+                    if (s < b1) {
+                        const uint32_t seg = a.segments > 1 ? s / per : 0u;
+                        const size_t k = size_t(s - seg * per) * kTileK + piece * 8;
+                        const uint16_t* m = a.a[a.rank0 + seg];
+                        const uint16_t* x = a.x[a.rank0 + seg];
+                        const uint32_t to = base + (s % kTileStages) * tile_bytes<MT>() + row0 * kTilePitch + piece * 16;
+                        const bool in = k < a.K;
 #pragma unroll
-                    for (int i = 0; i < MT + 2; ++i)
-                        cp_async16(to + i * 16 * kTilePitch, (i < MT ? m : x) + (in ? at[i] + k : 0), in && some[i] ? 16u : 0u);
+                        for (int i = 0; i < MT + 2; ++i)
+                            cp_async16(to + i * 16 * kTilePitch, (i < MT ? m : x) + (in ? at[i] + k : 0), in && some[i] ? 16u : 0u);
+                    }
+                    cp_async_commit();
+                };
+                float acc[MT][NT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kTileStages - 1; ++q) copy(b0 + q);
+                for (uint32_t s = b0; s < b1; ++s) {
+                    asm volatile("cp.async.wait_group %0;" :: "n"(kTileStages - 2) : "memory");
+                    __syncthreads();  // the stage is in, and the one before it is used up
+                    copy(s + kTileStages - 1);
+                    const uint32_t from = base + (s % kTileStages) * tile_bytes<MT>() + warp * 32;
+                    uint32_t x[NT / 2][4];
+#pragma unroll
+                    for (int n = 0; n < NT / 2; ++n)
+                        ldmatrix4(x[n], from + (16 * MT + 16 * n + (lane >> 4) * 8 + (lane & 7)) * kTilePitch + ((lane >> 3) & 1) * 16);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        uint32_t w[4];
+                        ldmatrix4(w, from + (16 * m + (lane & 15)) * kTilePitch + (lane >> 4) * 16);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_bf16(acc[m][n], w[0], w[1], w[2], w[3], x[n / 2][2 * (n & 1)], x[n / 2][2 * (n & 1) + 1]);
+                    }
                 }
-                cp_async_commit();
-            };
-            float acc[MT][NT][4];
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncthreads();
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int q = 0; q < kTileStages - 1; ++q) copy(s0 + q);
-            for (uint32_t s = s0; s < s1; ++s) {
-                asm volatile("cp.async.wait_group %0;" :: "n"(kTileStages - 2) : "memory");
-                __syncthreads();  // the stage is in, and the one before it is used up
-                copy(s + kTileStages - 1);
-                const uint32_t from = base + (s % kTileStages) * tile_bytes<MT>() + warp * 32;
-                uint32_t x[NT / 2][4];
+                        for (int i = 0; i < 4; ++i)
+                            sums[warp * (16 * MT * 8 * NT) + (8 * n + 2 * c + (i & 1)) * (16 * MT) + m * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
+                __syncthreads();
+                for (int i = threadIdx.x; i < 16 * MT * 8 * NT; i += kAdThreads) {
+                    const int row = tile0 * 16 + i % (16 * MT), t = i / (16 * MT);
+                    if (row >= R || !((tokens >> t) & 1u)) continue;
+                    float v = sums[i];
 #pragma unroll
-                for (int n = 0; n < NT / 2; ++n)
-                    ldmatrix4(x[n], from + (16 * MT + 16 * n + (lane >> 4) * 8 + (lane & 7)) * kTilePitch + ((lane >> 3) & 1) * 16);
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint32_t w[4];
-                    ldmatrix4(w, from + (16 * m + (lane & 15)) * kTilePitch + (lane >> 4) * 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_bf16(acc[m][n], w[0], w[1], w[2], w[3], x[n / 2][2 * (n & 1)], x[n / 2][2 * (n & 1) + 1]);
+                    for (int d = 1; d < kAdWarps; ++d) v += sums[d * (16 * MT * 8 * NT) + i];
+                    float* u = a.u + (size_t(split) * a.T + t0 + t) * a.Rp + row;
+                    *u = LONG && b0 > s0 ? *u + v : v;  // an element is one thread's every time
                 }
+                __syncthreads();
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sums[warp * (16 * MT * 8 * NT) + (8 * n + 2 * c + (i & 1)) * (16 * MT) + m * 16 + g + 8 * (i >> 1)] = acc[m][n][i];
-            __syncthreads();
-            for (int i = threadIdx.x; i < 16 * MT * 8 * NT; i += kAdThreads) {
-                const int row = tile0 * 16 + i % (16 * MT), t = i / (16 * MT);
-                if (row >= R || !((tokens >> t) & 1u)) continue;
-                float v = sums[i];
-#pragma unroll
-                for (int d = 1; d < kAdWarps; ++d) v += sums[d * (16 * MT * 8 * NT) + i];
-                a.u[(size_t(split) * a.T + t0 + t) * a.Rp + row] = v;
-            }
-            __syncthreads();
         }
     }
 }
@@ -584,31 +597,32 @@ static int group_slots(size_t tokens) { return tokens <= 512 ? 8 * group_tiles(t
 
 // Parts of the sum over k: as many as give the first kernel a CTA to an SM (two of the form with stages), each of at least 8
 // steps or 2 stages; the second kernel waits for all parts (32 tokens of 64 adapters, k 4096, us with 4, 5, 10 and 16 parts: 16.8,
-// 17.7, 20.7, 22.3). At least one for 4096 k's, however many: an addition of the matrix instruction cuts what is beyond the sum's
-// last bits, always to the same side, and a warp's chain of 64 of them (8192 k's) was off by 1e-6, one of 32 by half of that (2^22 k's
-// in 16 parts by 1.5e-4). The parts' sums take at most an eighth of the tokens' memory.
+// 17.7, 20.7, 22.3). At least one for 4096 k's, as far as they go: an addition of the matrix instruction cuts what is beyond the sum's
+// last bits, always to the same side, and a warp's chain of 64 of them (8192 k's) was off by 1e-6, one of 32 by half of that. Beyond 16 times
+// 4096 k's a part's chains end every 4096 (2^22 k's without that were off by 1.5e-4; with more parts instead, as exact, 300 tokens of 8
+// adapters of rank 16, 2^20 k's, took 613 us, with chains that end 343, without 255).
 // The parts depend on the call's sizes alone, so that a token's sums do not depend on the others' adapters.
 int adapter_splits(const AdapterArgs& a, int num_sms) {
     const size_t per = 8 * group_tiles(a.T), groups = (a.T + per - 1) / per, units = a.T <= 512 ? a.T : groups;
     const bool staged = a.x_vec && group_tiles(a.T) > 1;
     const size_t work = staged ? (a.K + kTileK - 1) / kTileK * a.segments / 2 : (a.K + kAdChunk - 1) / kAdChunk * a.segments / 8;
-    const size_t least = (a.K * a.segments + 4095) / 4096;
-    return int(std::max(least, std::min({size_t(num_sms) * (staged ? 2 : 1) / units, work, size_t(16)})));
+    const size_t least = (a.K * a.segments + kAdChain - 1) / kAdChain;
+    return int(std::max<size_t>(1, std::min({std::max(size_t(num_sms) * (staged ? 2 : 1) / units, least), work, size_t(kAdParts)})));
 }
 
-template <int NT, int MT> static cudaError_t go_down(const AdapterArgs& a, unsigned ctas, int slots, cudaStream_t s) {
+template <int NT, int MT, bool LONG> static cudaError_t go_down(const AdapterArgs& a, unsigned ctas, int slots, cudaStream_t s) {
     if constexpr (NT == 4) {
         if (a.x_vec) {
             constexpr int kSmem = kTileStages * tile_bytes<MT>();
-            cudaError_t e = cudaFuncSetAttribute(k_adapter_down_tiles<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            cudaError_t e = cudaFuncSetAttribute(k_adapter_down_tiles<MT, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             if (e != cudaSuccess) return e;
-            k_adapter_down_tiles<MT><<<ctas, kAdThreads, kSmem, s>>>(a, slots);
+            k_adapter_down_tiles<MT, LONG><<<ctas, kAdThreads, kSmem, s>>>(a, slots);
             return cudaGetLastError();
         }
-        k_adapter_down<NT, MT, false><<<ctas, kAdThreads, 0, s>>>(a, slots);
+        k_adapter_down<NT, MT, false, LONG><<<ctas, kAdThreads, 0, s>>>(a, slots);
     } else {
-        if (a.x_vec) k_adapter_down<NT, MT, true><<<ctas, kAdThreads, 0, s>>>(a, slots);
-        else k_adapter_down<NT, MT, false><<<ctas, kAdThreads, 0, s>>>(a, slots);
+        if (a.x_vec) k_adapter_down<NT, MT, true, LONG><<<ctas, kAdThreads, 0, s>>>(a, slots);
+        else k_adapter_down<NT, MT, false, LONG><<<ctas, kAdThreads, 0, s>>>(a, slots);
     }
     return cudaGetLastError();
 }
@@ -659,8 +673,13 @@ template <int NT> static cudaError_t go_adapters(const AdapterArgs& a, int num_s
     const int slots = group_slots(a.T);
     const size_t groups = (a.T + 8 * NT - 1) / (8 * NT), down = groups * slots * a.splits;
     if (down > size_t(INT32_MAX)) return cudaErrorInvalidValue;
-    cudaError_t e = a.R <= 16 ? go_down<NT, 1>(a, unsigned(down), slots, s) : a.R <= 32 ? go_down<NT, 2>(a, unsigned(down), slots, s)
-                                                                                       : go_down<NT, 4>(a, unsigned(down), slots, s);
+    auto ranks = [&](auto chains) {
+        constexpr bool LONG = decltype(chains)::value;
+        return a.R <= 16 ? go_down<NT, 1, LONG>(a, unsigned(down), slots, s) : a.R <= 32 ? go_down<NT, 2, LONG>(a, unsigned(down), slots, s)
+                                                                                       : go_down<NT, 4, LONG>(a, unsigned(down), slots, s);
+    };
+    // in the same kernels the ends of chains cost 4,099 tokens at rank 64, k 4096, 1 us of 48
+    cudaError_t e = a.K * a.segments > size_t(kAdParts) * kAdChain ? ranks(std::true_type{}) : ranks(std::false_type{});
     return e != cudaSuccess ? e : go_up<NT == 1 ? 1 : 2>(a, num_sms, s);
 }
 

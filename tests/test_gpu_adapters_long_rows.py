@@ -1,5 +1,5 @@
-"""The adapters' fp32 results where k is far beyond 65,536: a warp's chain of matrix instructions stays as short as for shorter
-rows, since the sum is cut into more parts.
+"""The adapters' fp32 results where k is far beyond 65,536: a warp's chain of matrix instructions ends as soon as for shorter
+rows, and its sums are added up.
 
 Tolerance: as for shorter rows, an addition of the matrix instruction cuts less than 2^-23 of the largest number in it,
 and the numbers are of one sign: (32 + 3 R / 16) 2^-23 for a chain over 4,096 k's of a part (8 warps, 16 k's to an instruction) and the
