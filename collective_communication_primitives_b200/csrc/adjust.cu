@@ -293,7 +293,9 @@ cudaError_t launch_adjust(const AdjustArgs& args, int dtype, int num_sms, cudaSt
     const size_t span = a.last - a.first, wanted = std::max<size_t>(1, size_t(4 * num_sms) / a.rows);
     size_t cols = std::max<size_t>(2048, (span + wanted - 1) / wanted);
     // Columns that a row can name: a hash table with twice as many places, where that is less than a word per column; the table
-    // has 8192 places at most, a CTA with a word per column 8192 columns (with biases) or 16384.
+    // has 8192 places at most, a CTA with a word per column 8192 columns (with biases) or 16384. What a row can name goes by the sizes of the
+    // arrays, not by what it does name: 256 rows of 131072 bf16 with 1024 tokens and masks, us by the width of the history's rows: up to
+    // 2048 39, 4096 61, 8192 and more 68; with 20 biases to a row (5120 in all) 94.
     const size_t names = (a.rules.history_len ? a.rules.ld_history : 0) + (bias ? a.rules.bias_count : 0);
     size_t places = 256;
     while (places < 2 * names && places < 16384) places *= 2;

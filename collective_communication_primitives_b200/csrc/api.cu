@@ -1815,11 +1815,12 @@ coll_status_t check_row(size_t len, const char* what) {
 }
 
 // CTAs per row of scores. Five run on an SM at a time; a CTA costs its columns and, in columns, `fixed` for its start and
-// end (log probabilities 4096, with alternatives 12288), and 512 for every part that the last one joins. The SM with the most
+// end (log probabilities 4096, with alternatives 12288, distillation 8192), and 512 for every part that the last one joins. The SM with the most
 // CTAs takes a fifth of that sum for each, but a CTA alone at the end as long as two (it has less to overlap with).
 // Measured on B200 with V = 131072, log probabilities, us with 1, 2, 4, 8 and 16 parts: 8 rows fp32, 8 alternatives 31, 23, 18,
 // 14, 14; 64 rows bf16, 4 alternatives 27, 21, 17, 17, 21; 300 rows 41, 37, 39, 43, 60; 700 rows without 45, 48, 50, 56,
-// 70; 2048 rows with 4 145, 171, 183, 225, 344.
+// 70; 2048 rows with 4 145, 171, 183, 225, 344. Distillation, 32 places and the rest, us with `fixed` 4096, 8192 and 12288: 150 rows fp32 26.6,
+// 22.7, 22.8, bf16 18.3, 19.3, 19.5; 300 rows 38.6, 43.5, 43.7, bf16 29.6, 27.9, 27.8; fewer and more alike.
 int row_parts(const sim_comm* c, size_t rows, size_t vocab, size_t fixed) {
     int parts = 1;
     if (rows > size_t(kLogprobMaxSplitRows)) return parts;

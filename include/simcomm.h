@@ -598,7 +598,8 @@ coll_status_t coll_rmsnorm_backward(sim_comm_t comm, const void* const* grad_out
  *   base_dtype, dtype  types of base and of out: fp32 or bf16 (int32: COLL_ERR_UNSUPPORTED).
  * max_rank in [1, 256], adapters in [1, 2^24], n divisible by p (COLUMN) or k by p (ROW), n and k at most 2^24, tokens
  * at most 2^31 - 1. Sums are fp32; A x goes into the second product in two bf16 parts (2^-16 of it is lost), where out is
- * fp32 in three (2^-24); one rounding to out's type. A token's result does not depend on the other tokens of a call of the same size. An adapter or rank out of range is
+ * fp32 in three (2^-24), so that an infinity in B may give NaN; one rounding to out's type. A token's result does not depend
+ * on the other tokens of a call of the same size. An adapter or rank out of range is
  * reported asynchronously as COLL_ERR_INVALID_ARG. Tokens of one request that follow each other share its matrices'
  * loads. No output may overlap another buffer but as said. T = 0 or n = 0 enqueues nothing. On a rank view COLUMN uses
  * this rank's entries only; ROW reads every rank's x and a as this process maps them and this rank's b, base and out. */
