@@ -72,7 +72,7 @@ def marshal_path():
 def _marshal_stale():
     try:
         return _newer(marshal_path(), [MARSHAL_SRC])
-    except ImportError:
+    except (ImportError, OSError):  # no torch, or one whose own libraries are missing
         return False  # nothing to build it for
 
 

@@ -58,3 +58,15 @@ def test_a_library_that_fails_is_an_error(tools, monkeypatch):
     monkeypatch.setattr(B.subprocess, "run", run)
     with pytest.raises(subprocess.CalledProcessError):
         B.build()
+
+
+def test_without_a_torch_that_loads(tools, monkeypatch):
+    ran, _ = tools
+
+    def path():
+        raise OSError("libcudart.so: cannot open shared object file")
+
+    monkeypatch.setattr(B, "marshal_path", path)
+    assert B.build() == B.LIB and os.path.exists(B.LIB)
+    assert "g++" not in ran
+    assert B.build(force=True) == B.LIB
